@@ -1,0 +1,855 @@
+// mla_chunk_attention: attention of a chunk of new tokens over the paged FP8 cache.
+//
+// Token i of a sequence's n new tokens, with L positions in the cache, attends the
+// positions p <= L - n + i (all of them without `causal`):
+//   s_p = sm_scale * (q . K_p), out = softmax(s) V, lse = ln sum exp s_p,
+// K_p = the row's dequantised latent and its RoPE tail, V_p = the latent.
+//
+// The query rows of a sequence are its (token, head) pairs in order, so any number of
+// heads fills tiles of consecutive rows. This file holds what the two kernels of the
+// call share (the plan of the work and the merge of split tiles) and the kernel for
+// few query rows, where reading the cache is what costs: tiles of 16 rows (one token
+// of 16 heads) on m16n8k16, the same arithmetic as the sparse decode, with q.K exact
+// before fp32 accumulation (codes as exact f16, the fp32 tile scale applied to each
+// tile's partial afterwards). Positions come in order, so a block of 32 that lies in
+// one page is a single bulk copy.
+//
+// The host knows the sizes of the arrays, not the lengths in them: a first launch of
+// one CTA reads the lengths and plans the pieces (chunk_plan_kernel), so a captured
+// graph serves any lengths. A tile is cut into pieces of about a G-th of all work (G
+// the CTAs of one wave) and at least kMinPiece positions; pieces of a cut tile write
+// normalised partials that mla_chunk_merge_kernel joins in piece order.
+#include <cfloat>
+#include <climits>
+#include <cmath>
+
+#include "mla_chunk.cuh"
+
+namespace {
+
+using namespace mla;
+using namespace mla_chunk;
+
+constexpr int kWarps = 4;                    // consumer warps (one per latent tile)
+constexpr int kProducers = 2;                // copy-issuing warps (alternate blocks)
+constexpr int kThreads = (kWarps + kProducers) * 32;
+constexpr int kConsumerThreads = kWarps * 32;
+constexpr int kNB = 32;                      // positions per block
+constexpr int kStages = 4;
+constexpr int kHeads = kSmallRows;           // query rows per CTA (M of m16n8k16)
+constexpr int kStageBytes = kNB * kRowBytes;
+constexpr int kSmemStages = kStages * kStageBytes;
+constexpr int kSmemRed = kWarps * 4 * 32 * 16;       // QK tile partials: float4 [warp][n-tile][lane]
+constexpr int kSmemP = 4 * 32 * 8;                   // P (f16): uint2 [n-tile][lane], A-fragment order
+constexpr int kSmemQmax = 3 * kWarps * kHeads * 4;   // |q| maxima, block score maxima, l partials
+constexpr int kSmemMisc = 2 * kStages * 8 + kStages * 4 + 16 + 16;   // barriers, present masks, poisoned rows, issued
+constexpr int kSmemTotal = kSmemStages + kSmemRed + kSmemP + kSmemQmax + kSmemMisc;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The running max used as the exp2 offset is only moved when a score exceeds it
+// by more than this (log2 units): p <= 2^8 keeps the f16 P operand in range.
+constexpr float kRescaleSlack = 8.0f;
+
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+// Plan of the work (one CTA): how many pieces each sequence's tiles are cut into, and
+// the prefixes by which a CTA finds its piece and the merge its rows. C, the longest
+// piece, is at least a wave-th of all positions that tiles read, so the pieces number
+// at most tiles + wave, and those of split tiles (each more than C, so cut into less
+// than 2 x its length / C) at most 2 wave: the sizes of the grid and the workspace.
+constexpr int kPlanThreads = 512;
+
+__device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* buf) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int64_t t = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) t += buf[w];
+    return t;
+}
+
+// Exclusive prefix over the CTA; total in `all`.
+__device__ __forceinline__ int plan_scan(int v, int& all, int64_t* buf) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) buf[warp] = incl;
+    __syncthreads();
+    int off = 0;
+    all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const int c = static_cast<int>(buf[w]);
+        off += w < warp ? c : 0;
+        all += c;
+    }
+    return off + incl - v;
+}
+
+// The largest value in the threads before this one (INT_MIN for the first); the CTA's in `all`.
+__device__ __forceinline__ int plan_scan_max(int v, int& all, int64_t* buf) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl = max(incl, x);
+    }
+    __syncthreads();
+    if (lane == 31) buf[warp] = incl;
+    __syncthreads();
+    int before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = INT_MIN;
+    all = INT_MIN;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const int c = static_cast<int>(buf[w]);
+        if (w < warp) before = max(before, c);
+        all = max(all, c);
+    }
+    return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+chunk_plan_kernel(const ChunkArgs a) {
+    __shared__ int64_t buf[kPlanThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    // A sequence is taken if its start is not below any earlier one, nor its end below its
+    // start or past T: so the sequences taken are disjoint, and together at most T tokens.
+    int64_t work = 0;
+    int top = 0;                                       // the largest start so far
+    for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        const int start = s < a.n_seq ? __ldg(a.q_start + s) : INT_MIN;
+        int all;
+        const int before = max(top, plan_scan_max(start, all, buf));
+        top = max(top, all);
+        if (s >= a.n_seq) continue;
+        const Seq q = load_seq(a, s);
+        const int end = __ldg(a.q_start + s + 1);
+        const bool taken = start >= before && start <= end && end <= a.T;
+        if (!taken || static_cast<int64_t>(q.len) > static_cast<int64_t>(a.max_pages) * a.page_size)
+            atomicOr(a.err, MLA_ERR_CHUNK_RANGE);
+        a.split[s] = taken ? 1 : 0;
+        const int64_t tiles = (static_cast<int64_t>(q.n) * a.H + a.tile_rows - 1) / a.tile_rows;
+        if (taken) work += tiles * mean_limit(a, q);
+    }
+    work = plan_sum(work, buf);
+    int64_t C = (work + a.wave - 1) / a.wave;
+    C = C < a.min_piece ? a.min_piece : (C + a.align - 1) / a.align * a.align;
+    int p_base = 0, q_base = 0, r_base = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        int nk = 1, pieces = 0, parts = 0, rows = 0;
+        if (s < a.n_seq && a.split[s] != 0) {
+            const Seq q = load_seq(a, s);
+            const int tiles = static_cast<int>((static_cast<int64_t>(q.n) * a.H + a.tile_rows - 1) / a.tile_rows);
+            nk = max(1, static_cast<int>((mean_limit(a, q) + C - 1) / C));
+            pieces = tiles * nk;
+            if (nk > 1) {
+                parts = pieces;
+                rows = q.n * a.H;
+            }
+        }
+        int all;
+        const int p = plan_scan(pieces, all, buf) + p_base;
+        p_base += all;
+        const int k = plan_scan(parts, all, buf) + q_base;
+        q_base += all;
+        const int r = plan_scan(rows, all, buf) + r_base;
+        r_base += all;
+        if (s < a.n_seq) {
+            a.piece0[s] = p;
+            a.part0[s] = k;
+            a.mrow0[s] = r;
+            a.split[s] = nk;
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.piece0[a.n_seq] = p_base;
+        a.part0[a.n_seq] = q_base;
+        a.mrow0[a.n_seq] = r_base;
+    }
+}
+
+// Joins the partials of the split tiles' rows in piece order: lse = ln sum exp(lse_k),
+// out = sum exp(lse_k - lse) o_k; a NaN partial makes both NaN. A CTA takes a row at a
+// time, thread x dims 4x .. 4x + 3, the loads of kMergeBatch pieces together.
+constexpr int kMergeBatch = 8;
+
+__global__ void __launch_bounds__(128)
+mla_chunk_merge_kernel(const ChunkArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int d = 4 * threadIdx.x;
+    const int total = a.mrow0[a.n_seq];
+    for (int r = blockIdx.x; r < total; r += gridDim.x) {
+        const int s = find_seq(a.mrow0, a.n_seq, r, lane);
+        const int local = r - a.mrow0[s];
+        const int np = a.split[s];
+        const int tile = local / a.tile_rows;
+        const int64_t row0 = (static_cast<int64_t>(a.part0[s]) + static_cast<int64_t>(tile) * np) * a.tile_rows +
+                             (local - tile * a.tile_rows);
+        const int64_t grow = static_cast<int64_t>(__ldg(a.q_start + s)) * a.H + local;
+        float mx = -INFINITY;
+        bool nan = false;
+        for (int s0 = 0; s0 < np; s0 += kMergeBatch) {
+            float ls[kMergeBatch];
+#pragma unroll
+            for (int q = 0; q < kMergeBatch; ++q)
+                ls[q] = (s0 + q < np) ? a.part_lse[row0 + static_cast<int64_t>(s0 + q) * a.tile_rows] : -INFINITY;
+#pragma unroll
+            for (int q = 0; q < kMergeBatch; ++q) {
+                mx = fmaxf(mx, ls[q]);
+                nan = nan || ls[q] != ls[q];
+            }
+        }
+        float wsum = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mx != -INFINITY && !nan) {
+            for (int s0 = 0; s0 < np; s0 += kMergeBatch) {
+                float ls[kMergeBatch];
+                float4 v[kMergeBatch];
+#pragma unroll
+                for (int q = 0; q < kMergeBatch; ++q) {
+                    const int64_t prow = row0 + static_cast<int64_t>(min(s0 + q, np - 1)) * a.tile_rows;
+                    ls[q] = (s0 + q < np) ? a.part_lse[prow] : -INFINITY;
+                    // A piece with nothing attended (lse -inf) left its o unwritten.
+                    v[q] = (ls[q] == -INFINITY) ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                : *reinterpret_cast<const float4*>(a.part_o + prow * kLatent + d);
+                }
+#pragma unroll
+                for (int q = 0; q < kMergeBatch; ++q) {
+                    const float w = (ls[q] == -INFINITY) ? 0.0f : expf(ls[q] - mx);
+                    wsum += w;
+                    acc.x = fmaf(w, v[q].x, acc.x);
+                    acc.y = fmaf(w, v[q].y, acc.y);
+                    acc.z = fmaf(w, v[q].z, acc.z);
+                    acc.w = fmaf(w, v[q].w, acc.w);
+                }
+            }
+        }
+        float lse = mx + logf(wsum), inv = 1.0f / wsum;
+        if (mx == -INFINITY) { lse = -INFINITY; inv = 0.0f; }
+        if (nan) lse = inv = __int_as_float(0x7FC00000);
+        *reinterpret_cast<uint2*>(a.out + grow * kLatent + d) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (threadIdx.x == 0) a.lse[grow] = lse;
+    }
+}
+
+// Whether a staged row holds a value that is not finite: a NaN code, or a tile scale
+// or RoPE value that is NaN or infinite (one warp; every lane gets it).
+__device__ __forceinline__ bool row_not_finite(const uint8_t* row, bool rope, int lane) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * lane);
+    uint32_t bad = 0;
+    bad |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u);
+    bad |= ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
+    bool b = (bad & 0x80808080u) != 0u;
+    if (lane < 4) b = b || !isfinite(*reinterpret_cast<const float*>(row + kScaleOff + 4 * lane));
+    if (rope) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + kTailOff + 4 * lane);
+        b = b || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    }
+    return __any_sync(0xffffffffu, b);
+}
+
+template <bool kRopeOn>
+__global__ void __launch_bounds__(kThreads, 2)
+mla_chunk_small_kernel(const ChunkArgs args) {
+    constexpr uint32_t kRowRead = kRopeOn ? kRowBytes : kNopeReadBytes;
+    constexpr int kStride = kRowRead;        // staged rows: 164 or 132 words apart, 4 mod 32
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* stages = smem;
+    float4* red = reinterpret_cast<float4*>(smem + kSmemStages);
+    uint32_t* pbuf = reinterpret_cast<uint32_t*>(smem + kSmemStages + kSmemRed);
+    float* qmax_s = reinterpret_cast<float*>(smem + kSmemStages + kSmemRed + kSmemP);
+    float* rmax_s = qmax_s + kWarps * kHeads;
+    float* lsum_s = rmax_s + kWarps * kHeads;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSmemStages + kSmemRed + kSmemP + kSmemQmax);
+    uint64_t* empty = full + kStages;
+    uint32_t* vmask = reinterpret_cast<uint32_t*>(empty + kStages);   // present positions of each stage
+    uint32_t* poison_s = vmask + kStages;                             // [4] bytes of 8 rows each, by warp
+    int* issued_s = reinterpret_cast<int*>(poison_s + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const Piece pc = find_piece(args, blockIdx.x, lane);
+    if (pc.seq < 0) return;
+    const int k0 = pc.k0, n_keys = pc.k1 - pc.k0;
+    const int nblk = (n_keys + kNB - 1) / kNB;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        issued_s[0] = issued_s[1] = 0;
+        fence_mbar_init();
+    }
+    if (threadIdx.x < 4) poison_s[threadIdx.x] = 0u;
+    __syncthreads();
+
+    if (warp >= kWarps) {
+        // ---- producers: warp kWarps + p copies blocks p, p + kProducers, ...; lane j
+        // finds the slot of position 32 b + j one block ahead of its copy ----
+        const int pw = warp - kWarps;
+        const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
+        int64_t slot = (pw < nblk && pw * kNB + lane < n_keys) ? chunk_slot(args, bt, k0 + pw * kNB + lane) : -1;
+        int b = pw, cnt = 0;
+        for (; b < nblk; b += kProducers, ++cnt) {
+            const int s = b % kStages;
+            const int nb = b + kProducers;
+            const int64_t next =
+                (nb < nblk && nb * kNB + lane < n_keys) ? chunk_slot(args, bt, k0 + nb * kNB + lane) : -1;
+            if (b >= kStages && !mbar_wait_bounded(&empty[s], static_cast<uint32_t>(((b / kStages) - 1) & 1))) {
+                if (lane == 0) atomicOr(args.err, MLA_ERR_PIPELINE_TIMEOUT);
+                break;
+            }
+            uint8_t* dst = stages + s * kStageBytes;
+            const bool present = slot >= 0;
+            const unsigned mask = __ballot_sync(0xffffffffu, present);
+            if (!present) {
+                // An absent position loads nothing: its row is zeros (E4M3 0, scale 0.0).
+                uint4* z = reinterpret_cast<uint4*>(dst + lane * kStride);
+                for (int k = 0; k < kStride / 16; ++k) z[k] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            const int64_t first = __shfl_sync(0xffffffffu, slot, 0);
+            // All 32 rows side by side in the cache, and nothing but rows as staged: one copy.
+            const bool run = __all_sync(0xffffffffu, present && slot == first + lane) && args.row_bytes == kRowRead;
+            if (lane == 0) {
+                vmask[s] = mask;
+                mbar_arrive_expect_tx(&full[s], __popc(mask) * kRowRead);
+            }
+            __syncwarp();
+            if (run) {
+                if (lane == 0) bulk_g2s(dst, args.cache + first * args.row_bytes, kNB * kRowRead, &full[s]);
+            } else if (present) {
+                bulk_g2s(dst + lane * kStride, args.cache + slot * args.row_bytes, kRowRead, &full[s]);
+            }
+            slot = next;
+        }
+        if (lane == 0) issued_s[pw] = cnt;
+        __syncthreads();     // matches the consumers' final barrier
+        return;
+    }
+
+    // ---- consumers: q of this tile's rows, loads issued first ----
+    const int g = lane >> 2;
+    const int c = lane & 3;
+    uint32_t qraw[2][16];
+    uint32_t qr[2][2];
+    int lim[2];                              // positions each row attends, counted from k0
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = pc.row0 + g + 8 * r;
+        qr[r][0] = qr[r][1] = 0u;
+        lim[r] = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) qraw[r][k] = 0u;
+        if (row < pc.rows) {
+            lim[r] = row_limit(args, pc, row) - k0;
+            const __nv_bfloat16* qh = args.q + (pc.grow0 + row) * args.d_qk;
+            const uint8_t* p = reinterpret_cast<const uint8_t*>(qh + 128 * warp + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint4 v = ld_nc_v4(p + 16 * k);
+                qraw[r][4 * k + 0] = v.x; qraw[r][4 * k + 1] = v.y;
+                qraw[r][4 * k + 2] = v.z; qraw[r][4 * k + 3] = v.w;
+            }
+            if (kRopeOn) {
+                const uint2 v = *reinterpret_cast<const uint2*>(qh + kLatent + 16 * warp + 4 * c);
+                qr[r][0] = v.x; qr[r][1] = v.y;
+            }
+        }
+    }
+    // ---- consumers: q fragments ----
+    float qm[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        qm[r] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) qm[r] = fmaxf(qm[r], fmaxf(fabsf(bf16lo(qraw[r][k])), fabsf(bf16hi(qraw[r][k]))));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) qm[r] = fmaxf(qm[r], fmaxf(fabsf(bf16lo(qr[r][k])), fabsf(bf16hi(qr[r][k]))));
+        qm[r] = quad_max(qm[r]);
+    }
+    if (c == 0) {
+        qmax_s[warp * kHeads + g] = qm[0];
+        qmax_s[warp * kHeads + g + 8] = qm[1];
+    }
+    bar_sync_or(1, kConsumerThreads, false);
+    // Exponent-only rescale so that |q| < 2^15 in f16 (exact in f16's normal
+    // range); the same power of two scales the RoPE part, and is undone on the
+    // scores through the per-row softmax factor.
+    float qdown[2], rowf[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float mx = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, qmax_s[w * kHeads + g + 8 * r]);
+        int e = 0;
+        frexpf(mx, &e);                              // mx < 2^e
+        const int k = (e > 15) ? (e - 15) : 0;
+        qdown[r] = ldexpf(1.0f, -k);
+        rowf[r] = args.sm_scale_log2 * ldexpf(1.0f, k);
+    }
+    uint32_t qa[8][4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int wi = 8 * hf + 2 * kk;
+            qa[4 * hf + kk][0] = pack_f16x2(bf16lo(qraw[0][wi]) * qdown[0], bf16hi(qraw[0][wi]) * qdown[0]);
+            qa[4 * hf + kk][1] = pack_f16x2(bf16lo(qraw[1][wi]) * qdown[1], bf16hi(qraw[1][wi]) * qdown[1]);
+            qa[4 * hf + kk][2] = pack_f16x2(bf16lo(qraw[0][wi + 1]) * qdown[0], bf16hi(qraw[0][wi + 1]) * qdown[0]);
+            qa[4 * hf + kk][3] = pack_f16x2(bf16lo(qraw[1][wi + 1]) * qdown[1], bf16hi(qraw[1][wi + 1]) * qdown[1]);
+        }
+    }
+    uint32_t qra[4];
+    qra[0] = pack_bf16x2(bf16lo(qr[0][0]) * qdown[0], bf16hi(qr[0][0]) * qdown[0]);
+    qra[1] = pack_bf16x2(bf16lo(qr[1][0]) * qdown[1], bf16hi(qr[1][0]) * qdown[1]);
+    qra[2] = pack_bf16x2(bf16lo(qr[0][1]) * qdown[0], bf16hi(qr[0][1]) * qdown[0]);
+    qra[3] = pack_bf16x2(bf16lo(qr[1][1]) * qdown[1], bf16hi(qr[1][1]) * qdown[1]);
+
+    // ---- consumers: main loop ----
+    // Per 32-position block: (1) QK partial of tile `warp` for all 32 positions, (2) the
+    // four tile partials meet in shared memory and warp w finishes the scores of
+    // positions 8w .. 8w+7 (its n-tile) and writes their P, (3) every warp multiplies
+    // all 32 rows of P into V of its own tile.
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m_ref[2] = {-INFINITY, -INFINITY};   // exp2 offset per row (log2 units); -inf: nothing seen yet
+    float l_run[2] = {0.0f, 0.0f};             // sum of p over this warp's positions
+    float sigma = FLT_MIN;                     // running max of tile `warp`'s row scales
+    float inv_sigma = 1.0f / FLT_MIN;
+    bool failed = false;
+
+    for (int b = 0; b < nblk; ++b) {
+        const int s = b % kStages;
+        const bool ok = mbar_wait_bounded(&full[s], static_cast<uint32_t>((b / kStages) & 1));
+        uint8_t* st = stages + s * kStageBytes;
+        const uint32_t present = vmask[s];
+        uint32_t poison = 0;                   // positions whose row holds a value that is not finite
+        bool again = false;
+        float acc[4][4], accr[4][4];
+        float sc[4][2];
+        uint32_t rs[2][2];
+qk_again:
+        // (1) QK^T of tile `warp`: latent on f16 MMA, RoPE slice on bf16 MMA.
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][i] = accr[nt][i] = 0.0f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            uint4 kv[4];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                kv[nt] = *reinterpret_cast<const uint4*>(st + (nt * 8 + g) * kStride + 128 * warp + 32 * c + 16 * hf);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const uint32_t wrd = kk == 0 ? kv[nt].x : kk == 1 ? kv[nt].y : kk == 2 ? kv[nt].z : kv[nt].w;
+                    uint32_t b0, b1;
+                    e4m3x4_to_f16x2x2(wrd, b0, b1);
+                    mma_f16(acc[nt], qa[4 * hf + kk], b0, b1);
+                }
+            }
+        }
+        if (kRopeOn) {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const uint2 rb = *reinterpret_cast<const uint2*>(st + (nt * 8 + g) * kStride + kTailOff + 32 * warp + 8 * c);
+                mma_bf16(accr[nt], qra, rb.x, rb.y);
+            }
+        }
+        // Scale of tile `warp` for rows nt*8 + 2c + e (absent rows were
+        // zero-filled: scale 0). The same registers serve the PV step.
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                sc[nt][e] = *reinterpret_cast<const float*>(st + (nt * 8 + 2 * c + e) * kStride + kScaleOff + 4 * warp);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            red[(warp * 4 + nt) * 32 + lane] =
+                make_float4(fmaf(acc[nt][0], sc[nt][0], accr[nt][0]), fmaf(acc[nt][1], sc[nt][1], accr[nt][1]),
+                            fmaf(acc[nt][2], sc[nt][0], accr[nt][2]), fmaf(acc[nt][3], sc[nt][1], accr[nt][3]));
+        // The part of PV that does not need P, ahead of the barriers: sigma (the
+        // running max of tile `warp`'s scales, so p * scale / sigma <= 2^8 in f16),
+        // O rescaled when it moves, and the rows' scale / sigma as f16 pairs.
+        float smax = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) smax = fmaxf(smax, fmaxf(sc[nt][0], sc[nt][1]));
+        smax = quad_max(smax);                 // all 32 rows: the same in every lane
+        if (smax > sigma && smax <= FLT_MAX) {   // an infinite scale's row is zeroed below
+            const float f = sigma / smax;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+            }
+            sigma = smax;
+            inv_sigma = 1.0f / smax;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            rs[kb][0] = pack_f16x2(sc[2 * kb][0] * inv_sigma, sc[2 * kb][1] * inv_sigma);
+            rs[kb][1] = pack_f16x2(sc[2 * kb + 1][0] * inv_sigma, sc[2 * kb + 1][1] * inv_sigma);
+        }
+        // A value that is not finite in a staged row shows in its products. Then (rare)
+        // such rows are found, marked and zeroed, so that a position masked for a query
+        // row cannot reach it through 0 * NaN in PV; the block's QK is done again.
+        bool odd = false;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd = odd || !(fabsf(fmaf(acc[nt][i], sc[nt][i & 1], accr[nt][i])) <= FLT_MAX);
+        // Barrier 1 also carries a timeout of any warp, or such a value, to all of them.
+        if (bar_sync_or(1, kConsumerThreads, !ok || (odd && !again))) {
+            if (bar_sync_or(1, kConsumerThreads, !ok)) { failed = true; break; }
+            uint32_t mine = 0;
+            for (int j = 0; j < 8; ++j) {
+                uint8_t* row = st + (8 * warp + j) * kStride;
+                if (!row_not_finite(row, kRopeOn, lane)) continue;
+                mine |= 1u << j;
+                __syncwarp();
+                for (int k = lane; k < kStride / 16; k += 32) *reinterpret_cast<uint4*>(row + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (lane == 0) poison_s[warp] = mine;
+            bar_sync_or(1, kConsumerThreads, false);
+            poison = poison_s[0] | (poison_s[1] << 8) | (poison_s[2] << 16) | (poison_s[3] << 24);
+            again = true;
+            goto qk_again;
+        }
+
+        // (2) scores of n-tile `warp`: positions 8*warp + 2c + {0,1}, rows g and g+8.
+        float4 a = red[warp * 32 + lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 bq = red[(w * 4 + warp) * 32 + lane];
+            a.x += bq.x; a.y += bq.y; a.z += bq.z; a.w += bq.w;
+        }
+        float sv[4] = {a.x * rowf[0], a.y * rowf[0], a.z * rowf[1], a.w * rowf[1]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 8 * warp + 2 * c + (i & 1);
+            if (((poison >> j) & 1u) != 0u) sv[i] = __int_as_float(0x7FC00000);
+            if (((present >> j) & 1u) == 0u || kNB * b + j >= lim[i >> 1]) sv[i] = -INFINITY;
+        }
+        const float bm0 = quad_max(fmaxf(sv[0], sv[1]));
+        const float bm1 = quad_max(fmaxf(sv[2], sv[3]));
+        if (c == 0) {
+            rmax_s[warp * kHeads + g] = bm0;
+            rmax_s[warp * kHeads + g + 8] = bm1;
+        }
+        const bool need = bm0 > m_ref[0] + kRescaleSlack || bm1 > m_ref[1] + kRescaleSlack;
+        float p[4];
+        // nothing seen yet: any finite offset makes the masked scores 0
+        const float off0 = m_ref[0] == -INFINITY ? 0.0f : m_ref[0];
+        const float off1 = m_ref[1] == -INFINITY ? 0.0f : m_ref[1];
+        p[0] = ex2_approx(sv[0] - off0);
+        p[1] = ex2_approx(sv[1] - off0);
+        p[2] = ex2_approx(sv[2] - off1);
+        p[3] = ex2_approx(sv[3] - off1);
+        uint2* pw = reinterpret_cast<uint2*>(pbuf) + warp * 32 + lane;
+        *pw = make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
+        // V rows of the first PV step: loaded before barrier 2 (they do not depend on P).
+        const uint8_t* vb = st + 128 * warp + 16 * g;
+        uint4 Vn[4];
+        Vn[0] = *reinterpret_cast<const uint4*>(vb + (2 * c + 0) * kStride);
+        Vn[1] = *reinterpret_cast<const uint4*>(vb + (2 * c + 1) * kStride);
+        Vn[2] = *reinterpret_cast<const uint4*>(vb + (2 * c + 8) * kStride);
+        Vn[3] = *reinterpret_cast<const uint4*>(vb + (2 * c + 9) * kStride);
+        if (bar_sync_or(1, kConsumerThreads, need)) {
+            // Rare after the first block: move the offsets of the rows whose
+            // block maximum ran ahead, rescale O and l, and rewrite this warp's P.
+            float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                M0 = fmaxf(M0, rmax_s[w * kHeads + g]);
+                M1 = fmaxf(M1, rmax_s[w * kHeads + g + 8]);
+            }
+            const float mn0 = (M0 > m_ref[0] + kRescaleSlack) ? M0 : m_ref[0];
+            const float mn1 = (M1 > m_ref[1] + kRescaleSlack) ? M1 : m_ref[1];
+            const float a0 = mn0 == m_ref[0] ? 1.0f : ex2_approx(m_ref[0] - mn0);     // -inf -> 0
+            const float a1 = mn1 == m_ref[1] ? 1.0f : ex2_approx(m_ref[1] - mn1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i][0] *= a0; o[i][1] *= a0; o[i][2] *= a1; o[i][3] *= a1;
+            }
+            l_run[0] *= a0;
+            l_run[1] *= a1;
+            m_ref[0] = mn0;
+            m_ref[1] = mn1;
+            const float of0 = mn0 == -INFINITY ? 0.0f : mn0;
+            const float of1 = mn1 == -INFINITY ? 0.0f : mn1;
+            p[0] = ex2_approx(sv[0] - of0);
+            p[1] = ex2_approx(sv[1] - of0);
+            p[2] = ex2_approx(sv[2] - of1);
+            p[3] = ex2_approx(sv[3] - of1);
+            *pw = make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
+            bar_sync_or(1, kConsumerThreads, false);
+        }
+        l_run[0] += p[0] + p[1];
+        l_run[1] += p[2] + p[3];
+
+        // (3) PV of tile `warp`.
+        const uint2* pr = reinterpret_cast<const uint2*>(pbuf) + lane;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            // A: P of heads (g, g+8) x rows 16kb + 2c + {0,1} and + 8, times the
+            // row's tile scale / sigma.
+            const uint2 plo = pr[(2 * kb) * 32];
+            const uint2 phi = pr[(2 * kb + 1) * 32];
+            const uint32_t r01 = rs[kb][0];
+            const uint32_t r89 = rs[kb][1];
+            uint32_t pa[4];
+            pa[0] = hmul2(plo.x, r01);
+            pa[1] = hmul2(plo.y, r01);
+            pa[2] = hmul2(phi.x, r89);
+            pa[3] = hmul2(phi.y, r89);
+            // B: V rows j0, j0+1, j0+8, j0+9; lane g takes dims 128w + 16g .. +15,
+            // so n-tile (q, i) column n is dim 128w + 16n + 4q + i.
+            const int j0 = 16 * kb + 2 * c;
+            const uint4 V0 = kb == 0 ? Vn[0] : *reinterpret_cast<const uint4*>(vb + (j0 + 0) * kStride);
+            const uint4 V1 = kb == 0 ? Vn[1] : *reinterpret_cast<const uint4*>(vb + (j0 + 1) * kStride);
+            const uint4 V2 = kb == 0 ? Vn[2] : *reinterpret_cast<const uint4*>(vb + (j0 + 8) * kStride);
+            const uint4 V3 = kb == 0 ? Vn[3] : *reinterpret_cast<const uint4*>(vb + (j0 + 9) * kStride);
+#pragma unroll
+            for (int qd = 0; qd < 4; ++qd) {
+                const uint32_t W0 = qd == 0 ? V0.x : qd == 1 ? V0.y : qd == 2 ? V0.z : V0.w;
+                const uint32_t W1 = qd == 0 ? V1.x : qd == 1 ? V1.y : qd == 2 ? V1.z : V1.w;
+                const uint32_t W2 = qd == 0 ? V2.x : qd == 1 ? V2.y : qd == 2 ? V2.z : V2.w;
+                const uint32_t W3 = qd == 0 ? V3.x : qd == 1 ? V3.y : qd == 2 ? V3.z : V3.w;
+                uint32_t b0a, b0b, b0c, b0d, b1a, b1b, b1c, b1d;
+                e4m3x4_to_f16x2x2(prmt(W0, W1, 0x5140), b0a, b0b);   // d offsets 0, 1
+                e4m3x4_to_f16x2x2(prmt(W0, W1, 0x7362), b0c, b0d);   // d offsets 2, 3
+                e4m3x4_to_f16x2x2(prmt(W2, W3, 0x5140), b1a, b1b);
+                e4m3x4_to_f16x2x2(prmt(W2, W3, 0x7362), b1c, b1d);
+                mma_f16(o[4 * qd + 0], pa, b0a, b1a);
+                mma_f16(o[4 * qd + 1], pa, b0b, b1b);
+                mma_f16(o[4 * qd + 2], pa, b0c, b1c);
+                mma_f16(o[4 * qd + 3], pa, b0d, b1d);
+            }
+        }
+        // The stage is next written by the async proxy (cp.async.bulk): order this
+        // warp's generic accesses of it before that write.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    __syncthreads();     // all warps: producers done issuing, consumers done reading
+    if (failed || issued_s[0] + issued_s[1] < nblk) {
+        // A wait ran out: record it, let the copies already issued land (bounded)
+        // and leave without touching the outputs.
+        if (threadIdx.x == 0) {
+            atomicOr(args.err, MLA_ERR_PIPELINE_TIMEOUT);
+            for (int p = 0; p < kProducers; ++p) {
+                const int cnt = issued_s[p];
+                for (int k = max(0, cnt - kStages / kProducers); k < cnt; ++k) {
+                    const int bb = p + kProducers * k;
+                    (void)mbar_wait_bounded(&full[bb % kStages], static_cast<uint32_t>((bb / kStages) & 1));
+                }
+            }
+        }
+        return;
+    }
+
+    // ---- epilogue: l over the four warps' positions, then O * sigma / l ----
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float l = l_run[r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (c == 0) lsum_s[warp * kHeads + g + 8 * r] = l;
+    }
+    bar_sync_or(1, kConsumerThreads, false);
+    float lt[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        lt[0] += lsum_s[w * kHeads + g];
+        lt[1] += lsum_s[w * kHeads + g + 8];
+    }
+    // l = 0: nothing attended (out 0, lse -inf). l NaN: an attended row holds a value
+    // that is not finite (out and lse NaN).
+    const float kNaN = __int_as_float(0x7FC00000);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = pc.row0 + g + 8 * r;
+        if (row >= pc.rows) continue;
+        const float mm = lt[r] > 0.0f ? sigma / lt[r] : (lt[r] == 0.0f ? 0.0f : kNaN);
+        const float lse = lt[r] > 0.0f ? (m_ref[r] + log2f(lt[r])) * kLn2 : (lt[r] == 0.0f ? -INFINITY : kNaN);
+        // Thread (g, c) holds, for row r, dims 128w + 32c + 16e + 4q + i in
+        // o[4q + i][2r + e]: 32 contiguous output values per row.
+        if (pc.part < 0) {
+            __nv_bfloat16* orow = args.out + (pc.grow0 + row) * kLatent + 128 * warp + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int hq = 0; hq < 2; ++hq) {
+                    uint4 v;
+                    v.x = pack_bf16x2(o[8 * hq + 0][2 * r + e] * mm, o[8 * hq + 1][2 * r + e] * mm);
+                    v.y = pack_bf16x2(o[8 * hq + 2][2 * r + e] * mm, o[8 * hq + 3][2 * r + e] * mm);
+                    v.z = pack_bf16x2(o[8 * hq + 4][2 * r + e] * mm, o[8 * hq + 5][2 * r + e] * mm);
+                    v.w = pack_bf16x2(o[8 * hq + 6][2 * r + e] * mm, o[8 * hq + 7][2 * r + e] * mm);
+                    st_v4(orow + 16 * e + 8 * hq, v);
+                }
+            }
+            if (warp == 0 && c == 0) args.lse[pc.grow0 + row] = lse;
+        } else {
+            const int64_t prow = static_cast<int64_t>(pc.part) * args.tile_rows + g + 8 * r;
+            if (warp == 0 && c == 0) args.part_lse[prow] = lse;
+            if (lt[r] == 0.0f) continue;       // lse = -inf: the merge skips this partial's o
+            float* orow = args.part_o + prow * kLatent + 128 * warp + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int qd = 0; qd < 4; ++qd)
+                    reinterpret_cast<float4*>(orow + 16 * e + 4 * qd)[0] =
+                        make_float4(o[4 * qd + 0][2 * r + e] * mm, o[4 * qd + 1][2 * r + e] * mm,
+                                    o[4 * qd + 2][2 * r + e] * mm, o[4 * qd + 3][2 * r + e] * mm);
+        }
+    }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Two CTAs of the small-tile kernel fit an SM. A piece shorter than kMinPiece saves
+// less than its partial and its share of the merge cost.
+constexpr int kCtasPerSm = 2;
+constexpr int kMinPiece = 128;
+
+struct Sizes {
+    int tile_rows, wave;
+    int64_t max_pieces;
+    size_t parts_o, parts_lse, prefix;     // bytes
+    size_t total() const { return parts_o + parts_lse + 4 * prefix; }
+};
+
+Sizes sizes_of(int T, int H, int n_seq, int sms) {
+    Sizes z;
+    z.tile_rows = kSmallRows;
+    z.wave = kCtasPerSm * sms;
+    z.max_pieces = static_cast<int64_t>(T) * H / z.tile_rows + (n_seq < T ? n_seq : T) + z.wave;
+    const size_t rows = 2 * static_cast<size_t>(z.wave) * z.tile_rows;
+    z.parts_o = rows * kLatent * sizeof(float);
+    z.parts_lse = align256(rows * sizeof(float));
+    z.prefix = align256((static_cast<size_t>(n_seq) + 1) * sizeof(int32_t));
+    return z;
+}
+
+template <typename K, typename... A>
+bool launch(K kernel, int64_t grid, int threads, size_t smem, void* stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" size_t mla_chunk_attention_workspace_bytes(int T, int H, int n_seq) {
+    if (T <= 0 || H < 1 || H > 128 || n_seq <= 0) return 0;
+    const int sms = mla_host::sm_count();
+    return sms <= 0 ? 0 : sizes_of(T, H, n_seq, sms).total();
+}
+
+extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
+                                   const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages,
+                                   int page_size, int causal, float sm_scale, void* out_bf16, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || n_seq < 0 || max_pages < 0 || page_size <= 0 || kv.num_slots < 0 || !std::isfinite(sm_scale))
+        return MLA_EINVAL;
+    if (kv.row_bytes != MLA_ROW_BYTES && kv.row_bytes != MLA_ROW_BYTES_NOPE) return MLA_EINVAL;
+    if (d_qk != kLatent && d_qk != kLatent + kRope) return MLA_EUNSUPPORTED;
+    if (kv.row_bytes == MLA_ROW_BYTES_NOPE && d_qk != kLatent) return MLA_EUNSUPPORTED;   // no tail to read
+    if (H < 1 || H > 128) return MLA_EUNSUPPORTED;
+    if (T == 0 || n_seq == 0) return MLA_OK;
+    if (static_cast<int64_t>(T) * H > INT_MAX / 4) return MLA_EUNSUPPORTED;
+    if (q_bf16 == nullptr || out_bf16 == nullptr || lse == nullptr || q_start == nullptr || kv_len == nullptr ||
+        (max_pages > 0 && (block_table == nullptr || kv.data == nullptr)))
+        return MLA_EINVAL;
+    if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16) || !aligned(kv.data, 16) || !aligned(lse, 4) ||
+        !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
+        return MLA_EINVAL;
+    int* err = mla_host::device_error_word();
+    const int sms = mla_host::sm_count();
+    if (err == nullptr || sms <= 0) return MLA_ECUDA;
+    const Sizes z = sizes_of(T, H, n_seq, sms);
+    if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < z.total()) return MLA_ENOWORKSPACE;
+    const bool rope = d_qk == kLatent + kRope;
+    const void* kernel = rope ? reinterpret_cast<const void*>(mla_chunk_small_kernel<true>)
+                              : reinterpret_cast<const void*>(mla_chunk_small_kernel<false>);
+    if (!mla_host::max_dynamic_smem(kernel, kSmemTotal)) return MLA_ECUDA;
+
+    ChunkArgs a;
+    a.q = static_cast<const __nv_bfloat16*>(q_bf16);
+    a.cache = static_cast<const uint8_t*>(kv.data);
+    a.out = static_cast<__nv_bfloat16*>(out_bf16);
+    a.lse = lse;
+    a.num_slots = kv.num_slots;
+    a.row_bytes = kv.row_bytes;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.block_table = block_table;
+    a.n_seq = n_seq;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.T = T;
+    a.H = H;
+    a.d_qk = d_qk;
+    a.causal = causal != 0;
+    a.sm_scale_log2 = sm_scale * kLog2e;
+    a.err = err;
+    a.tile_rows = z.tile_rows;
+    a.align = kNB;
+    a.wave = z.wave;
+    a.min_piece = kMinPiece;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    a.part_o = reinterpret_cast<float*>(w);
+    w += z.parts_o;
+    a.part_lse = reinterpret_cast<float*>(w);
+    w += z.parts_lse;
+    int32_t** prefixes[4] = {&a.piece0, &a.part0, &a.mrow0, &a.split};
+    for (int32_t** p : prefixes) {
+        *p = reinterpret_cast<int32_t*>(w);
+        w += z.prefix;
+    }
+    if (!launch(chunk_plan_kernel, 1, kPlanThreads, 0, stream, a)) return MLA_ECUDA;
+    const bool ok = rope ? launch(mla_chunk_small_kernel<true>, z.max_pieces, kThreads, kSmemTotal, stream, a)
+                         : launch(mla_chunk_small_kernel<false>, z.max_pieces, kThreads, kSmemTotal, stream, a);
+    if (!ok) return MLA_ECUDA;
+    // Rows of split tiles: at most those of 2 wave pieces, in pairs at least.
+    int64_t merge = static_cast<int64_t>(z.wave) * z.tile_rows;
+    if (merge > static_cast<int64_t>(T) * H) merge = static_cast<int64_t>(T) * H;
+    if (merge > static_cast<int64_t>(sms) * 16) merge = static_cast<int64_t>(sms) * 16;
+    return launch(mla_chunk_merge_kernel, merge, 128, 0, stream, a) ? MLA_OK : MLA_ECUDA;
+}

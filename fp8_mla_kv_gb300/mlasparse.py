@@ -27,10 +27,16 @@ MLA_ERR_WRITE_SLOT_RANGE = 0x1
 MLA_ERR_DECODE_INDEX_RANGE = 0x2
 MLA_ERR_PIPELINE_TIMEOUT = 0x4
 MLA_ERR_GATHER_INDEX_RANGE = 0x8
+MLA_ERR_CHUNK_RANGE = 0x10
+MLA_ERR_PAGE_RANGE = 0x20
+MLA_ERR_PAGE_COUNT = 0x40
+MLA_ERR_POOL_EMPTY = 0x80
 
 SYMBOLS = ("mla_kv_write", "mla_sparse_decode", "mla_sparse_decode_workspace_bytes",
            "mla_sparse_decode_paged", "mla_sparse_prefill", "mla_sparse_prefill_paged",
-           "mla_gather_upconvert", "mla_get_error", "mla_strerror")
+           "mla_gather_upconvert", "mla_rope", "mla_rope_kv_write", "mla_chunk_attention",
+           "mla_chunk_attention_workspace_bytes", "mla_page_copy", "mla_page_free", "mla_page_fork",
+           "mla_page_compact", "mla_page_workspace_bytes", "mla_get_error", "mla_strerror")
 
 
 class MlaError(RuntimeError):
@@ -41,6 +47,12 @@ class MlaError(RuntimeError):
 
 class KVCache(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
+
+
+class RopeSpec(ctypes.Structure):
+    """mla_rope_t; rope_spec() makes one."""
+    _fields_ = [("inv_freq", ctypes.c_double * 32), ("scale", ctypes.c_float), ("n_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("axis", ctypes.c_uint8 * 32)]
 
 
 _lock = threading.Lock()
@@ -80,6 +92,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                      c.c_float, c.c_void_p, c.c_void_p, c.c_void_p]
             lib.mla_gather_upconvert.restype = c.c_int
             lib.mla_gather_upconvert.argtypes = [KVCache, c.c_void_p, c.c_int64, c.c_int, c.c_void_p, c.c_void_p]
+            vp, i32, i64 = c.c_void_p, c.c_int, c.c_int64
+            lib.mla_rope.restype = i32
+            lib.mla_rope.argtypes = [vp, i64, i64, vp, i64, i64, i64, i32, vp, i64, c.POINTER(RopeSpec), vp]
+            lib.mla_rope_kv_write.restype = i32
+            lib.mla_rope_kv_write.argtypes = [KVCache, vp, vp, vp, i64, i64, vp, i64, c.POINTER(RopeSpec), vp, i64, i64,
+                                              vp, i64, i64, i32, vp]
+            lib.mla_chunk_attention_workspace_bytes.restype = c.c_size_t
+            lib.mla_chunk_attention_workspace_bytes.argtypes = [i32, i32, i32]
+            lib.mla_chunk_attention.restype = i32
+            lib.mla_chunk_attention.argtypes = [vp, i32, i32, i32, KVCache, vp, vp, vp, i32, i32, i32, i32, c.c_float,
+                                                vp, vp, vp, c.c_size_t, vp]
+            lib.mla_page_copy.restype = i32
+            lib.mla_page_copy.argtypes = [KVCache, KVCache, i32, vp, vp, i64, vp]
+            lib.mla_page_free.restype = i32
+            lib.mla_page_free.argtypes = [vp, i32, vp, i32, i32, vp, i32, vp]
+            lib.mla_page_fork.restype = i32
+            lib.mla_page_fork.argtypes = [KVCache, i32, vp, i32, vp, i32, i32, vp, vp, vp, i32, vp, c.c_size_t, vp]
+            lib.mla_page_compact.restype = i32
+            lib.mla_page_compact.argtypes = [KVCache, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, c.c_size_t, vp]
+            lib.mla_page_workspace_bytes.restype = c.c_size_t
+            lib.mla_page_workspace_bytes.argtypes = [i32, i32]
             lib.mla_get_error.restype = c.c_int
             lib.mla_get_error.argtypes = [c.POINTER(c.c_int32)]
             lib.mla_strerror.restype = c.c_char_p
@@ -265,6 +298,207 @@ def mla_gather_upconvert(cache: torch.Tensor, slots: torch.Tensor, pe_dim: int,
     if rc != MLA_OK:
         raise MlaError(rc, "mla_gather_upconvert")
     return out
+
+
+def rope_spec(inv_freq, axis=None, interleaved: bool = False, scale: float = 1.0, inverse: bool = False) -> RopeSpec:
+    """Rotary frequencies of the 32 pairs (radians per position) and the axis each pair turns by (default: axis 0)."""
+    inv, ax = list(inv_freq), [0] * 32 if axis is None else [int(a) for a in axis]
+    if len(inv) != 32 or len(ax) != 32 or min(ax) < 0 or max(ax) > 3:
+        raise ValueError("rope_spec takes 32 frequencies and 32 axes in 0..3")
+    return RopeSpec((ctypes.c_double * 32)(*inv), scale, max(ax) + 1, int(interleaved), int(inverse),
+                    (ctypes.c_uint8 * 32)(*ax))
+
+
+def _same_device(*ts) -> None:
+    _require_cuda(*ts)
+    if len({t.device for t in ts if t is not None}) > 1:
+        raise ValueError("tensors on different devices")
+
+
+def _positions(pos: torch.Tensor, n: int, n_axes: int) -> int:
+    """Checks positions int32 [n] or [axes, n]; returns the stride between axes."""
+    if pos.dtype != torch.int32 or pos.dim() not in (1, 2) or pos.shape[-1] != n or (n > 1 and pos.stride(-1) != 1):
+        raise ValueError("positions must be int32 [n] or [axes, n], contiguous along n")
+    if (1 if pos.dim() == 1 else int(pos.shape[0])) < n_axes:
+        raise ValueError(f"positions for {n_axes} axes expected")
+    return n if pos.dim() == 1 else max(n, int(pos.stride(0)))
+
+
+def _rope_view(x: torch.Tensor, n: int):
+    """(pointer, row stride, head stride, heads) of a bf16 [n, heads, 64] or [n, 64] view."""
+    if x.dtype != torch.bfloat16 or x.dim() not in (2, 3) or x.shape[0] != n or x.shape[-1] != 64 or x.stride(-1) != 1:
+        raise ValueError("rotary values must be bf16 [n, heads, 64] or [n, 64], contiguous along the 64")
+    if x.dim() == 2:
+        return x.data_ptr(), x.stride(0), 0, 1
+    return x.data_ptr(), x.stride(0), x.stride(1), int(x.shape[1])
+
+
+def mla_rope(x: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """Rotates x bf16 [n, heads, 64] (or [n, 64], any row and head strides that are multiples of 8) by positions
+    int32 [n] or [axes, n]; out may be x."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _same_device(x, pos, out)
+    n = int(x.shape[0])
+    stride = _positions(pos, n, rope.n_axes)
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    xp, xr, xh, heads = _rope_view(x, n)
+    yp, yr, yh, _ = _rope_view(out, n)
+    rc = load().mla_rope(xp, xr, xh, yp, yr, yh, n, heads, pos.data_ptr(), stride, ctypes.byref(rope), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_rope")
+    return out
+
+
+def mla_rope_kv_write(cache: torch.Tensor, slot_idx: torch.Tensor, latent: torch.Tensor, k_pe: torch.Tensor,
+                      pos: torch.Tensor, rope: RopeSpec, q_pe: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None, reserved_slot: int = 0, stream=None) -> None:
+    """mla_kv_write with k_pe [n, 64] rotated on the way; q_pe [n, heads, 64] (a view, for example the last 64 values of
+    a query projection) rotated into q_out (default: in place) in the same launch."""
+    if q_pe is not None and q_out is None:
+        q_out = q_pe
+    _same_device(cache, slot_idx, latent, k_pe, pos, q_pe, q_out)
+    n = int(slot_idx.shape[0])
+    assert slot_idx.dtype == torch.int64 and slot_idx.is_contiguous()
+    assert latent.dtype == torch.bfloat16 and latent.is_contiguous() and latent.numel() == n * 512
+    assert k_pe.dtype == torch.bfloat16 and k_pe.is_contiguous() and k_pe.numel() == n * 64
+    stride = _positions(pos, n, rope.n_axes)
+    xp = yp = None
+    xr = xh = yr = yh = heads = 0
+    if q_pe is not None:
+        if q_out.shape != q_pe.shape:
+            raise ValueError("q_out must have the shape of q_pe")
+        xp, xr, xh, heads = _rope_view(q_pe, n)
+        yp, yr, yh, _ = _rope_view(q_out, n)
+    elif q_out is not None:
+        raise ValueError("q_out without q_pe")
+    rc = load().mla_rope_kv_write(kv_cache(cache), slot_idx.data_ptr(), latent.data_ptr(), k_pe.data_ptr(), n,
+                                  int(reserved_slot), pos.data_ptr(), stride, ctypes.byref(rope), xp, xr, xh, yp, yr, yh,
+                                  heads, _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_rope_kv_write")
+
+
+def mla_chunk_attention_workspace_bytes(T: int, H: int, n_seq: int) -> int:
+    return int(load().mla_chunk_attention_workspace_bytes(int(T), int(H), int(n_seq)))
+
+
+def alloc_chunk_workspace(T: int, H: int, n_seq: int, device=None) -> torch.Tensor:
+    return torch.empty(max(16, mla_chunk_attention_workspace_bytes(T, H, n_seq)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def mla_chunk_attention(q: torch.Tensor, cache: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                        block_table: torch.Tensor, page_size: int, sm_scale: float, causal: bool = True,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Attention of new tokens over the paged cache, ragged batch: q bf16 [T, H, d_qk]; q_start int32 [n_seq + 1];
+    kv_len int32 [n_seq] (new tokens included); block_table int32 [n_seq, max_pages]. Returns (out bf16 [T, H, 512],
+    lse fp32 [T, H]); without `out` and `lse`, tokens outside every sequence get 0 and -inf."""
+    _same_device(q, cache, q_start, kv_len, block_table, out, lse, workspace)
+    T, H, d_qk = (int(s) for s in q.shape)
+    n_seq = int(kv_len.shape[0])
+    assert q.dtype == torch.bfloat16 and q.is_contiguous()
+    assert q_start.dtype == torch.int32 and q_start.is_contiguous() and q_start.numel() == n_seq + 1
+    assert kv_len.dtype == torch.int32 and kv_len.is_contiguous()
+    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2
+    assert block_table.shape[0] == n_seq
+    if out is None:
+        out = torch.zeros((T, H, 512), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q.device)
+    assert out.dtype == torch.bfloat16 and out.is_contiguous() and out.numel() == T * H * 512
+    assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == T * H
+    if workspace is None:
+        workspace = alloc_chunk_workspace(T, H, n_seq, q.device)
+    rc = load().mla_chunk_attention(q.data_ptr(), T, H, d_qk, kv_cache(cache), q_start.data_ptr(), kv_len.data_ptr(),
+                                    block_table.data_ptr(), n_seq, int(block_table.shape[1]), int(page_size),
+                                    int(bool(causal)), float(sm_scale), out.data_ptr(), lse.data_ptr(),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_chunk_attention")
+    return out, lse
+
+
+def _ints(*ts) -> None:
+    for t in ts:
+        if t is not None:
+            assert t.dtype == torch.int32 and t.is_contiguous()
+
+
+def mla_page_workspace_bytes(num_pages: int, n_forks: int = 0) -> int:
+    return int(load().mla_page_workspace_bytes(int(num_pages), int(n_forks)))
+
+
+def alloc_page_workspace(num_pages: int, n_forks: int = 0, device=None) -> torch.Tensor:
+    return torch.empty(mla_page_workspace_bytes(num_pages, n_forks), dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_page_copy(dst_cache: torch.Tensor, src_cache: torch.Tensor, page_size: int, dst: torch.Tensor,
+                  src: torch.Tensor, stream=None) -> None:
+    """Pages src (int32 [n]) of src_cache to pages dst of dst_cache (which may be the same cache)."""
+    _same_device(dst_cache, src_cache, dst, src)
+    _ints(dst, src)
+    assert dst.numel() == src.numel()
+    rc = load().mla_page_copy(kv_cache(dst_cache), kv_cache(src_cache), int(page_size), dst.data_ptr(), src.data_ptr(),
+                              int(dst.numel()), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_page_copy")
+
+
+def mla_page_free(refcount: torch.Tensor, block_table: torch.Tensor, rows: torch.Tensor, stream=None) -> None:
+    """Rows (int32 [n]) of block_table let go of their pages."""
+    _same_device(refcount, block_table, rows)
+    _ints(refcount, block_table, rows)
+    rc = load().mla_page_free(refcount.data_ptr(), int(refcount.numel()), block_table.data_ptr(),
+                              int(block_table.shape[0]), int(block_table.shape[1]), rows.data_ptr(), int(rows.numel()),
+                              _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_page_free")
+
+
+def mla_page_fork(cache: torch.Tensor, page_size: int, refcount: torch.Tensor, block_table: torch.Tensor,
+                  parent: torch.Tensor, child: torch.Tensor, lens: torch.Tensor,
+                  workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Row child[i] of block_table becomes a copy of row parent[i] up to lens[i] positions: whole pages shared, a last
+    page that is not full copied to a free page."""
+    _same_device(cache, refcount, block_table, parent, child, lens, workspace)
+    _ints(refcount, block_table, parent, child, lens)
+    n = int(parent.numel())
+    assert child.numel() == n and lens.numel() == n
+    if workspace is None:
+        workspace = alloc_page_workspace(refcount.numel(), n, cache.device)
+    rc = load().mla_page_fork(kv_cache(cache), int(page_size), refcount.data_ptr(), int(refcount.numel()),
+                              block_table.data_ptr(), int(block_table.shape[0]), int(block_table.shape[1]),
+                              parent.data_ptr(), child.data_ptr(), lens.data_ptr(), n, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_page_fork")
+
+
+def mla_page_compact(cache: torch.Tensor, page_size: int, refcount: torch.Tensor, block_table: torch.Tensor,
+                     refcount_out: torch.Tensor | None = None, table_out: torch.Tensor | None = None,
+                     page_map: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Moves the live pages to 1 .. live. Counts and table are updated in place unless refcount_out / table_out are
+    given; page_map (int32 [num_pages]) receives where each page went."""
+    refcount_out = refcount if refcount_out is None else refcount_out
+    table_out = block_table if table_out is None else table_out
+    _same_device(cache, refcount, block_table, refcount_out, table_out, page_map, workspace)
+    _ints(refcount, block_table, refcount_out, table_out, page_map)
+    assert refcount_out.numel() == refcount.numel() and table_out.shape == block_table.shape
+    assert page_map is None or page_map.numel() == refcount.numel()
+    if workspace is None:
+        workspace = alloc_page_workspace(refcount.numel(), 0, cache.device)
+    rc = load().mla_page_compact(kv_cache(cache), int(page_size), refcount.data_ptr(), refcount_out.data_ptr(),
+                                 int(refcount.numel()), block_table.data_ptr(), table_out.data_ptr(),
+                                 int(block_table.shape[0]), int(block_table.shape[1]),
+                                 page_map.data_ptr() if page_map is not None else None, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_page_compact")
 
 
 def mla_get_error() -> int:

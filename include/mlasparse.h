@@ -62,6 +62,10 @@ extern "C" {
 #define MLA_ERR_DECODE_INDEX_RANGE 0x2  /* mla_sparse_decode: index >= num_slots, entry absent */
 #define MLA_ERR_PIPELINE_TIMEOUT   0x4  /* a kernel's bounded wait on its own copies ran out */
 #define MLA_ERR_GATHER_INDEX_RANGE 0x8  /* mla_gather_upconvert: slot >= num_slots, zero row */
+#define MLA_ERR_CHUNK_RANGE        0x10 /* mla_chunk_attention: q_start not nondecreasing within [0, T], or kv_len past the table */
+#define MLA_ERR_PAGE_RANGE         0x20 /* mla_page_*: a page, row or length out of range, dropped */
+#define MLA_ERR_PAGE_COUNT         0x40 /* mla_page_free: a page whose count was 0 already */
+#define MLA_ERR_POOL_EMPTY         0x80 /* mla_page_fork: no free page left, the entry stays -1 */
 
 /* A cache: `data` is a device array of num_slots rows of row_bytes bytes,
  * 16-byte aligned. row_bytes is MLA_ROW_BYTES (656), or MLA_ROW_BYTES_NOPE
@@ -294,6 +298,161 @@ int mla_gather_upconvert(mla_kv_cache_t kv, const int32_t* slots, int64_t n, int
 int mla_sparse_decode_noalloc(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv,
                               const int32_t* topk_idx, int W, float sm_scale, void* out_bf16,
                               float* lse, void* stream);
+
+/*
+ * mla_rope_t - rotary positions with one to four axes (text: one; images and video:
+ * time, height, width). A host structure, read during the call.
+ *
+ * Pair i of the 64 rotary values is (x, y) = values (i, i + 32), or (2i, 2i + 1) when
+ * `interleaved`; at position p of axis[i] it becomes
+ *     scale * (x cos a - y sin a, x sin a + y cos a),   a = p * inv_freq[i]  (-a: `inverse`)
+ * rounded to BF16 once. Sections of pairs per axis may be contiguous, interleaved or
+ * anything else: axis[] says it pair by pair. `inverse` undoes the rotation, and
+ * is its gradient: dx of y = rope(x) is the inverse rope of dy.
+ */
+#define MLA_ROPE_MAX_AXES  4
+typedef struct {
+    double  inv_freq[MLA_ROPE_DIM / 2];   /* radians per unit of position; finite */
+    float   scale;                        /* of cos and sin (1 where none is wanted); finite */
+    int32_t n_axes;                       /* 1 .. MLA_ROPE_MAX_AXES */
+    int32_t interleaved;                  /* pairs (2i, 2i + 1), else (i, i + 32) */
+    int32_t inverse;                      /* turn back */
+    uint8_t axis[MLA_ROPE_DIM / 2];       /* 0 .. n_axes - 1 */
+} mla_rope_t;
+
+/*
+ * mla_rope - rotates a strided view of rows x heads x 64 BF16 values.
+ *
+ * Positions are any int32 (angles are reduced exactly, so far positions lose nothing).
+ *   x_bf16, y_bf16  first rotary value of row 0, head 0; 16-byte aligned; y may be x
+ *                   with the same strides (in place), otherwise they may not overlap
+ *   *_row, *_head   strides in values, multiples of 8 (unused where there is one row
+ *                   or one head)
+ *   n_rows, n_heads >= 0 (0 launches nothing)
+ *   pos             int32 [n_axes, n_rows], device; axis k at pos + k * pos_stride
+ *                   (pos_stride >= n_rows when n_axes > 1)
+ * Launched with programmatic stream serialization like the writer.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+int mla_rope(const void* x_bf16, int64_t x_row, int64_t x_head, void* y_bf16, int64_t y_row, int64_t y_head,
+             int64_t n_rows, int n_heads, const int32_t* pos, int64_t pos_stride, const mla_rope_t* rope,
+             void* stream);
+
+/*
+ * mla_rope_kv_write - mla_kv_write with the rotary tail turned on the way, and, where
+ * q is given, the rotary part of the same rows' queries turned in the same launch.
+ *
+ * Rows are dropped exactly as in mla_kv_write (reserved slot, negative, past the
+ * cache: flagged) with none of their latent, k_pe and position read for the write. The
+ * row written is the one mla_kv_write would write with rope_bf16 = mla_rope(k_pe). The
+ * queries of every row are turned, those of dropped rows too.
+ *
+ *   kv, slot_idx, latent_bf16, n_rows, reserved_slot   as mla_kv_write; row_bytes 656
+ *   k_pe_bf16     bf16 [n_rows, 64] row-major, device, 4-byte aligned
+ *   pos, pos_stride, rope                              as mla_rope
+ *   q_bf16, q_out_bf16 and their strides               as x and y of mla_rope, with
+ *                 n_heads heads; both NULL: no queries
+ * Precondition as mla_kv_write: no two rows of one call name the same non-reserved slot.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* latent_bf16, const void* k_pe_bf16,
+                      int64_t n_rows, int64_t reserved_slot, const int32_t* pos, int64_t pos_stride,
+                      const mla_rope_t* rope, const void* q_bf16, int64_t q_row, int64_t q_head, void* q_out_bf16,
+                      int64_t q_out_row, int64_t q_out_head, int n_heads, void* stream);
+
+/*
+ * mla_chunk_attention - dense attention of a chunk of new tokens over the paged cache,
+ * for a ragged batch: prefill chunks, single decode tokens, drafts to verify, mixed.
+ *
+ * Sequence s has the tokens q_start[s] .. q_start[s+1]-1 of q and kv_len[s] positions in
+ * the cache, its own new tokens included (write them first). Position p stands for the
+ * slot block_table[s, p / page_size] * page_size + p % page_size. Token i of its n
+ * attends the positions p <= kv_len[s] - n + i (all kv_len[s] when causal is 0) that
+ * are present; a position in a page with a negative table entry, the reserved slot 0,
+ * or a slot >= num_slots (flagged MLA_ERR_DECODE_INDEX_RANGE) is absent: never read. Over those
+ * positions out and lse are what mla_sparse_decode computes. A token that attends nothing
+ * gets out = 0 and lse = -inf. A row that holds a value that is not finite (a NaN code, a NaN
+ * or infinite scale or RoPE value) makes out and lse NaN for exactly the tokens that
+ * attend it. Tokens outside every sequence keep their out and lse. The result does not
+ * depend on what slot 0, absent pages or positions past kv_len hold.
+ *
+ *   q_bf16       bf16 [T, H, d_qk] row-major, device, 16-byte aligned; d_qk 576 or 512
+ *   T, H         tokens (>= 0) and heads (1..128); T * H at most 2^29
+ *   kv           the cache (row_bytes 656, or 528 with d_qk 512)
+ *   q_start      int32 [n_seq + 1], device, nondecreasing within [0, T]; a sequence for
+ *                which it is not is skipped and flagged MLA_ERR_CHUNK_RANGE
+ *   kv_len       int32 [n_seq], device; a negative one counts as 0; positions past
+ *                max_pages * page_size are absent and flagged MLA_ERR_CHUNK_RANGE
+ *   block_table  int32 [n_seq, max_pages], device
+ *   out_bf16     bf16 [T, H, 512], device, 16-byte aligned;  lse  fp32 [T, H], device
+ *   workspace    device scratch of mla_chunk_attention_workspace_bytes(T, H, n_seq) bytes,
+ *                16-byte aligned; its contents on entry do not matter. Calls that may
+ *                overlap (other streams, graphs replayed at once) need their own.
+ * The lengths are read on the device: a captured call serves any lengths within the
+ * arrays' sizes. Launched with programmatic stream serialization like the decode.
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED, MLA_ENOWORKSPACE or MLA_ECUDA.
+ */
+size_t mla_chunk_attention_workspace_bytes(int T, int H, int n_seq);
+int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
+                        const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages, int page_size,
+                        int causal, float sm_scale, void* out_bf16, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Pages of a cache. Page p is the slots p * page_size .. (p + 1) * page_size - 1; pages
+ * are counted in `refcount` (int32 [num_pages], device): how many block-table rows
+ * hold each, 0 for a free page. Page 0 contains the reserved slot: it is never handed
+ * out, freed, moved or counted. num_pages is at most num_slots / page_size. Block
+ * tables are int32 [n_seq, max_pages], -1 where there is no page. All results are
+ * independent of the order in which CTAs run. Range violations are dropped and flagged
+ * (MLA_ERR_PAGE_RANGE). Launched with programmatic stream serialization.
+ *
+ * mla_page_copy - page src[i] of src_kv to page dst[i] of dst_kv, i < n (int32, device);
+ * the caches may be one. A negative src or a dst <= 0 is skipped. Precondition: no
+ * page is a dst twice, and within one cache no dst is also a src.
+ */
+int mla_page_copy(mla_kv_cache_t dst_kv, mla_kv_cache_t src_kv, int page_size, const int32_t* dst, const int32_t* src,
+                  int64_t n, void* stream);
+
+/*
+ * mla_page_free - rows[i] (int32 [n], device) of the table let go of their pages: each
+ * count drops by one (one that was 0 stays 0 and is flagged MLA_ERR_PAGE_COUNT) and the
+ * row becomes -1. A negative row is skipped; a row listed twice is freed once.
+ */
+int mla_page_free(int32_t* refcount, int num_pages, int32_t* block_table, int n_seq, int max_pages,
+                  const int32_t* rows, int n, void* stream);
+
+/*
+ * mla_page_fork - row child[i] of the table becomes a copy of row parent[i] as far as
+ * its first lens[i] positions, i < n (int32, device): whole pages are shared (their
+ * counts rise by one), a last page that is not full is copied, its rows up to
+ * lens[i], to a free page; the row's other entries become -1. Free pages are taken in
+ * ascending order, fork by fork; when none is left the entry stays -1 (the rows are then
+ * absent for the child) and MLA_ERR_POOL_EMPTY is set. The child's row is overwritten:
+ * free it first if it holds pages. A negative parent or child skips the fork; parent ==
+ * child or a length past the table is dropped and flagged. A parent may be forked
+ * many times in a call. Preconditions: every page that a parent holds is counted, no
+ * child is listed twice, and none is a parent of the same call.
+ */
+int mla_page_fork(mla_kv_cache_t kv, int page_size, int32_t* refcount, int num_pages, int32_t* block_table, int n_seq,
+                  int max_pages, const int32_t* parent, const int32_t* child, const int32_t* lens, int n,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_page_compact - moves the live pages (count > 0) to pages 1 .. live: a live page
+ * above that range goes to the vacant page of the same rank (both in ascending order),
+ * the others stay. refcount_out and table_out receive the counts and the table that go
+ * with it (they may be refcount and block_table themselves); an entry that names a free page
+ * becomes -1. page_map (int32 [num_pages], may be NULL) receives where each page went: its
+ * new index, -1 for a free page, 0 for page 0.
+ */
+int mla_page_compact(mla_kv_cache_t kv, int page_size, const int32_t* refcount, int32_t* refcount_out, int num_pages,
+                     const int32_t* block_table, int32_t* table_out, int n_seq, int max_pages, int32_t* page_map,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device scratch (16-byte aligned) for mla_page_fork of up to n_forks forks, and
+ * for mla_page_compact, of a pool of num_pages pages. */
+size_t mla_page_workspace_bytes(int num_pages, int n_forks);
 
 /*
  * mla_get_error - read and clear the device error word of the current device
