@@ -61,6 +61,12 @@ __device__ __forceinline__ float quad_max(float v) {
 // at most tiles + wave, and those of split tiles (each more than C, so cut into less
 // than 2 x its length / C) at most 2 wave: the sizes of the grid and the workspace.
 constexpr int kPlanThreads = 512;
+constexpr int kPlanTries = 16;
+
+// The k-th piece length tried: C, then an eighth of it more each time.
+__device__ __forceinline__ int64_t try_piece(int64_t C, int k, int align) {
+    return (C + C * k / 8 + align - 1) / align * align;
+}
 
 __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* buf) {
 #pragma unroll
@@ -121,6 +127,7 @@ __device__ __forceinline__ int plan_scan_max(int v, int& all, int64_t* buf) {
 __global__ void __launch_bounds__(kPlanThreads)
 chunk_plan_kernel(const ChunkArgs a) {
     __shared__ int64_t buf[kPlanThreads / 32];
+    __shared__ int tries[kPlanThreads / 32][kPlanTries + 1];
     pdl_wait();
     pdl_launch_dependents();
     // A sequence is taken if its start is not below any earlier one, nor its end below its
@@ -146,6 +153,43 @@ chunk_plan_kernel(const ChunkArgs a) {
     work = plan_sum(work, buf);
     int64_t C = (work + a.wave - 1) / a.wave;
     C = C < a.min_piece ? a.min_piece : (C + a.align - 1) / a.align * a.align;
+    // A few longer C as well: the one for which waves of pieces x longest piece is least
+    // (64 sequences of 1..16,384 positions make 336 pieces of W / 304, two waves, but 304
+    // of a slightly longer one).
+    int pieces_of[kPlanTries], longest = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanTries; ++k) pieces_of[k] = 0;
+    for (int s = threadIdx.x; s < a.n_seq; s += kPlanThreads) {
+        if (a.split[s] == 0) continue;
+        const Seq q = load_seq(a, s);
+        const int tiles = static_cast<int>((static_cast<int64_t>(q.n) * a.H + a.tile_rows - 1) / a.tile_rows);
+        const int len = mean_limit(a, q);
+        longest = max(longest, len);
+#pragma unroll
+        for (int k = 0; k < kPlanTries; ++k) pieces_of[k] += tiles * max(1, static_cast<int>((len + try_piece(C, k, a.align) - 1) / try_piece(C, k, a.align)));
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanTries; ++k) pieces_of[k] = __reduce_add_sync(0xffffffffu, pieces_of[k]);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if ((threadIdx.x & 31) == 0) {
+        for (int k = 0; k < kPlanTries; ++k) tries[threadIdx.x >> 5][k] = pieces_of[k];
+        tries[threadIdx.x >> 5][kPlanTries] = longest;
+    }
+    __syncthreads();
+    longest = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) longest = max(longest, tries[w][kPlanTries]);
+    int64_t best = INT64_MAX, best_C = C;
+    for (int k = 0; k < kPlanTries; ++k) {
+        int64_t n = 0;
+        for (int w = 0; w < kPlanThreads / 32; ++w) n += tries[w][k];
+        const int64_t c = try_piece(C, k, a.align);
+        const int64_t cost = (n + a.wave - 1) / a.wave * (c < longest ? c : longest);
+        if (cost < best) {
+            best = cost;
+            best_C = c;
+        }
+    }
+    C = best_C;
     int p_base = 0, q_base = 0, r_base = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
         const int s = s0 + threadIdx.x;
@@ -735,12 +779,17 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// Two CTAs of the small-tile kernel fit an SM. A piece shorter than kMinPiece saves
-// less than its partial and its share of the merge cost.
+// Two CTAs of the kernel for few rows fit an SM, one of the kernel for many. A piece
+// shorter than the minimum saves less than its partial and its share of the merge cost.
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPiece = 128;
+constexpr int kLargeMinPiece = 256;
+
+// Query rows per sequence, on average, from which the kernel for many rows is taken.
+constexpr int kLargeFrom = 48;
 
 struct Sizes {
+    bool large;
     int tile_rows, wave;
     int64_t max_pieces;
     size_t parts_o, parts_lse, prefix;     // bytes
@@ -749,9 +798,11 @@ struct Sizes {
 
 Sizes sizes_of(int T, int H, int n_seq, int sms) {
     Sizes z;
-    z.tile_rows = kSmallRows;
-    z.wave = kCtasPerSm * sms;
-    z.max_pieces = static_cast<int64_t>(T) * H / z.tile_rows + (n_seq < T ? n_seq : T) + z.wave;
+    const int64_t rows_all = static_cast<int64_t>(T) * H;
+    z.large = rows_all >= static_cast<int64_t>(kLargeFrom) * n_seq;
+    z.tile_rows = z.large ? kLargeRows : kSmallRows;
+    z.wave = z.large ? sms : kCtasPerSm * sms;
+    z.max_pieces = rows_all / z.tile_rows + (n_seq < T ? n_seq : T) + z.wave;
     const size_t rows = 2 * static_cast<size_t>(z.wave) * z.tile_rows;
     z.parts_o = rows * kLatent * sizeof(float);
     z.parts_lse = align256(rows * sizeof(float));
@@ -793,7 +844,7 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     if (kv.row_bytes == MLA_ROW_BYTES_NOPE && d_qk != kLatent) return MLA_EUNSUPPORTED;   // no tail to read
     if (H < 1 || H > 128) return MLA_EUNSUPPORTED;
     if (T == 0 || n_seq == 0) return MLA_OK;
-    if (static_cast<int64_t>(T) * H > INT_MAX / 4) return MLA_EUNSUPPORTED;
+    if (static_cast<int64_t>(T) * H > INT_MAX / 4 || kv.num_slots > INT_MAX) return MLA_EUNSUPPORTED;
     if (q_bf16 == nullptr || out_bf16 == nullptr || lse == nullptr || q_start == nullptr || kv_len == nullptr ||
         (max_pages > 0 && (block_table == nullptr || kv.data == nullptr)))
         return MLA_EINVAL;
@@ -830,9 +881,9 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     a.sm_scale_log2 = sm_scale * kLog2e;
     a.err = err;
     a.tile_rows = z.tile_rows;
-    a.align = kNB;
+    a.align = z.large ? kLargeBlock : kNB;
     a.wave = z.wave;
-    a.min_piece = kMinPiece;
+    a.min_piece = z.large ? kLargeMinPiece : kMinPiece;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(w);
     w += z.parts_o;
@@ -844,8 +895,9 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
         w += z.prefix;
     }
     if (!launch(chunk_plan_kernel, 1, kPlanThreads, 0, stream, a)) return MLA_ECUDA;
-    const bool ok = rope ? launch(mla_chunk_small_kernel<true>, z.max_pieces, kThreads, kSmemTotal, stream, a)
-                         : launch(mla_chunk_small_kernel<false>, z.max_pieces, kThreads, kSmemTotal, stream, a);
+    const bool ok = z.large ? mla_host::launch_chunk_large(a, z.max_pieces, rope, stream)
+                    : rope  ? launch(mla_chunk_small_kernel<true>, z.max_pieces, kThreads, kSmemTotal, stream, a)
+                            : launch(mla_chunk_small_kernel<false>, z.max_pieces, kThreads, kSmemTotal, stream, a);
     if (!ok) return MLA_ECUDA;
     // Rows of split tiles: at most those of 2 wave pieces, in pairs at least.
     int64_t merge = static_cast<int64_t>(z.wave) * z.tile_rows;

@@ -9,6 +9,8 @@ namespace mla_chunk {
 using namespace mla;
 
 constexpr int kSmallRows = 16;         // query rows per tile of the kernel for few rows
+constexpr int kLargeRows = 64;         // of the kernel for many rows
+constexpr int kLargeBlock = 128;       // positions per block there
 
 struct ChunkArgs {
     const __nv_bfloat16* q;
@@ -130,3 +132,8 @@ __device__ __forceinline__ int64_t chunk_slot(const ChunkArgs& a, const int32_t*
 }
 
 }  // namespace mla_chunk
+
+namespace mla_host {
+// Launches the kernel for many query rows (grid bound `pieces`), false on a CUDA error.
+bool launch_chunk_large(const mla_chunk::ChunkArgs& a, int64_t pieces, bool rope, void* stream);
+}

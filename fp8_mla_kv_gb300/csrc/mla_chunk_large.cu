@@ -1,0 +1,829 @@
+// mla_chunk_attention, the kernel for many query rows: tiles of 64 (token, head) rows on
+// tcgen05, where the tensor cores are what costs.
+//
+// Everything is turned: positions are the rows of the MMAs (M = 128 of them a block) and
+// query rows the columns (N = 64), so that O^T of 512 dims x 64 rows fills half of the
+// tensor memory and one CTA holds a whole tile, and so that what belongs to a position
+// (its four tile scales, whether it is present) is one thread's, a register instead of
+// a value broadcast from shared memory for every score: folding the partials of an
+// untransposed S that way took 1,536 of the SM's shared-memory cycles per 64 positions.
+//
+// Per block of 128 positions:
+//   QK   five products (the latent tiles, K = 128, and RoPE, 64): A = the positions'
+//        codes as exact f16, put into tensor memory by the converting warps, B = q
+//        (exact in f16 after an exponent-only shift) in shared memory. Each partial is
+//        exact before fp32 accumulation and goes to an S slot of its own; the softmax
+//        warps fold them with the fp32 tile scales as they come. (A K rounded to f16 with
+//        its scale in it needs one accumulator but moves a score near 20 by 3.5e-3.)
+//   P    thread = position x 32 query rows. The exp2 offset of a row is an earlier maximum:
+//        it moves only when a score is more than kRescaleSlack above it, which one
+//        vote per block shows; only then maxima over the positions are taken.
+//   PV   O^T_t += V_t^T P^T: V = code x scale / sigma as f16 in shared memory (sigma_t: a
+//        scale near the largest of tile t so far), read MN-major; P as f16, MN-major
+//        too. Roundings: P, scale / sigma and their product, half a step of 2^-11 each.
+// The order of the dims within QK is the one in which a thread that loaded 16 codes of a
+// row can store them to tensor memory; q is laid out to match.
+//
+// Roles: warps 0-7 softmax (lane quarter w % 4, query rows 32 (w / 4) ..), 8-11 turn cache
+// rows into operands (straight from global memory, the next tile's loads in flight),
+// 12 issues the MMAs, 13 walks the block table ahead of them: row addresses, scales,
+// sigma, prefetches into L2.
+#include <cfloat>
+#include <climits>
+#include <cmath>
+
+#include "mla_chunk.cuh"
+
+namespace {
+
+using namespace mla;
+using namespace mla_chunk;
+
+constexpr int kN = kLargeBlock;              // positions per block (M of the MMAs)
+constexpr int kRows = kLargeRows;            // query rows per tile (N of the MMAs)
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kMetaWarp = kMmaWarp + 1;
+constexpr int kThreads = 16 * 32;            // four warpgroups (two warps idle)
+// Registers per thread: 65,536 are launched as 128 each and dealt out again.
+constexpr int kSoftRegs = 160, kConvRegs = 128, kAuxRegs = 64;
+static_assert(2 * kSoftRegs + kConvRegs + kAuxRegs <= 4 * 128, "registers");
+constexpr int kCols = kRows / 2;             // query rows per softmax warp
+constexpr int kMeta = 2;                     // blocks the meta warp may be ahead
+constexpr float kRescaleSlack = 8.0f;        // log2 units: p <= 2^8
+constexpr float kSigmaSlack = 64.0f;         // scale / sigma <= 2^6: code x scale / sigma < 2^15 in f16
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Shared memory (the base is 1024-byte aligned). Operand tiles are rows of 64 16-bit
+// values (128 B) in 8-row groups of 1 KB, 16-byte unit u of row r at unit u ^ (r & 7);
+// wider tiles are sequences of such 64-column chunks.
+constexpr int kQChunk = kRows * 128;                       // 8 KB
+constexpr int kOffQ = 0;                                   // 8 latent chunks and RoPE
+constexpr int kVChunk = kN * 128;                          // 16 KB
+constexpr int kOffV = kOffQ + 9 * kQChunk;                 // 4 tiles of 128 positions x 128 dims
+constexpr int kOffP = kOffV + 8 * kVChunk;                 // 128 positions x 64 query rows
+constexpr int kOffMeta = kOffP + kN * 128;
+struct __align__(16) Meta {
+    float sc[4][kN];                         // tile scales; 0 where absent
+    uint16_t rs[4][kN];                      // scale / sigma, f16
+    int32_t slot[kN];                        // -1 where absent (a cache that fits a GPU has less than 2^31 rows)
+    float f[4];                              // what O^T of each tile has to be multiplied by (sigma moved)
+    float sigma[4];
+    uint8_t state[kN];                       // 0 absent, 1 present, 2 a value that is not finite
+};
+constexpr int kOffRow = kOffMeta + kMeta * static_cast<int>(sizeof(Meta));
+struct __align__(16) RowData {               // per query row
+    float m[kRows];                          // exp2 offset (log2 units)
+    float alpha[kRows];                      // what O^T and l are multiplied by when it moves; at the end 1 / l
+    float shift[kRows];                      // undoes the exponent shift of q
+    int lim[kRows];                          // positions it attends, counted from the piece's first
+    int unseen[kRows];                       // attends something, but nothing so far
+    float wmax[4][kRows];                    // by lane quarter: maxima; at the end sums of p
+    int any_unseen[2], pad[2];
+};
+constexpr int kOffBars = kOffRow + static_cast<int>(sizeof(RowData));
+constexpr int kNumBars = 32;
+constexpr int kOffMisc = kOffBars + kNumBars * 8;
+constexpr int kSmemTotal = kOffMisc + 16;
+static_assert(kSmemTotal <= 232448, "shared memory");
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColA = 4 * kRows, kColS = kColA + 128; // O^T tiles, two A slots of 64, two S slots of 64
+
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16 instruction descriptor: fp32 D, A and B format (0 f16, 1 bf16), majors, M, N.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t fmt, bool a_mn, bool b_mn, uint32_t m, uint32_t n) {
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+constexpr uint32_t kIdQK = idesc_f16(0, false, false, kN, kRows);     // S^T = K_t . q_t^T
+constexpr uint32_t kIdQR = idesc_f16(1, false, false, kN, kRows);     // RoPE (bf16)
+constexpr uint32_t kIdPV = idesc_f16(0, true, true, kTile, kRows);    // O^T_t += V_t^T . P^T
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)) : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)) : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Waits for this warp's tcgen05.ld; the registers pass through, so that no use of them
+// is scheduled before it.
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 lanes x 32 bits, 32 columns: thread t gets lane t, columns c .. c + 31.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+           "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+           "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16 lanes x 256 bits, 8 times (64 columns) or 4 (32): thread t gives lanes t / 4 and t / 4 + 8,
+// columns 8j + 2 (t % 4) + {0, 1} from r[4j], r[4j+1] (lane t / 4) and r[4j+2], r[4j+3].
+__device__ __forceinline__ void tmem_st_16x256_x8(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+           "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+           "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256_x4(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Byte offset of 16-byte unit u of row r in a swizzled tile of `rows` rows.
+__device__ __forceinline__ uint32_t swz(int rows, int r, int u) {
+    return static_cast<uint32_t>((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
+// A bounded wait that also ends as soon as another role has given up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (int i = 0;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15) == 15) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > kWaitCycles) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+// The same by a whole warp, with one answer for it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+template <bool kRopeOn>
+__global__ void __launch_bounds__(kThreads, 1)
+mla_chunk_large_kernel(const ChunkArgs args) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Meta* meta = reinterpret_cast<Meta*>(smem + kOffMeta);
+    RowData& rd = *reinterpret_cast<RowData*>(smem + kOffRow);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
+    uint64_t* afull = bars;            // [2] A slot written (4 converting warps)
+    uint64_t* afree = bars + 2;        // [2] its QK is done (commit)
+    uint64_t* sfull = bars + 4;        // [2] S slot written (commit)
+    uint64_t* sfree = bars + 6;        // [2] S slot read (8 softmax warps)
+    uint64_t* vfull = bars + 8;        // [4] V tile written (4 converting warps)
+    uint64_t* vfree = bars + 12;       // [4] its PV is done (commit)
+    uint64_t* pfull = bars + 16;       // P written, O^T corrected (8 softmax warps)
+    uint64_t* pvdone = bars + 17;      // PV of a block done (commit)
+    uint64_t* mfull = bars + 18;       // [2] meta stage written (meta warp)
+    uint64_t* mfree = bars + 21;       // [2] meta stage read (8 softmax, 4 converting warps)
+    uint64_t* cdone = bars + 24;       // [2] a block's rows converted: its states are final
+    uint64_t* fin = bars + 27;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const Piece pc = find_piece(args, static_cast<int>(blockIdx.x), lane);
+    if (pc.seq < 0) return;
+    if ((smem_u32(smem) & 1023u) != 0u) {      // the operand layout's phase would be off: no result
+        if (threadIdx.x == 0) atomicOr(args.err, MLA_ERR_PIPELINE_TIMEOUT);
+        return;
+    }
+    const int n_keys = pc.k1 - pc.k0;
+    const int nblk = (n_keys + kN - 1) / kN;
+    const int n_rows = min(kRows, pc.rows - pc.row0);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&afull[i], kConvWarps);
+            mbar_init(&afree[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sfree[i], kSoftWarps);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&vfull[i], kConvWarps);
+            mbar_init(&vfree[i], 1);
+        }
+        mbar_init(pfull, kSoftWarps);
+        mbar_init(pvdone, 1);
+        for (int i = 0; i < kMeta; ++i) {
+            mbar_init(&mfull[i], 1);
+            mbar_init(&mfree[i], kSoftWarps + kConvWarps);
+            mbar_init(&cdone[i], kConvWarps);
+        }
+        mbar_init(fin, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // ---- q of the tile's rows as operand tiles: a warp per row, lane l the 16-byte units
+    // l and l + 32 of the latent and, l < 8, unit l of RoPE ----
+    for (int r = warp; r < kRows; r += kThreads / 32) {
+        uint4 v[3];
+        v[0] = v[1] = v[2] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n_rows) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(args.q + (pc.grow0 + pc.row0 + r) * args.d_qk);
+            v[0] = ld_nc_v4(src + 16 * lane);
+            v[1] = ld_nc_v4(src + 512 + 16 * lane);
+            if (kRopeOn && lane < 8) v[2] = ld_nc_v4(src + 1024 + 16 * lane);
+        }
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        // Exponent-only shift so that |q| < 2^15 in f16, undone on the scores.
+        int e = 0;
+        if (mx <= FLT_MAX) frexpf(mx, &e);
+        const int k = e > 15 ? e - 15 : 0;
+        const float down = ldexpf(1.0f, -k);
+        if (lane == 0) {
+            const int lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
+            rd.shift[r] = ldexpf(1.0f, k);
+            rd.lim[r] = lim;
+            rd.unseen[r] = lim > 0;
+            rd.m[r] = 0.0f;
+        }
+        // Operand position of dim d of a tile: a converting thread's f16 pair m of 16 codes
+        // 64 p + 16 c .. goes to tensor-memory column 8 (m / 2) + 2 c + m % 2, so the 8 dims of
+        // a unit are two runs of 4 positions, 16 apart.
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
+            const int u = lane + 32 * i, ut = u & 15;
+            const int at = 16 * (4 * (ut >> 3) + 2 * (ut & 1)) + 4 * ((ut >> 1) & 3);
+            uint8_t* q = smem + kOffQ + 2 * (u >> 4) * kQChunk;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int pos = at + 16 * j;
+                *reinterpret_cast<uint2*>(q + swz(kRows, r, pos >> 3) + ((pos & 4) << 1)) = make_uint2(h[2 * j], h[2 * j + 1]);
+            }
+        }
+        if (kRopeOn && lane < 8) {
+            const uint32_t w[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = pack_bf16x2(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
+            const int at = 16 * (2 * (lane >> 2)) + 4 * (lane & 3);
+            uint8_t* q = smem + kOffQ + 8 * kQChunk;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int pos = at + 16 * j;
+                *reinterpret_cast<uint2*>(q + swz(kRows, r, pos >> 3) + ((pos & 4) << 1)) = make_uint2(h[2 * j], h[2 * j + 1]);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    constexpr int kGroups = kRopeOn ? 5 : 4;          // S partials per block: [RoPE,] tiles 0 .. 3
+
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
+        // ---- softmax: thread = position 32 quarter + lane, query rows c0 .. c0 + 31 ----
+        const int quarter = warp & 3, half = warp >> 2;
+        const int key = 32 * quarter + lane;
+        const int c0 = kCols * half;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        // what is uniform over this half's query rows
+        const int my_lim = rd.lim[c0 + lane];
+        const int lim_min = __reduce_min_sync(0xffffffffu, my_lim);
+        const bool shifted = __any_sync(0xffffffffu, rd.shift[c0 + lane] != 1.0f);
+        bool unseen = true;                            // some row has seen nothing yet: take maxima
+        float l[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) l[c] = 0.0f;
+        float sig[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        bool ok = true;
+        int g = 0;
+        for (int b = 0; b < nblk && ok; ++b) {
+            const Meta& mt = meta[b % kMeta];
+            // A wait that ran out only skips work up to the vote, which all four warps take.
+            ok = warp_wait(&mfull[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
+            uint64_t s[kCols / 2];
+#pragma unroll
+            for (int j = 0; j < kCols / 2; ++j) s[j] = 0ull;
+            // (loops over the groups and tiles are not unrolled anywhere: the roles' code, taken
+            // together, has to stay in the instruction cache)
+#pragma unroll 1
+            for (int t = 4 - kGroups; t < 4; ++t, ++g) {
+                const int slot = g & 1;
+                ok = ok && warp_wait(&sfull[slot], static_cast<uint32_t>((g >> 1) & 1), abort_flag);
+                if (!ok) break;
+                tc_after();
+                uint32_t v[kCols];
+                tmem_ld32(lane_base + kColS + kRows * slot + c0, v);
+                const uint32_t f = t < 0 ? 0x3f800000u : __float_as_uint(mt.sc[t][key]);
+                const uint64_t ff = two(f, f);
+                tc_wait_ld(v);
+                tc_before();
+                warp_arrive(&sfree[slot]);
+#pragma unroll
+                for (int j = 0; j < kCols / 2; ++j) s[j] = fma2(two(v[2 * j], v[2 * j + 1]), ff, s[j]);
+            }
+            ok = ok && warp_wait(&cdone[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
+            float d[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols / 2; ++j) {
+                d[2 * j] = lo_of(s[j]) * args.sm_scale_log2;
+                d[2 * j + 1] = hi_of(s[j]) * args.sm_scale_log2;
+            }
+            if (shifted) {
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) d[c] *= rd.shift[c0 + c];
+            }
+            const int state = mt.state[key];
+            if (__any_sync(0xffffffffu, state != 1) || kN * (b + 1) > lim_min) {
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    if (state == 2) d[c] = __int_as_float(0x7FC00000);
+                    if (state == 0 || kN * b + key >= rd.lim[c0 + c]) d[c] = -INFINITY;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                d[c] -= rd.m[c0 + c];
+                top = fmaxf(top, d[c]);
+            }
+            // P of the block before has been read, and O^T is complete up to it.
+            if (b > 0) {
+                ok = ok && warp_wait(pvdone, static_cast<uint32_t>((b - 1) & 1), abort_flag);
+                tc_after();
+            }
+            const bool moved = bar_sync_or(1 + half, 128, unseen || top > kRescaleSlack || !ok);
+            const float f0 = mt.f[0], f1 = mt.f[1], f2 = mt.f[2], f3 = mt.f[3];
+            const bool sigma_moved = b > 0 && (f0 != 1.0f || f1 != 1.0f || f2 != 1.0f || f3 != 1.0f);
+            if (moved) {
+                // Rare after the first block: maxima over the positions, new offsets for the rows
+                // whose scores ran ahead, l and O^T rescaled.
+                if (bar_sync_or(1 + half, 128, !ok)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    float v = d[c];
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+                    if (lane == c) rd.wmax[quarter][c0 + c] = v;
+                }
+                bar_sync_or(1 + half, 128, false);
+                if (quarter == 0) {
+                    const int c = c0 + lane;
+                    const float up = fmaxf(fmaxf(rd.wmax[0][c], rd.wmax[1][c]), fmaxf(rd.wmax[2][c], rd.wmax[3][c]));
+                    const bool first = rd.unseen[c] != 0 && up > -INFINITY;
+                    const bool move = first || up > kRescaleSlack;
+                    rd.alpha[c] = move ? (first ? 0.0f : ex2_approx(-up)) : 1.0f;
+                    if (first) rd.unseen[c] = 0;
+                    rd.wmax[0][c] = move ? up : 0.0f;      // by how much the offset moves
+                    if (move) rd.m[c] += up;
+                    const bool left = __any_sync(0xffffffffu, rd.unseen[c] != 0);
+                    if (lane == 0) rd.any_unseen[half] = left;
+                }
+                bar_sync_or(1 + half, 128, false);
+                unseen = rd.any_unseen[half] != 0;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    d[c] -= rd.wmax[0][c0 + c];
+                    l[c] *= rd.alpha[c0 + c];
+                }
+            }
+            if (b > 0 && (moved || sigma_moved)) {
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    uint32_t o[kCols];
+                    tmem_ld32(lane_base + kRows * t + c0, o);
+                    tc_wait_ld(o);
+                    const float f = t == 0 ? f0 : t == 1 ? f1 : t == 2 ? f2 : f3;
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+                        o[c] = __float_as_uint(__uint_as_float(o[c]) * (moved ? f * rd.alpha[c0 + c] : f));
+                    tmem_st32(lane_base + kRows * t + c0, o);
+                }
+                tc_wait_st();
+            }
+            uint8_t* prow = smem + kOffP + key * 128;
+#pragma unroll
+            for (int u = 0; u < kCols / 8; ++u) {
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float p0 = ex2_approx(d[8 * u + 2 * k]), p1 = ex2_approx(d[8 * u + 2 * k + 1]);
+                    l[8 * u + 2 * k] += p0;
+                    l[8 * u + 2 * k + 1] += p1;
+                    h[k] = pack_f16x2(p0, p1);
+                }
+                *reinterpret_cast<uint4*>(prow + (((4 * half + u) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) sig[t] = mt.sigma[t];
+            fence_proxy_async_smem();
+            tc_before();
+            warp_arrive(pfull);
+            warp_arrive(&mfree[b % kMeta]);
+        }
+        // ---- epilogue: l over the positions, then O^T * sigma / l ----
+        if (ok && nblk > 0) {
+            ok = warp_wait(pvdone, static_cast<uint32_t>((nblk - 1) & 1), abort_flag);
+            tc_after();
+        }
+        if (!bar_sync_or(1 + half, 128, !ok)) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                float v = l[c];
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+                if (lane == c) rd.wmax[quarter][c0 + c] = v;
+            }
+            bar_sync_or(1 + half, 128, false);
+            if (quarter == 0) {
+                const int c = c0 + lane;
+                const float sum = (rd.wmax[0][c] + rd.wmax[1][c]) + (rd.wmax[2][c] + rd.wmax[3][c]);
+                // 0: nothing attended; NaN: an attended row holds a value that is not finite
+                const float kNaN = __int_as_float(0x7FC00000);
+                rd.alpha[c] = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : kNaN);
+                const float lse = sum > 0.0f ? (rd.m[c] + log2f(sum)) * kLn2 : (sum == 0.0f ? -INFINITY : kNaN);
+                if (c < n_rows) {
+                    if (pc.part < 0) args.lse[pc.grow0 + pc.row0 + c] = lse;
+                    else args.part_lse[static_cast<int64_t>(pc.part) * kRows + c] = lse;
+                }
+            }
+            bar_sync_or(1 + half, 128, false);
+#pragma unroll 1
+            for (int t = 0; t < 4; ++t) {
+                uint32_t o[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) o[c] = 0u;
+                if (nblk > 0) {
+                    tmem_ld32(lane_base + kRows * t + c0, o);
+                    tc_wait_ld(o);
+                }
+                const float f = t == 0 ? sig[0] : t == 1 ? sig[1] : t == 2 ? sig[2] : sig[3];
+                const int dim = kTile * t + key;           // here the lane is a dim
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    if (c0 + c >= n_rows) break;
+                    const float x = __uint_as_float(o[c]) * (f * rd.alpha[c0 + c]);
+                    if (pc.part < 0)
+                        args.out[(pc.grow0 + pc.row0 + c0 + c) * kLatent + dim] = __float2bfloat16_rn(x);
+                    else
+                        args.part_o[(static_cast<int64_t>(pc.part) * kRows + c0 + c) * kLatent + dim] = x;
+                }
+            }
+            tc_before();
+        }
+    } else if (warp < kMmaWarp) {
+        // ---- conversion: lane (row r0 + 8 i of its quarter, 16-byte pieces c of each 64) ----
+        const int quarter = warp & 3;
+        const int c = lane & 3;
+        const int r0 = 32 * quarter + (lane >> 2);
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        int slot[4];                                   // of rows r0 + 8 i
+        uint4 v[4][2];
+        bool ok = true;
+        int g = 0;
+        auto rows_of = [&](int b) {
+            ok = ok && warp_wait(&mfull[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
+            if (!ok) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) slot[i] = meta[b % kMeta].slot[r0 + 8 * i];
+        };
+        auto load = [&](int t, int hh) {               // rows r0 + 16 hh, + 8 of latent tile t; -1: RoPE
+            const int off = (t < 0 ? kTailOff : 128 * t) + 16 * c;
+#pragma unroll
+            for (int i = 2 * hh; i < 2 * hh + 2; ++i) {
+                const uint8_t* row = args.cache + slot[i] * args.row_bytes + off;
+                v[i][0] = slot[i] >= 0 ? ld_nc_v4(row) : make_uint4(0u, 0u, 0u, 0u);
+                v[i][1] = slot[i] >= 0 ? ld_nc_v4(row + 64) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        constexpr int kFirst = kRopeOn ? -1 : 0;
+        if (nblk > 0) rows_of(0);
+        if (nblk > 0 && ok) {
+            load(kFirst, 0);
+            load(kFirst, 1);
+        }
+        for (int b = 0; b < nblk && ok; ++b) {
+            Meta& mt = meta[b % kMeta];
+#pragma unroll 1
+            for (int t = kFirst; t < 4; ++t, ++g) {
+                const bool more = t < 3 || b + 1 < nblk;
+                const int next = t < 3 ? t + 1 : kFirst;
+                if (t == 3 && more) rows_of(b + 1);
+                const int as = g & 1;
+                if (g >= 2) ok = ok && warp_wait(&afree[as], static_cast<uint32_t>(((g >> 1) - 1) & 1), abort_flag);
+                if (t >= 0 && b > 0) ok = ok && warp_wait(&vfree[t], static_cast<uint32_t>((b - 1) & 1), abort_flag);
+                if (!ok) break;
+                tc_after();
+                // An E4M3 NaN code (all exponent and mantissa bits) or a BF16 value that is not finite
+                // (all exponent bits) carries into the bit above when one is added to the field.
+                const uint32_t all = t < 0 ? 0x7f807f80u : 0x7f7f7f7fu, one = t < 0 ? 0x00800080u : 0x01010101u;
+                const uint32_t carry = t < 0 ? 0x80008000u : 0x80808080u;
+                const uint32_t a = lane_base + kColA + 64 * as;
+                uint8_t* tile = smem + kOffV + 2 * t * kVChunk;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t w[2][16];                  // 16-bit pairs of rows r0 + 16 hh, + 8
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 2 * hh + e;
+                        uint32_t odd = 0u;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+                            odd |= ((v[i][p].x & all) + one) | ((v[i][p].y & all) + one) | ((v[i][p].z & all) + one) |
+                                   ((v[i][p].w & all) + one);
+                        if ((odd & carry) != 0u) {
+                            // Its row is marked (a query row that attends it gets NaN) and taken as 0 here: one
+                            // for which it is masked must not meet 0 * NaN in PV.
+                            mt.state[r0 + 8 * i] = 2;
+                            v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        if (t < 0) {
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                w[e][4 * p] = v[i][p].x; w[e][4 * p + 1] = v[i][p].y;
+                                w[e][4 * p + 2] = v[i][p].z; w[e][4 * p + 3] = v[i][p].w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                e4m3x4_to_f16x2x2(v[i][p].x, w[e][8 * p], w[e][8 * p + 1]);
+                                e4m3x4_to_f16x2x2(v[i][p].y, w[e][8 * p + 2], w[e][8 * p + 3]);
+                                e4m3x4_to_f16x2x2(v[i][p].z, w[e][8 * p + 4], w[e][8 * p + 5]);
+                                e4m3x4_to_f16x2x2(v[i][p].w, w[e][8 * p + 6], w[e][8 * p + 7]);
+                            }
+                        }
+                    }
+                    if (more && ok) load(next, hh);     // on its way until the next tile's turn
+                    uint32_t r[32];
+                    if (t < 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) r[4 * j + k] = w[k >> 1][2 * j + (k & 1)];
+                        tmem_st_16x256_x4(a + (static_cast<uint32_t>(16 * hh) << 16), r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) r[4 * j + k] = w[k >> 1][2 * j + (k & 1)];
+                        tmem_st_16x256_x8(a + (static_cast<uint32_t>(16 * hh) << 16), r);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int rr = r0 + 16 * hh + 8 * e;
+                            const uint32_t f = mt.rs[t][rr] * 0x10001u;
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u)
+                                    *reinterpret_cast<uint4*>(tile + swz(kN, rr, 8 * p + 2 * c + u)) =
+                                        make_uint4(hmul2(w[e][8 * p + 4 * u], f), hmul2(w[e][8 * p + 4 * u + 1], f),
+                                                   hmul2(w[e][8 * p + 4 * u + 2], f), hmul2(w[e][8 * p + 4 * u + 3], f));
+                        }
+                    }
+                }
+                tc_wait_st();
+                tc_before();
+                warp_arrive(&afull[as]);
+                if (t >= 0) {
+                    fence_proxy_async_smem();
+                    warp_arrive(&vfull[t]);
+                }
+            }
+            if (!ok) break;
+            warp_arrive(&cdone[b % kMeta]);
+            warp_arrive(&mfree[b % kMeta]);
+        }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kAuxRegs));
+    if (warp == kMmaWarp) {
+        // ---- MMAs, one thread: RoPE's QK of the next block runs beside this one's softmax ----
+        if (lane == 0) {
+            const uint32_t base = smem_u32(smem);
+            const uint64_t dq = sw128_desc(base + kOffQ, 16, 1024);
+            const uint64_t dp = sw128_desc(base + kOffP, 16, 1024);
+            bool ok = true;
+            int g = 0;
+            auto qk = [&](int t) {                     // latent tile t; -1: RoPE
+                const int slot = g & 1;
+                ok = ok && wait_or_abort(&afull[slot], static_cast<uint32_t>((g >> 1) & 1), abort_flag);
+                if (g >= 2) ok = ok && wait_or_abort(&sfree[slot], static_cast<uint32_t>(((g >> 1) - 1) & 1), abort_flag);
+                if (!ok) return;
+                tc_after();
+                const uint32_t d = tmem + kColS + kRows * slot, a = tmem + kColA + 64 * slot;
+                const uint64_t dt = dq + static_cast<uint64_t>(((t >= 0 ? 2 * t : 8) * kQChunk) >> 4);
+                const uint32_t id = t >= 0 ? kIdQK : kIdQR;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) umma_ts(d, a + 8 * ks, dt + static_cast<uint64_t>(2 * ks), id, ks > 0);
+                if (t >= 0) {
+#pragma unroll
+                    for (int ks = 4; ks < 8; ++ks)
+                        umma_ts(d, a + 8 * ks, dt + static_cast<uint64_t>((kQChunk >> 4) + 2 * (ks - 4)), id, true);
+                }
+                umma_commit(&sfull[slot]);
+                umma_commit(&afree[slot]);
+                ++g;
+            };
+            auto pv = [&](int b) {
+                ok = ok && wait_or_abort(pfull, static_cast<uint32_t>(b & 1), abort_flag);
+#pragma unroll 1
+                for (int t = 0; t < 4 && ok; ++t) {
+                    ok = wait_or_abort(&vfull[t], static_cast<uint32_t>(b & 1), abort_flag);
+                    if (!ok) return;
+                    tc_after();
+                    const uint64_t dv = sw128_desc(base + kOffV + 2 * t * kVChunk, kVChunk, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < kN / 16; ++ks)
+                        umma_ss(tmem + kRows * t, dv + static_cast<uint64_t>(ks * 128), dp + static_cast<uint64_t>(ks * 128), kIdPV,
+                                b > 0 || ks > 0);
+                    umma_commit(&vfree[t]);
+                }
+                umma_commit(pvdone);
+            };
+            if (kRopeOn && nblk > 0) qk(-1);
+            for (int b = 0; b < nblk && ok; ++b) {
+#pragma unroll 1
+                for (int t = 0; t < (kRopeOn && b + 1 < nblk ? 5 : 4) && ok; ++t) qk(t < 4 ? t : -1);
+                if (ok) pv(b);
+            }
+            // Every MMA issued has completed before tensor memory is freed.
+            umma_commit(fin);
+            (void)mbar_wait_bounded(fin, 0);
+        }
+        __syncwarp();
+    } else if (warp == kMetaWarp) {
+        // ---- meta: addresses, scales and sigma, up to kMeta blocks ahead ----
+        const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
+        float sigma[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int b = 0; b < nblk; ++b) {
+            Meta& mt = meta[b % kMeta];
+            const uint8_t* row[4];
+            int slot_of[4];
+            float sc[4][4];                            // [position][tile]
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = kN * b + 32 * i + lane;
+                const int64_t slot = j < n_keys ? chunk_slot(args, bt, pc.k0 + j) : -1;
+                row[i] = slot >= 0 ? args.cache + slot * args.row_bytes : nullptr;
+                slot_of[i] = static_cast<int>(slot);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) sc[i][t] = 0.0f;
+                if (row[i] != nullptr) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) prefetch_l2(row[i] + 128 * k);
+                    const uint4 u = ld_nc_v4(row[i] + kScaleOff);
+                    if (kRopeOn) prefetch_l2(row[i] + kTailOff + 64);
+                    sc[i][0] = __uint_as_float(u.x); sc[i][1] = __uint_as_float(u.y);
+                    sc[i][2] = __uint_as_float(u.z); sc[i][3] = __uint_as_float(u.w);
+                }
+            }
+            if (b >= kMeta && !warp_wait(&mfree[b % kMeta], static_cast<uint32_t>((b / kMeta - 1) & 1), abort_flag)) break;
+            float smax[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 32 * i + lane;
+                const bool odd = !(isfinite(sc[i][0]) && isfinite(sc[i][1]) && isfinite(sc[i][2]) && isfinite(sc[i][3]));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (odd) sc[i][t] = 0.0f;
+                    smax[t] = fmaxf(smax[t], fabsf(sc[i][t]));
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) mt.sc[t][j] = sc[i][t];
+                mt.slot[j] = row[i] == nullptr ? -1 : slot_of[i];
+                mt.state[j] = row[i] == nullptr ? 0 : odd ? 2 : 1;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) smax[t] = fmaxf(smax[t], __shfl_xor_sync(0xffffffffu, smax[t], d));
+                float f = 1.0f;
+                // the first scale that is not 0, and later ones far above it, set sigma
+                if (smax[t] > sigma[t] * kSigmaSlack) {
+                    f = sigma[t] / smax[t];
+                    sigma[t] = smax[t];
+                }
+                const float inv = sigma[t] > 0.0f ? 1.0f / sigma[t] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float r = inv <= FLT_MAX ? sc[i][t] * inv : __fdiv_rn(sc[i][t], sigma[t]);
+                    mt.rs[t][32 * i + lane] = static_cast<uint16_t>(pack_f16x2(r, 0.0f));
+                }
+                if (lane == 0) {
+                    mt.f[t] = f;
+                    mt.sigma[t] = sigma[t];
+                }
+            }
+            warp_arrive(&mfull[b % kMeta]);
+        }
+    }
+    }
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) atomicOr(args.err, MLA_ERR_PIPELINE_TIMEOUT);
+    if (warp == kMmaWarp) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+}  // namespace
+
+namespace mla_host {
+
+bool launch_chunk_large(const mla_chunk::ChunkArgs& a, int64_t pieces, bool rope, void* stream) {
+    const void* kernel = rope ? reinterpret_cast<const void*>(mla_chunk_large_kernel<true>)
+                              : reinterpret_cast<const void*>(mla_chunk_large_kernel<false>);
+    if (!max_dynamic_smem(kernel, kSmemTotal)) return false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemTotal;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return (rope ? cudaLaunchKernelEx(&cfg, mla_chunk_large_kernel<true>, a)
+                 : cudaLaunchKernelEx(&cfg, mla_chunk_large_kernel<false>, a)) == cudaSuccess &&
+           cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace mla_host
