@@ -24,10 +24,10 @@
 // The order of the dims within QK is the one in which a thread that loaded 16 codes of a
 // row can store them to tensor memory; q is laid out to match.
 //
-// Roles: warps 0-7 softmax (lane quarter w % 4, query rows 32 (w / 4) ..), 8-11 turn cache
-// rows into operands (straight from global memory, the next tile's loads in flight),
-// 12 issues the MMAs, 13 walks the block table ahead of them: row addresses, scales,
-// sigma, prefetches into L2.
+// Roles: warps 0-7 softmax (lane quarter w % 4, query rows 32 (w / 4) ..), 8-15 turn cache
+// rows into operands (straight from global memory, the next tile's loads in flight; each
+// warp 16 positions), 16 issues the MMAs, 17 walks the block table ahead of them: slots,
+// scales, sigma, prefetches into L2.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -41,13 +41,13 @@ using namespace mla_chunk;
 
 constexpr int kN = kLargeBlock;              // positions per block (M of the MMAs)
 constexpr int kRows = kLargeRows;            // query rows per tile (N of the MMAs)
-constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kMetaWarp = kMmaWarp + 1;
-constexpr int kThreads = 16 * 32;            // four warpgroups (two warps idle)
-// Registers per thread: 65,536 are launched as 128 each and dealt out again.
-constexpr int kSoftRegs = 160, kConvRegs = 128, kAuxRegs = 64;
-static_assert(2 * kSoftRegs + kConvRegs + kAuxRegs <= 4 * 128, "registers");
+constexpr int kThreads = 20 * 32;            // five warpgroups (two warps idle)
+// Registers per thread: launched as 96 each and dealt out again.
+constexpr int kSoftRegs = 128, kConvRegs = 80, kAuxRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * 96, "registers");
 constexpr int kCols = kRows / 2;             // query rows per softmax warp
 constexpr int kMeta = 2;                     // blocks the meta warp may be ahead
 constexpr float kRescaleSlack = 8.0f;        // log2 units: p <= 2^8
@@ -69,7 +69,7 @@ struct __align__(16) Meta {
     int32_t slot[kN];                        // -1 where absent (a cache that fits a GPU has less than 2^31 rows)
     float f[4];                              // what O^T of each tile has to be multiplied by (sigma moved)
     float sigma[4];
-    uint8_t state[kN];                       // 0 absent, 1 present, 2 a value that is not finite
+    uint8_t state[kN];                       // 0 absent, 1 present, 2 a scale that is not finite
 };
 constexpr int kOffRow = kOffMeta + kMeta * static_cast<int>(sizeof(Meta));
 struct __align__(16) RowData {               // per query row
@@ -155,6 +155,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tc_wait_ld16(uint32_t* r, uint32_t* q) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7]),
+                   "+r"(q[8]), "+r"(q[9]), "+r"(q[10]), "+r"(q[11]), "+r"(q[12]), "+r"(q[13]), "+r"(q[14]), "+r"(q[15])
+                 :: "memory");
+}
 // 16 lanes x 256 bits, 8 times (64 columns) or 4 (32): thread t gives lanes t / 4 and t / 4 + 8,
 // columns 8j + 2 (t % 4) + {0, 1} from r[4j], r[4j+1] (lane t / 4) and r[4j+2], r[4j+3].
 __device__ __forceinline__ void tmem_st_16x256_x8(uint32_t taddr, const uint32_t* r) {
@@ -217,6 +232,41 @@ __device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
+// Whether a cache row holds a value that is not finite: a NaN code, or a RoPE value that is
+// NaN or infinite (the scales have been looked at). One is added to the field of all the
+// exponent (and, of a code, mantissa) bits: a carry into the bit above.
+template <bool kRopeOn>
+__device__ __noinline__ bool row_is_odd(const uint8_t* row) {
+    uint32_t odd = 0u;
+    for (int i = 0; i < kLatent / 4; ++i) odd |= ((__ldg(reinterpret_cast<const uint32_t*>(row) + i) & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (kRopeOn)
+        for (int i = 0; i < kRope / 2; ++i)
+            odd |= ((__ldg(reinterpret_cast<const uint32_t*>(row + kTailOff) + i) & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    return odd != 0u;
+}
+
+// A row's 16 bytes, zeros where the row is absent (slot < 0): a predicate, not a branch.
+__device__ __forceinline__ uint4 ld_row(const uint8_t* cache, int slot, uint32_t row_bytes, uint32_t off) {
+    const uint8_t* p = cache + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * row_bytes + off;
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"(slot));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// One thread of the warp; ptxas knows that it is one, so the MMAs' operands need no loop
+// over the active threads.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 template <bool kRopeOn>
 __global__ void __launch_bounds__(kThreads, 1)
 mla_chunk_large_kernel(const ChunkArgs args) {
@@ -224,17 +274,16 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     Meta* meta = reinterpret_cast<Meta*>(smem + kOffMeta);
     RowData& rd = *reinterpret_cast<RowData*>(smem + kOffRow);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
-    uint64_t* afull = bars;            // [2] A slot written (4 converting warps)
+    uint64_t* afull = bars;            // [2] A slot written (8 converting warps)
     uint64_t* afree = bars + 2;        // [2] its QK is done (commit)
     uint64_t* sfull = bars + 4;        // [2] S slot written (commit)
     uint64_t* sfree = bars + 6;        // [2] S slot read (8 softmax warps)
-    uint64_t* vfull = bars + 8;        // [4] V tile written (4 converting warps)
+    uint64_t* vfull = bars + 8;        // [4] V tile written (8 converting warps)
     uint64_t* vfree = bars + 12;       // [4] its PV is done (commit)
     uint64_t* pfull = bars + 16;       // P written, O^T corrected (8 softmax warps)
     uint64_t* pvdone = bars + 17;      // PV of a block done (commit)
     uint64_t* mfull = bars + 18;       // [2] meta stage written (meta warp)
-    uint64_t* mfree = bars + 21;       // [2] meta stage read (8 softmax, 4 converting warps)
-    uint64_t* cdone = bars + 24;       // [2] a block's rows converted: its states are final
+    uint64_t* mfree = bars + 21;       // [2] meta stage read (8 softmax, 8 converting warps)
     uint64_t* fin = bars + 27;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
@@ -269,7 +318,6 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         for (int i = 0; i < kMeta; ++i) {
             mbar_init(&mfull[i], 1);
             mbar_init(&mfree[i], kSoftWarps + kConvWarps);
-            mbar_init(&cdone[i], kConvWarps);
         }
         mbar_init(fin, 1);
         *abort_flag = 0;
@@ -384,28 +432,47 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 ok = ok && warp_wait(&sfull[slot], static_cast<uint32_t>((g >> 1) & 1), abort_flag);
                 if (!ok) break;
                 tc_after();
-                uint32_t v[kCols];
-                tmem_ld32(lane_base + kColS + kRows * slot + c0, v);
+                uint32_t v[16], w[16];
+                tmem_ld16(lane_base + kColS + kRows * slot + c0, v);
+                tmem_ld16(lane_base + kColS + kRows * slot + c0 + 16, w);
                 const uint32_t f = t < 0 ? 0x3f800000u : __float_as_uint(mt.sc[t][key]);
                 const uint64_t ff = two(f, f);
-                tc_wait_ld(v);
+                tc_wait_ld16(v, w);
                 tc_before();
                 warp_arrive(&sfree[slot]);
 #pragma unroll
-                for (int j = 0; j < kCols / 2; ++j) s[j] = fma2(two(v[2 * j], v[2 * j + 1]), ff, s[j]);
+                for (int j = 0; j < 8; ++j) {
+                    s[j] = fma2(two(v[2 * j], v[2 * j + 1]), ff, s[j]);
+                    s[j + 8] = fma2(two(w[2 * j], w[2 * j + 1]), ff, s[j + 8]);
+                }
             }
-            ok = ok && warp_wait(&cdone[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
+            // A value of the position's row that is not finite shows in its scores (0 * it is not 0).
+            uint64_t chk = 0ull;
             float d[kCols];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) {
+                chk = fma2(s[j], 0ull, chk);
                 d[2 * j] = lo_of(s[j]) * args.sm_scale_log2;
                 d[2 * j + 1] = hi_of(s[j]) * args.sm_scale_log2;
+            }
+            int state = mt.state[key];
+            if (ok && __any_sync(0xffffffffu, !(lo_of(chk) + hi_of(chk) == 0.0f))) {
+                // Rare: which rows it is. A query row that attends one gets NaN; one for which it is
+                // masked must not meet 0 * NaN in PV, so its V becomes 0.
+                const int slot = mt.slot[key];
+                if (slot >= 0 && !(lo_of(chk) + hi_of(chk) == 0.0f) && row_is_odd<kRopeOn>(args.cache + slot * args.row_bytes)) state = 2;
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    ok = ok && warp_wait(&vfull[t], static_cast<uint32_t>(b & 1), abort_flag);
+                    if (state == 2)
+                        for (int u = 0; u < 16; ++u)
+                            *reinterpret_cast<uint4*>(smem + kOffV + 2 * t * kVChunk + swz(kN, key, u)) = make_uint4(0u, 0u, 0u, 0u);
+                }
             }
             if (shifted) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) d[c] *= rd.shift[c0 + c];
             }
-            const int state = mt.state[key];
             if (__any_sync(0xffffffffu, state != 1) || kN * (b + 1) > lim_min) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) {
@@ -415,9 +482,13 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-                d[c] -= rd.m[c0 + c];
-                top = fmaxf(top, d[c]);
+            for (int c = 0; c < kCols; c += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&rd.m[c0 + c]);
+                d[c] -= m.x;
+                d[c + 1] -= m.y;
+                d[c + 2] -= m.z;
+                d[c + 3] -= m.w;
+                top = fmaxf(fmaxf(top, fmaxf(d[c], d[c + 1])), fmaxf(d[c + 2], d[c + 3]));
             }
             // P of the block before has been read, and O^T is complete up to it.
             if (b > 0) {
@@ -547,132 +618,99 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             tc_before();
         }
     } else if (warp < kMmaWarp) {
-        // ---- conversion: lane (row r0 + 8 i of its quarter, 16-byte pieces c of each 64) ----
-        const int quarter = warp & 3;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvRegs));
+        // ---- conversion: lane (rows r0 and r0 + 8, 16-byte pieces c of each 64) ----
+        const int quarter = warp & 3, hh = (warp - kSoftWarps) >> 2;
         const int c = lane & 3;
-        const int r0 = 32 * quarter + (lane >> 2);
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-        int slot[4];                                   // of rows r0 + 8 i
-        uint4 v[4][2];
+        const int r0 = 32 * quarter + 16 * hh + (lane >> 2);
+        const uint32_t a_base = tmem + (static_cast<uint32_t>(32 * quarter + 16 * hh) << 16) + kColA;
+        const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
+        int slot[2];
+        uint4 v[2][2];
         bool ok = true;
         int g = 0;
         auto rows_of = [&](int b) {
             ok = ok && warp_wait(&mfull[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
             if (!ok) return;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) slot[i] = meta[b % kMeta].slot[r0 + 8 * i];
+            slot[0] = meta[b % kMeta].slot[r0];
+            slot[1] = meta[b % kMeta].slot[r0 + 8];
         };
-        auto load = [&](int t, int hh) {               // rows r0 + 16 hh, + 8 of latent tile t; -1: RoPE
-            const int off = (t < 0 ? kTailOff : 128 * t) + 16 * c;
+        auto load = [&](int t) {                       // latent tile t; -1: RoPE
+            const uint32_t off = (t < 0 ? kTailOff : 128 * t) + 16 * c;
 #pragma unroll
-            for (int i = 2 * hh; i < 2 * hh + 2; ++i) {
-                const uint8_t* row = args.cache + slot[i] * args.row_bytes + off;
-                v[i][0] = slot[i] >= 0 ? ld_nc_v4(row) : make_uint4(0u, 0u, 0u, 0u);
-                v[i][1] = slot[i] >= 0 ? ld_nc_v4(row + 64) : make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < 2; ++e) {
+                v[e][0] = ld_row(args.cache, slot[e], row_bytes, off);
+                v[e][1] = ld_row(args.cache, slot[e], row_bytes, off + 64);
             }
         };
         constexpr int kFirst = kRopeOn ? -1 : 0;
         if (nblk > 0) rows_of(0);
-        if (nblk > 0 && ok) {
-            load(kFirst, 0);
-            load(kFirst, 1);
-        }
+        if (nblk > 0 && ok) load(kFirst);
         for (int b = 0; b < nblk && ok; ++b) {
-            Meta& mt = meta[b % kMeta];
+            const Meta& mt = meta[b % kMeta];
 #pragma unroll 1
             for (int t = kFirst; t < 4; ++t, ++g) {
                 const bool more = t < 3 || b + 1 < nblk;
-                const int next = t < 3 ? t + 1 : kFirst;
                 if (t == 3 && more) rows_of(b + 1);
                 const int as = g & 1;
                 if (g >= 2) ok = ok && warp_wait(&afree[as], static_cast<uint32_t>(((g >> 1) - 1) & 1), abort_flag);
-                if (t >= 0 && b > 0) ok = ok && warp_wait(&vfree[t], static_cast<uint32_t>((b - 1) & 1), abort_flag);
                 if (!ok) break;
                 tc_after();
-                // An E4M3 NaN code (all exponent and mantissa bits) or a BF16 value that is not finite
-                // (all exponent bits) carries into the bit above when one is added to the field.
-                const uint32_t all = t < 0 ? 0x7f807f80u : 0x7f7f7f7fu, one = t < 0 ? 0x00800080u : 0x01010101u;
-                const uint32_t carry = t < 0 ? 0x80008000u : 0x80808080u;
-                const uint32_t a = lane_base + kColA + 64 * as;
-                uint8_t* tile = smem + kOffV + 2 * t * kVChunk;
+                uint32_t w[32];        // 16-bit pair m of row e at 4 (m / 2) + 2 e + m % 2, as they are stored
+                if (t < 0) {
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t w[2][16];                  // 16-bit pairs of rows r0 + 16 hh, + 8
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = 2 * hh + e;
-                        uint32_t odd = 0u;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-                            odd |= ((v[i][p].x & all) + one) | ((v[i][p].y & all) + one) | ((v[i][p].z & all) + one) |
-                                   ((v[i][p].w & all) + one);
-                        if ((odd & carry) != 0u) {
-                            // Its row is marked (a query row that attends it gets NaN) and taken as 0 here: one
-                            // for which it is masked must not meet 0 * NaN in PV.
-                            mt.state[r0 + 8 * i] = 2;
-                            v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int p = 0; p < 2; ++p) {
+                            w[8 * p + 2 * e] = v[e][p].x; w[8 * p + 2 * e + 1] = v[e][p].y;
+                            w[8 * p + 4 + 2 * e] = v[e][p].z; w[8 * p + 5 + 2 * e] = v[e][p].w;
                         }
-                        if (t < 0) {
+                    load(0);                           // on its way until the next tile's turn
+                    tmem_st_16x256_x4(a_base + 64 * as, w);
+                } else {
 #pragma unroll
-                            for (int p = 0; p < 2; ++p) {
-                                w[e][4 * p] = v[i][p].x; w[e][4 * p + 1] = v[i][p].y;
-                                w[e][4 * p + 2] = v[i][p].z; w[e][4 * p + 3] = v[i][p].w;
-                            }
-                        } else {
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int p = 0; p < 2; ++p) {
-                                e4m3x4_to_f16x2x2(v[i][p].x, w[e][8 * p], w[e][8 * p + 1]);
-                                e4m3x4_to_f16x2x2(v[i][p].y, w[e][8 * p + 2], w[e][8 * p + 3]);
-                                e4m3x4_to_f16x2x2(v[i][p].z, w[e][8 * p + 4], w[e][8 * p + 5]);
-                                e4m3x4_to_f16x2x2(v[i][p].w, w[e][8 * p + 6], w[e][8 * p + 7]);
-                            }
+                        for (int p = 0; p < 2; ++p) {
+                            e4m3x4_to_f16x2x2(v[e][p].x, w[16 * p + 2 * e], w[16 * p + 2 * e + 1]);
+                            e4m3x4_to_f16x2x2(v[e][p].y, w[16 * p + 4 + 2 * e], w[16 * p + 5 + 2 * e]);
+                            e4m3x4_to_f16x2x2(v[e][p].z, w[16 * p + 8 + 2 * e], w[16 * p + 9 + 2 * e]);
+                            e4m3x4_to_f16x2x2(v[e][p].w, w[16 * p + 12 + 2 * e], w[16 * p + 13 + 2 * e]);
                         }
-                    }
-                    if (more && ok) load(next, hh);     // on its way until the next tile's turn
-                    uint32_t r[32];
-                    if (t < 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) r[4 * j + k] = w[k >> 1][2 * j + (k & 1)];
-                        tmem_st_16x256_x4(a + (static_cast<uint32_t>(16 * hh) << 16), r);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) r[4 * j + k] = w[k >> 1][2 * j + (k & 1)];
-                        tmem_st_16x256_x8(a + (static_cast<uint32_t>(16 * hh) << 16), r);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int rr = r0 + 16 * hh + 8 * e;
-                            const uint32_t f = mt.rs[t][rr] * 0x10001u;
-#pragma unroll
-                            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                                for (int u = 0; u < 2; ++u)
-                                    *reinterpret_cast<uint4*>(tile + swz(kN, rr, 8 * p + 2 * c + u)) =
-                                        make_uint4(hmul2(w[e][8 * p + 4 * u], f), hmul2(w[e][8 * p + 4 * u + 1], f),
-                                                   hmul2(w[e][8 * p + 4 * u + 2], f), hmul2(w[e][8 * p + 4 * u + 3], f));
-                        }
-                    }
+                    if (more) load(t < 3 ? t + 1 : kFirst);
+                    tmem_st_16x256_x8(a_base + 64 * as, w);
                 }
                 tc_wait_st();
                 tc_before();
                 warp_arrive(&afull[as]);
-                if (t >= 0) {
-                    fence_proxy_async_smem();
-                    warp_arrive(&vfull[t]);
+                if (t < 0) continue;
+                // V: the product with scale / sigma, once PV of the block before has read the tile
+                if (b > 0) ok = warp_wait(&vfree[t], static_cast<uint32_t>((b - 1) & 1), abort_flag);
+                if (!ok) break;
+                uint8_t* tile = smem + kOffV + 2 * t * kVChunk;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t f = mt.rs[t][r0 + 8 * e] * 0x10001u;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const uint32_t* x = w + 16 * p + 8 * u + 2 * e;
+                            *reinterpret_cast<uint4*>(tile + swz(kN, r0 + 8 * e, 8 * p + 2 * c + u)) =
+                                make_uint4(hmul2(x[0], f), hmul2(x[1], f), hmul2(x[4], f), hmul2(x[5], f));
+                        }
                 }
+                fence_proxy_async_smem();
+                warp_arrive(&vfull[t]);
             }
             if (!ok) break;
-            warp_arrive(&cdone[b % kMeta]);
             warp_arrive(&mfree[b % kMeta]);
         }
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kAuxRegs));
     if (warp == kMmaWarp) {
-        // ---- MMAs, one thread: RoPE's QK of the next block runs beside this one's softmax ----
-        if (lane == 0) {
+        // ---- MMAs, one elected thread: RoPE's QK of the next block runs beside this one's softmax ----
+        if (elect_one()) {
             const uint32_t base = smem_u32(smem);
             const uint64_t dq = sw128_desc(base + kOffQ, 16, 1024);
             const uint64_t dp = sw128_desc(base + kOffP, 16, 1024);
@@ -726,64 +764,70 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         }
         __syncwarp();
     } else if (warp == kMetaWarp) {
-        // ---- meta: addresses, scales and sigma, up to kMeta blocks ahead ----
+        // ---- meta: slots, scales and sigma, ahead of the others: block b + 1's scales and block
+        // b + 2's table entries are on their way before the stage of block b + 1 is waited for ----
         const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
+        const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
         float sigma[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int b = 0; b < nblk; ++b) {
-            Meta& mt = meta[b % kMeta];
-            const uint8_t* row[4];
-            int slot_of[4];
-            float sc[4][4];                            // [position][tile]
+        int slot[4], slot1[4];                         // positions 32 i + lane of blocks b and b + 1
+        uint4 u[4];                                    // their scales
+        auto look_up = [&](int b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = kN * b + 32 * i + lane;
-                const int64_t slot = j < n_keys ? chunk_slot(args, bt, pc.k0 + j) : -1;
-                row[i] = slot >= 0 ? args.cache + slot * args.row_bytes : nullptr;
-                slot_of[i] = static_cast<int>(slot);
+                slot1[i] = j < n_keys ? static_cast<int>(chunk_slot(args, bt, pc.k0 + j)) : -1;
             }
+        };
+        auto fetch = [&]() {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                slot[i] = slot1[i];
+                u[i] = ld_row(args.cache, slot[i], row_bytes, kScaleOff);
+                if (slot[i] >= 0) {
+                    const uint8_t* row = args.cache + static_cast<uint64_t>(static_cast<uint32_t>(slot[i])) * row_bytes;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) sc[i][t] = 0.0f;
-                if (row[i] != nullptr) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) prefetch_l2(row[i] + 128 * k);
-                    const uint4 u = ld_nc_v4(row[i] + kScaleOff);
-                    if (kRopeOn) prefetch_l2(row[i] + kTailOff + 64);
-                    sc[i][0] = __uint_as_float(u.x); sc[i][1] = __uint_as_float(u.y);
-                    sc[i][2] = __uint_as_float(u.z); sc[i][3] = __uint_as_float(u.w);
+                    for (int k = 0; k < 4; ++k) prefetch_l2(row + 128 * k);
+                    if (kRopeOn) prefetch_l2(row + kTailOff + 64);
                 }
+            }
+        };
+        if (nblk > 0) {
+            look_up(0);
+            fetch();
+            look_up(1);
+        }
+#pragma unroll 1
+        for (int b = 0; b < nblk; ++b) {
+            Meta& mt = meta[b % kMeta];
+            int state[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool odd = !(isfinite(__uint_as_float(u[i].x)) && isfinite(__uint_as_float(u[i].y)) &&
+                                   isfinite(__uint_as_float(u[i].z)) && isfinite(__uint_as_float(u[i].w)));
+                state[i] = slot[i] < 0 ? 0 : odd ? 2 : 1;
+                if (odd) u[i] = make_uint4(0u, 0u, 0u, 0u);
             }
             if (b >= kMeta && !warp_wait(&mfree[b % kMeta], static_cast<uint32_t>((b / kMeta - 1) & 1), abort_flag)) break;
-            float smax[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 32 * i + lane;
-                const bool odd = !(isfinite(sc[i][0]) && isfinite(sc[i][1]) && isfinite(sc[i][2]) && isfinite(sc[i][3]));
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (odd) sc[i][t] = 0.0f;
-                    smax[t] = fmaxf(smax[t], fabsf(sc[i][t]));
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) mt.sc[t][j] = sc[i][t];
-                mt.slot[j] = row[i] == nullptr ? -1 : slot_of[i];
-                mt.state[j] = row[i] == nullptr ? 0 : odd ? 2 : 1;
-            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
+                float sc[4], smax = 0.0f, f = 1.0f;
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) smax[t] = fmaxf(smax[t], __shfl_xor_sync(0xffffffffu, smax[t], d));
-                float f = 1.0f;
+                for (int i = 0; i < 4; ++i) {
+                    sc[i] = __uint_as_float(word4(u[i], t));
+                    smax = fmaxf(smax, fabsf(sc[i]));
+                    mt.sc[t][32 * i + lane] = sc[i];
+                }
                 // the first scale that is not 0, and later ones far above it, set sigma
-                if (smax[t] > sigma[t] * kSigmaSlack) {
-                    f = sigma[t] / smax[t];
-                    sigma[t] = smax[t];
+                if (__any_sync(0xffffffffu, smax > sigma[t] * kSigmaSlack)) {
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
+                    f = sigma[t] / smax;
+                    sigma[t] = smax;
                 }
                 const float inv = sigma[t] > 0.0f ? 1.0f / sigma[t] : 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float r = inv <= FLT_MAX ? sc[i][t] * inv : __fdiv_rn(sc[i][t], sigma[t]);
+                    const float r = inv <= FLT_MAX ? sc[i] * inv : __fdiv_rn(sc[i], sigma[t]);
                     mt.rs[t][32 * i + lane] = static_cast<uint16_t>(pack_f16x2(r, 0.0f));
                 }
                 if (lane == 0) {
@@ -791,7 +835,14 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     mt.sigma[t] = sigma[t];
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mt.slot[32 * i + lane] = slot[i];
+                mt.state[32 * i + lane] = static_cast<uint8_t>(state[i]);
+            }
             warp_arrive(&mfull[b % kMeta]);
+            if (b + 1 < nblk) fetch();
+            if (b + 2 < nblk) look_up(b + 2);
         }
     }
     }
