@@ -28,6 +28,7 @@ using namespace mla;
 constexpr int kRotThreads = 128;      // 4 warps
 constexpr int kRotWarpsPerSm = 32;
 constexpr int kHeadsPerPass = 8;      // heads a warp has in its lanes at once
+constexpr int kPasses = 2;            // passes in flight
 
 struct RopeParams {
     uint64_t turn[32];                // fraction of a turn per position, times 2^64
@@ -104,10 +105,10 @@ __device__ __forceinline__ void rotate_heads(const RotArgs& a, const RopeParams&
     const int off_hi = kInter ? 16 * k + 8 : 32 + 8 * k;
     const uint16_t* xr = a.x + r * a.x_row;
     uint16_t* yr = a.y + r * a.y_row;
-    uint4 lo[2], hi[2];
-    // the first two passes' values are on their way while the angles are computed
+    uint4 lo[kPasses], hi[kPasses];
+    // the first passes' values are on their way while the angles are computed
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < kPasses; ++q) {
         const int h = h0 + q * kHeadsPerPass + (lane >> 2);
         if (h < h1) {
             lo[q] = *reinterpret_cast<const uint4*>(xr + h * a.x_head + off_lo);
@@ -121,18 +122,20 @@ __device__ __forceinline__ void rotate_heads(const RotArgs& a, const RopeParams&
         c[i] = __shfl_sync(0xffffffffu, cs.x, 8 * k + i);
         s[i] = __shfl_sync(0xffffffffu, cs.y, 8 * k + i);
     }
-    for (int hb = h0; hb < h1; hb += 2 * kHeadsPerPass) {
+    for (int hb = h0; hb < h1; hb += kPasses * kHeadsPerPass) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kPasses; ++q) {
             const int h = hb + q * kHeadsPerPass + (lane >> 2);
+            const int next = h + kPasses * kHeadsPerPass;
             if (h >= h1) continue;
-            if (hb > h0) {
-                lo[q] = *reinterpret_cast<const uint4*>(xr + h * a.x_head + off_lo);
-                hi[q] = *reinterpret_cast<const uint4*>(xr + h * a.x_head + off_hi);
+            uint4 u = lo[q], v = hi[q];
+            if (next < h1) {
+                lo[q] = *reinterpret_cast<const uint4*>(xr + next * a.x_head + off_lo);
+                hi[q] = *reinterpret_cast<const uint4*>(xr + next * a.x_head + off_hi);
             }
-            turn8<kInter>(lo[q], hi[q], c, s);
-            st_v4(yr + h * a.y_head + off_lo, lo[q]);
-            st_v4(yr + h * a.y_head + off_hi, hi[q]);
+            turn8<kInter>(u, v, c, s);
+            st_v4(yr + h * a.y_head + off_lo, u);
+            st_v4(yr + h * a.y_head + off_hi, v);
         }
     }
 }

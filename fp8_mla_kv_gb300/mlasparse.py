@@ -134,8 +134,14 @@ def _require_cuda(*ts):
             raise ValueError("libmlasparse takes device tensors only")
 
 
+# The current stream's handle by itself costs a tenth of the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -310,27 +316,32 @@ def rope_spec(inv_freq, axis=None, interleaved: bool = False, scale: float = 1.0
 
 
 def _same_device(*ts) -> None:
-    _require_cuda(*ts)
-    if len({t.device for t in ts if t is not None}) > 1:
-        raise ValueError("tensors on different devices")
+    """Device tensors, all on the current device (whose stream and kernels the call uses)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            _require_cuda(t)
+            raise ValueError(f"a tensor on {t.device} while the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _positions(pos: torch.Tensor, n: int, n_axes: int) -> int:
     """Checks positions int32 [n] or [axes, n]; returns the stride between axes."""
-    if pos.dtype != torch.int32 or pos.dim() not in (1, 2) or pos.shape[-1] != n or (n > 1 and pos.stride(-1) != 1):
+    shape = pos.shape
+    if pos.dtype != torch.int32 or len(shape) not in (1, 2) or shape[-1] != n or (n > 1 and pos.stride(-1) != 1):
         raise ValueError("positions must be int32 [n] or [axes, n], contiguous along n")
-    if (1 if pos.dim() == 1 else int(pos.shape[0])) < n_axes:
+    if (1 if len(shape) == 1 else shape[0]) < n_axes:
         raise ValueError(f"positions for {n_axes} axes expected")
-    return n if pos.dim() == 1 else max(n, int(pos.stride(0)))
+    return n if len(shape) == 1 else max(n, pos.stride(0))
 
 
 def _rope_view(x: torch.Tensor, n: int):
     """(pointer, row stride, head stride, heads) of a bf16 [n, heads, 64] or [n, 64] view."""
-    if x.dtype != torch.bfloat16 or x.dim() not in (2, 3) or x.shape[0] != n or x.shape[-1] != 64 or x.stride(-1) != 1:
+    shape, stride = x.shape, x.stride()
+    if x.dtype != torch.bfloat16 or len(shape) not in (2, 3) or shape[0] != n or shape[-1] != 64 or stride[-1] != 1:
         raise ValueError("rotary values must be bf16 [n, heads, 64] or [n, 64], contiguous along the 64")
-    if x.dim() == 2:
-        return x.data_ptr(), x.stride(0), 0, 1
-    return x.data_ptr(), x.stride(0), x.stride(1), int(x.shape[1])
+    if len(shape) == 2:
+        return x.data_ptr(), stride[0], 0, 1
+    return x.data_ptr(), stride[0], stride[1], shape[1]
 
 
 def mla_rope(x: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, out: torch.Tensor | None = None,

@@ -90,6 +90,16 @@ def test_empty_sequences_rows_and_tokens_outside(causal):
     assert (out[-3:] == 3.0).all() and (lse[-3:] == 5.0).all()
 
 
+@pytest.mark.parametrize("n_seq", [33, 64, 65, 130, 700])
+@pytest.mark.parametrize("H", [2, 64])
+def test_many_sequences(n_seq, H):
+    """Around the batch sizes that are planned in each CTA (64) and by a kernel of their own."""
+    g = torch.Generator().manual_seed(n_seq)
+    seqs = [(int(torch.randint(0, 3, (1,), generator=g)), int(torch.randint(0, 120, (1,), generator=g))) for _ in range(n_seq)]
+    seqs[n_seq // 2] = (2, 2000)                            # one long context among short ones
+    run(batch(seqs, H, 576, 16, 656, seed=n_seq))
+
+
 def test_nothing_in_the_table():
     b = batch([(2, 100), (70, 300)], 16, 576, 64, 656, seed=2)
     b["table"][:] = -1
