@@ -61,11 +61,17 @@ __device__ __forceinline__ float quad_max(float v) {
 // at most tiles + wave, and those of split tiles (each more than C, so cut into less
 // than 2 x its length / C) at most 2 wave: the sizes of the grid and the workspace.
 constexpr int kPlanThreads = 512;
-constexpr int kPlanTries = 16;
+constexpr int kPlanTries = kPlanThreads / 32;
 
 // The k-th piece length tried: C, then an eighth of it more each time.
-__device__ __forceinline__ int64_t try_piece(int64_t C, int k, int align) {
-    return (C + C * k / 8 + align - 1) / align * align;
+__device__ __forceinline__ int try_piece(int C, int k, int align) {
+    const int64_t c = (C + ((static_cast<int64_t>(C) * k) >> 3) + align - 1) & ~static_cast<int64_t>(align - 1);
+    return static_cast<int>(min(c, static_cast<int64_t>(INT_MAX & ~(align - 1))));
+}
+// Pieces of a tile of `len` positions. (The quotient rounds: a piece more or less.)
+__device__ __forceinline__ int pieces_of(int len, int C) {
+    const float q = __fdiv_rn(static_cast<float>(len), static_cast<float>(C));
+    return q <= 1.0f ? 1 : static_cast<int>(ceilf(q));
 }
 
 __device__ __forceinline__ int64_t plan_sum(int64_t v, int64_t* buf) {
@@ -127,12 +133,14 @@ __device__ __forceinline__ int plan_scan_max(int v, int& all, int64_t* buf) {
 __global__ void __launch_bounds__(kPlanThreads)
 chunk_plan_kernel(const ChunkArgs a) {
     __shared__ int64_t buf[kPlanThreads / 32];
-    __shared__ int tries[kPlanThreads / 32][kPlanTries + 1];
+    __shared__ int64_t cost[kPlanTries];
+    __shared__ int tries[kPlanTries];
     pdl_wait();
     pdl_launch_dependents();
     // A sequence is taken if its start is not below any earlier one, nor its end below its
     // start or past T: so the sequences taken are disjoint, and together at most T tokens.
     int64_t work = 0;
+    int longest = 0;
     int top = 0;                                       // the largest start so far
     for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
         const int s = s0 + threadIdx.x;
@@ -146,62 +154,50 @@ chunk_plan_kernel(const ChunkArgs a) {
         const bool taken = start >= before && start <= end && end <= a.T;
         if (!taken || static_cast<int64_t>(q.len) > static_cast<int64_t>(a.max_pages) * a.page_size)
             atomicOr(a.err, MLA_ERR_CHUNK_RANGE);
-        a.split[s] = taken ? 1 : 0;
-        const int64_t tiles = (static_cast<int64_t>(q.n) * a.H + a.tile_rows - 1) / a.tile_rows;
-        if (taken) work += tiles * mean_limit(a, q);
+        const int tiles = taken ? tiles_of(a, q) : 0, len = mean_limit(a, q);
+        a.part0[s] = tiles;                            // for the next step; the prefixes come last
+        a.mrow0[s] = len;
+        if (tiles > 0) longest = max(longest, len);
+        work += static_cast<int64_t>(tiles) * len;
     }
-    work = plan_sum(work, buf);
-    int64_t C = (work + a.wave - 1) / a.wave;
-    C = C < a.min_piece ? a.min_piece : (C + a.align - 1) / a.align * a.align;
-    // A few longer C as well: the one for which waves of pieces x longest piece is least
-    // (64 sequences of 1..16,384 positions make 336 pieces of W / 304, two waves, but 304
-    // of a slightly longer one).
-    int pieces_of[kPlanTries], longest = 0;
-#pragma unroll
-    for (int k = 0; k < kPlanTries; ++k) pieces_of[k] = 0;
-    for (int s = threadIdx.x; s < a.n_seq; s += kPlanThreads) {
-        if (a.split[s] == 0) continue;
-        const Seq q = load_seq(a, s);
-        const int tiles = static_cast<int>((static_cast<int64_t>(q.n) * a.H + a.tile_rows - 1) / a.tile_rows);
-        const int len = mean_limit(a, q);
-        longest = max(longest, len);
-#pragma unroll
-        for (int k = 0; k < kPlanTries; ++k) pieces_of[k] += tiles * max(1, static_cast<int>((len + try_piece(C, k, a.align) - 1) / try_piece(C, k, a.align)));
-    }
-#pragma unroll
-    for (int k = 0; k < kPlanTries; ++k) pieces_of[k] = __reduce_add_sync(0xffffffffu, pieces_of[k]);
+    work = plan_sum(work, buf);                        // (its barriers order the stores above, too)
+    // C, and a few longer ones: each warp counts the pieces of one, and the one for which waves
+    // of pieces x longest piece is least is taken (64 sequences of 1..16,384 positions make 336
+    // pieces of W / 304, two waves, but 304 of a slightly longer one).
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     longest = __reduce_max_sync(0xffffffffu, longest);
-    if ((threadIdx.x & 31) == 0) {
-        for (int k = 0; k < kPlanTries; ++k) tries[threadIdx.x >> 5][k] = pieces_of[k];
-        tries[threadIdx.x >> 5][kPlanTries] = longest;
+    if (lane == 0) tries[warp] = longest;
+    const int64_t share = (work + a.wave - 1) / a.wave;
+    const int64_t most = INT_MAX & ~(a.align - 1);     // no context is longer: nothing is split then
+    int C = static_cast<int>(min((share + a.align - 1) & ~static_cast<int64_t>(a.align - 1), most));
+    C = max(a.min_piece, C);
+    __syncthreads();
+    for (int w = 0; w < kPlanTries; ++w) longest = max(longest, tries[w]);
+    {
+        const int c = try_piece(C, warp, a.align);
+        int n = 0;
+        for (int s = lane; s < a.n_seq; s += 32) n += a.part0[s] * pieces_of(a.mrow0[s], c);
+        n = __reduce_add_sync(0xffffffffu, n);
+        const unsigned waves = (static_cast<unsigned>(n) + a.wave - 1u) / static_cast<unsigned>(a.wave);
+        if (lane == 0) cost[warp] = static_cast<int64_t>(waves) * min(c, longest);
     }
     __syncthreads();
-    longest = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) longest = max(longest, tries[w][kPlanTries]);
-    int64_t best = INT64_MAX, best_C = C;
-    for (int k = 0; k < kPlanTries; ++k) {
-        int64_t n = 0;
-        for (int w = 0; w < kPlanThreads / 32; ++w) n += tries[w][k];
-        const int64_t c = try_piece(C, k, a.align);
-        const int64_t cost = (n + a.wave - 1) / a.wave * (c < longest ? c : longest);
-        if (cost < best) {
-            best = cost;
-            best_C = c;
-        }
-    }
-    C = best_C;
+    int best = 0;
+#pragma unroll
+    for (int w = 1; w < kPlanTries; ++w)
+        if (cost[w] < cost[best]) best = w;
+    C = try_piece(C, best, a.align);
     int p_base = 0, q_base = 0, r_base = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
         const int s = s0 + threadIdx.x;
         int nk = 1, pieces = 0, parts = 0, rows = 0;
-        if (s < a.n_seq && a.split[s] != 0) {
-            const Seq q = load_seq(a, s);
-            const int tiles = static_cast<int>((static_cast<int64_t>(q.n) * a.H + a.tile_rows - 1) / a.tile_rows);
-            nk = max(1, static_cast<int>((mean_limit(a, q) + C - 1) / C));
+        if (s < a.n_seq) {
+            const int tiles = a.part0[s];
+            if (tiles > 0) nk = pieces_of(a.mrow0[s], C);
             pieces = tiles * nk;
             if (nk > 1) {
                 parts = pieces;
-                rows = q.n * a.H;
+                rows = load_seq(a, s).n * a.H;
             }
         }
         int all;
@@ -241,7 +237,7 @@ mla_chunk_merge_kernel(const ChunkArgs a) {
         const int s = find_seq(a.mrow0, a.n_seq, r, lane);
         const int local = r - a.mrow0[s];
         const int np = a.split[s];
-        const int tile = local / a.tile_rows;
+        const int tile = local >> a.tile_shift;
         const int64_t row0 = (static_cast<int64_t>(a.part0[s]) + static_cast<int64_t>(tile) * np) * a.tile_rows +
                              (local - tile * a.tile_rows);
         const int64_t grow = static_cast<int64_t>(__ldg(a.q_start + s)) * a.H + local;
@@ -802,8 +798,9 @@ Sizes sizes_of(int T, int H, int n_seq, int sms) {
     z.large = rows_all >= static_cast<int64_t>(kLargeFrom) * n_seq;
     z.tile_rows = z.large ? kLargeRows : kSmallRows;
     z.wave = z.large ? sms : kCtasPerSm * sms;
-    z.max_pieces = rows_all / z.tile_rows + (n_seq < T ? n_seq : T) + z.wave;
-    const size_t rows = 2 * static_cast<size_t>(z.wave) * z.tile_rows;
+    // (a few more than the plan's bounds: the quotient that counts a tile's pieces rounds)
+    z.max_pieces = rows_all / z.tile_rows + (n_seq < T ? n_seq : T) + z.wave + 16;
+    const size_t rows = (2 * static_cast<size_t>(z.wave) + 16) * z.tile_rows;
     z.parts_o = rows * kLatent * sizeof(float);
     z.parts_lse = align256(rows * sizeof(float));
     z.prefix = align256((static_cast<size_t>(n_seq) + 1) * sizeof(int32_t));
@@ -881,6 +878,8 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     a.sm_scale_log2 = sm_scale * kLog2e;
     a.err = err;
     a.tile_rows = z.tile_rows;
+    a.tile_shift = z.large ? 6 : 4;
+    static_assert(kLargeRows == 1 << 6 && kSmallRows == 1 << 4, "tile shift");
     a.align = z.large ? kLargeBlock : kNB;
     a.wave = z.wave;
     a.min_piece = z.large ? kLargeMinPiece : kMinPiece;

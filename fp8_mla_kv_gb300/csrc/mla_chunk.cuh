@@ -26,8 +26,8 @@ struct ChunkArgs {
     float sm_scale_log2;
     int* err;
     // The plan (workspace): exclusive prefixes over the sequences, and pieces per tile.
-    int tile_rows;                     // query rows per tile
-    int align;                         // positions per block: pieces start at multiples of it
+    int tile_rows, tile_shift;         // query rows per tile, a power of two
+    int align;                         // positions per block, a power of two: pieces start at multiples of it
     int wave;                          // pieces that fill the GPU once
     int min_piece;
     int32_t* piece0;                   // [n_seq + 1] pieces
@@ -65,6 +65,10 @@ __device__ __forceinline__ int mean_limit(const ChunkArgs& a, const Seq& q) {
     return q.n == 0 ? 0 : token_limit(a, q, q.n / 2);
 }
 
+__device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Seq& q) {
+    return (q.n * a.H + a.tile_rows - 1) >> a.tile_shift;
+}
+
 struct Piece {
     int seq;                           // -1: no piece
     Seq s;
@@ -97,7 +101,7 @@ __device__ __forceinline__ Piece find_piece(const ChunkArgs& a, int b, int lane)
     const int nk = a.split[p.seq];
     const int local = b - a.piece0[p.seq];
     p.rows = p.s.n * a.H;
-    const int tiles = (p.rows + a.tile_rows - 1) / a.tile_rows;
+    const int tiles = tiles_of(a, p.s);
     const int back = local / nk;
     const int tile = tiles - 1 - back;               // a causal chunk's last tiles are the longest: first
     const int k = local - back * nk;
@@ -105,7 +109,7 @@ __device__ __forceinline__ Piece find_piece(const ChunkArgs& a, int b, int lane)
     p.grow0 = static_cast<int64_t>(p.s.start) * a.H;
     const int last = min(p.rows, p.row0 + a.tile_rows) - 1;
     const int lim = token_limit(a, p.s, last / a.H);
-    const int per = ((lim + nk - 1) / nk + a.align - 1) / a.align * a.align;
+    const int per = ((lim + nk - 1) / nk + a.align - 1) & ~(a.align - 1);
     p.k0 = static_cast<int>(min(static_cast<int64_t>(lim), static_cast<int64_t>(k) * per));
     p.k1 = min(lim, p.k0 + per);
     p.part = nk > 1 ? a.part0[p.seq] + tile * nk + k : -1;
