@@ -781,8 +781,13 @@ constexpr int kCtasPerSm = 2;
 constexpr int kMinPiece = 128;
 constexpr int kLargeMinPiece = 256;
 
-// Query rows per sequence, on average, from which the kernel for many rows is taken.
+// The kernel for many rows is taken from this many query rows per sequence, on average (64
+// sequences of up to 16,384 positions: 32 rows each 243 us small, 359 large, 48 rows 388
+// and 363, 64 rows 547 and 322), and from so many (row, position) pairs at most in the
+// batch: it starts about 20 us later (4 sequences of 64 rows and up to 700 positions: 18
+// us small, 37 large).
 constexpr int kLargeFrom = 48;
+constexpr int64_t kLargeWork = 6 << 20;
 
 struct Sizes {
     bool large;
@@ -792,10 +797,11 @@ struct Sizes {
     size_t total() const { return parts_o + parts_lse + 4 * prefix; }
 };
 
-Sizes sizes_of(int T, int H, int n_seq, int sms) {
+Sizes sizes_of(int T, int H, int n_seq, int64_t positions, int sms) {
     Sizes z;
     const int64_t rows_all = static_cast<int64_t>(T) * H;
-    z.large = rows_all >= static_cast<int64_t>(kLargeFrom) * n_seq;
+    z.large = rows_all >= static_cast<int64_t>(kLargeFrom) * n_seq &&
+              (positions > kLargeWork || rows_all * positions >= kLargeWork);
     z.tile_rows = z.large ? kLargeRows : kSmallRows;
     z.wave = z.large ? sms : kCtasPerSm * sms;
     // (a few more than the plan's bounds: the quotient that counts a tile's pieces rounds)
@@ -827,7 +833,10 @@ bool launch(K kernel, int64_t grid, int threads, size_t smem, void* stream, A...
 extern "C" size_t mla_chunk_attention_workspace_bytes(int T, int H, int n_seq) {
     if (T <= 0 || H < 1 || H > 128 || n_seq <= 0) return 0;
     const int sms = mla_host::sm_count();
-    return sms <= 0 ? 0 : sizes_of(T, H, n_seq, sms).total();
+    if (sms <= 0) return 0;
+    // whichever kernel the contexts' capacity decides for
+    const size_t few = sizes_of(T, H, n_seq, 0, sms).total(), many = sizes_of(T, H, n_seq, INT64_MAX, sms).total();
+    return few > many ? few : many;
 }
 
 extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
@@ -851,8 +860,9 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     int* err = mla_host::device_error_word();
     const int sms = mla_host::sm_count();
     if (err == nullptr || sms <= 0) return MLA_ECUDA;
-    const Sizes z = sizes_of(T, H, n_seq, sms);
-    if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < z.total()) return MLA_ENOWORKSPACE;
+    const Sizes z = sizes_of(T, H, n_seq, static_cast<int64_t>(max_pages) * page_size, sms);
+    if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < mla_chunk_attention_workspace_bytes(T, H, n_seq))
+        return MLA_ENOWORKSPACE;
     const bool rope = d_qk == kLatent + kRope;
     const void* kernel = rope ? reinterpret_cast<const void*>(mla_chunk_small_kernel<true>)
                               : reinterpret_cast<const void*>(mla_chunk_small_kernel<false>);

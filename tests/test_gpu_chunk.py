@@ -12,8 +12,22 @@ pytestmark = pytest.mark.gpu
 D = "cuda:0"
 
 
+WIDE = False
+
+
+@pytest.fixture(params=["narrow", "wide"], autouse=True)
+def table_width(request):
+    """A batch with 48 rows a sequence goes to the kernel for many rows only where its contexts' capacity is large, so
+    every test runs with a table just wide enough and with one of many unused columns."""
+    global WIDE
+    WIDE = request.param == "wide"
+
+
 def batch(seqs, H, d_qk, page, row, seed=0, extra=2, tail_tokens=0, outliers=False):
     """seqs: (new tokens, context length). Pages in random order, page 0 unused."""
+    rows = (sum(n for n, _ in seqs) + tail_tokens) * H
+    if WIDE and extra and rows >= 48 * len(seqs):
+        extra += 8_000_000 // (rows * page) + 1
     g = torch.Generator().manual_seed(seed)
     pages = [-(-L // page) for _, L in seqs]
     total = sum(pages) + 3
