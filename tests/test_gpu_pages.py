@@ -205,9 +205,11 @@ def test_bad_rows_pages_and_counts_are_flagged():
     assert torch.equal(cache, keep)
 
 
-@pytest.mark.parametrize("live", [0, 1, 4095, 2048])
-def test_compact_at_the_ends(live):
-    P, page = 4096, 1
+@pytest.mark.parametrize("P,live", [(4096, 0), (4096, 1), (4096, 4095), (4096, 2048), (1, 0), (2, 1), (31, 12), (33, 32),
+                                    (65536, 30000), (65537, 65536), (150001, 70000), (70000, 1)])
+def test_compact_at_the_ends(P, live):
+    """The live pages last in the pool; up to 65,536 pages are planned by one CTA."""
+    page = 1
     cache = torch.randint(0, 256, (P, 528), dtype=torch.uint8)
     refs = torch.zeros(P, dtype=torch.int32)
     if live:
