@@ -444,7 +444,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, qmax_s[w * kHeads + g + 8 * r]);
         int e = 0;
-        frexpf(mx, &e);                              // mx < 2^e
+        if (mx <= FLT_MAX) frexpf(mx, &e);           // mx < 2^e
         const int k = (e > 15) ? (e - 15) : 0;
         qdown[r] = ldexpf(1.0f, -k);
         rowf[r] = args.sm_scale_log2 * ldexpf(1.0f, k);

@@ -252,6 +252,7 @@ mla_fork_part_kernel(const ForkArgs a, int chunks, int units_per_page) {
         }
         const int64_t page_bytes = a.row_bytes * a.page_size;
         const int from = fork_part(a, p, len);
+        if (from < 0) continue;                            // the parent's row was changed meanwhile: not allowed, not read
         copy_unit(a.cache + page * page_bytes, a.cache + from * page_bytes, static_cast<int64_t>(piece) * kUnitBytes, bytes, lane);
         if (piece == 0 && lane == 0) {
             a.table[static_cast<int64_t>(c) * a.max_pages + len / a.page_size] = page;

@@ -7,6 +7,7 @@ the call raises. There is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -144,6 +145,14 @@ def _stream(stream) -> int:
             return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Where a call's own tensors are made: on its stream, so that they are ordered with its kernels and the allocator
+    hands their memory to nothing else before those are done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def kv_cache(cache: torch.Tensor) -> KVCache:
@@ -349,7 +358,8 @@ def mla_rope(x: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, out: torch.Tens
     """Rotates x bf16 [n, heads, 64] (or [n, 64], any row and head strides that are multiples of 8) by positions
     int32 [n] or [axes, n]; out may be x."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        with _on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _same_device(x, pos, out)
     n = int(x.shape[0])
     stride = _positions(pos, n, rope.n_axes)
@@ -416,14 +426,16 @@ def mla_chunk_attention(q: torch.Tensor, cache: torch.Tensor, q_start: torch.Ten
     assert kv_len.dtype == torch.int32 and kv_len.is_contiguous()
     assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2
     assert block_table.shape[0] == n_seq
-    if out is None:
-        out = torch.zeros((T, H, 512), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q.device)
+    if out is None or lse is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.zeros((T, H, 512), dtype=torch.bfloat16, device=q.device)
+            if lse is None:
+                lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                workspace = alloc_chunk_workspace(T, H, n_seq, q.device)
     assert out.dtype == torch.bfloat16 and out.is_contiguous() and out.numel() == T * H * 512
     assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == T * H
-    if workspace is None:
-        workspace = alloc_chunk_workspace(T, H, n_seq, q.device)
     rc = load().mla_chunk_attention(q.data_ptr(), T, H, d_qk, kv_cache(cache), q_start.data_ptr(), kv_len.data_ptr(),
                                     block_table.data_ptr(), n_seq, int(block_table.shape[1]), int(page_size),
                                     int(bool(causal)), float(sm_scale), out.data_ptr(), lse.data_ptr(),
@@ -481,7 +493,8 @@ def mla_page_fork(cache: torch.Tensor, page_size: int, refcount: torch.Tensor, b
     n = int(parent.numel())
     assert child.numel() == n and lens.numel() == n
     if workspace is None:
-        workspace = alloc_page_workspace(refcount.numel(), n, cache.device)
+        with _on(stream):
+            workspace = alloc_page_workspace(refcount.numel(), n, cache.device)
     rc = load().mla_page_fork(kv_cache(cache), int(page_size), refcount.data_ptr(), int(refcount.numel()),
                               block_table.data_ptr(), int(block_table.shape[0]), int(block_table.shape[1]),
                               parent.data_ptr(), child.data_ptr(), lens.data_ptr(), n, workspace.data_ptr(),
@@ -502,7 +515,8 @@ def mla_page_compact(cache: torch.Tensor, page_size: int, refcount: torch.Tensor
     assert refcount_out.numel() == refcount.numel() and table_out.shape == block_table.shape
     assert page_map is None or page_map.numel() == refcount.numel()
     if workspace is None:
-        workspace = alloc_page_workspace(refcount.numel(), 0, cache.device)
+        with _on(stream):
+            workspace = alloc_page_workspace(refcount.numel(), 0, cache.device)
     rc = load().mla_page_compact(kv_cache(cache), int(page_size), refcount.data_ptr(), refcount_out.data_ptr(),
                                  int(refcount.numel()), block_table.data_ptr(), table_out.data_ptr(),
                                  int(block_table.shape[0]), int(block_table.shape[1]),

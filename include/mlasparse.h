@@ -373,7 +373,8 @@ int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* la
  * positions out and lse are what mla_sparse_decode computes. A token that attends nothing
  * gets out = 0 and lse = -inf. A row that holds a value that is not finite (a NaN code, a NaN
  * or infinite scale or RoPE value) makes out and lse NaN for exactly the tokens that
- * attend it. Tokens outside every sequence keep their out and lse. The result does not
+ * attend it; a query row that holds one gets unspecified values, and no other row does.
+ * Tokens outside every sequence keep their out and lse. The result does not
  * depend on what slot 0, absent pages or positions past kv_len hold.
  *
  *   q_bf16       bf16 [T, H, d_qk] row-major, device, 16-byte aligned; d_qk 576 or 512

@@ -285,6 +285,46 @@ def test_on_another_stream():
     assert torch.equal(out.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, l2)
 
 
+def test_a_stream_of_its_own_for_what_the_call_makes():
+    """Without out, lse and workspace the call makes them on its stream, behind nothing of the current one."""
+    b = batch([(3, 500), (60, 90)], 16, 576, 16, 656, seed=17)
+    want, wlse = call(b)
+    t = {k: v.to(D) if isinstance(v, torch.Tensor) else v for k, v in b.items()}
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)                           # the current stream is busy meanwhile
+    for stream in (s, s.cuda_stream):
+        out, lse = M.mla_chunk_attention(t["q"], t["cache"], t["q_start"], t["kv_len"], t["table"], 16, t["scale"], stream=stream)
+        s.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_a_query_row_that_is_not_finite_is_alone(n, value):
+    b = batch([(n, 300), (n, 200)], 16, 576, 16, 656, seed=15)
+    out, lse = call(b)
+    b["q"][n // 2, 3, 100] = value
+    o2, l2 = call(b)
+    assert M.mla_get_error() == 0
+    keep = torch.ones(out.shape[:2], dtype=torch.bool)
+    keep[n // 2, 3] = False
+    assert torch.equal(out.cpu()[keep].view(torch.int16), o2.cpu()[keep].view(torch.int16))
+    assert torch.equal(lse.cpu()[keep], l2.cpu()[keep])
+    if math.isnan(value):
+        assert torch.isnan(o2[n // 2, 3]).all() and torch.isnan(l2[n // 2, 3])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_query_rows_of_very_different_sizes(n):
+    """q rows scaled from 2^-30 to 2^40: each row's exponent shift is its own."""
+    b = batch([(n, 300)], 16, 576, 16, 656, seed=16)
+    e = torch.linspace(-30, 40, n * 16).view(n, 16, 1).round()
+    b["q"] = (b["q"].double() * torch.pow(2.0, e.double())).to(torch.bfloat16)
+    b["scale"] = 2.0 ** -12
+    run(b)
+
+
 def test_a_cache_whose_offsets_pass_32_bits():
     """Rows beyond 4 GiB of the cache (7 million slots of 656 bytes)."""
     slots, page = 7_000_000, 64

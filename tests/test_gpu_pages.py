@@ -244,3 +244,15 @@ def test_pages_in_a_graph():
         h.compact()
         same(h, dc, dr, dt)
     assert M.mla_get_error() == 0
+
+
+def test_nothing_to_do():
+    cache = torch.zeros((64, 656), dtype=torch.uint8, device=D)
+    refs, table = torch.zeros(4, dtype=torch.int32, device=D), torch.full((2, 2), -1, dtype=torch.int32, device=D)
+    none = torch.empty(0, dtype=torch.int32, device=D)
+    M.mla_page_copy(cache, cache, 16, none, none)
+    M.mla_page_free(refs, table, none)
+    M.mla_page_fork(cache, 16, refs, table, none, none, none)
+    M.mla_page_compact(cache, 16, refs, table)
+    M.mla_page_compact(cache, 16, refs, table[:0])
+    assert M.mla_get_error() == 0 and (cache == 0).all() and (refs == 0).all() and (table == -1).all()

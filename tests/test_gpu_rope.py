@@ -156,3 +156,18 @@ def test_rope_on_another_stream_and_in_a_graph():
     gr.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, M.mla_rope(x, pos, spec))
+
+
+def test_nothing_to_do_and_one_dimensional_positions():
+    spec = M.rope_spec(INV)
+    pos = torch.arange(5, dtype=torch.int32, device=D)
+    assert M.mla_rope(torch.empty((0, 3, 64), dtype=torch.bfloat16, device=D), pos[:0], spec).shape == (0, 3, 64)
+    assert M.mla_rope(torch.empty((5, 0, 64), dtype=torch.bfloat16, device=D), pos, spec).shape == (5, 0, 64)
+    x = torch.randn((5, 64), device=D).to(torch.bfloat16)
+    y = M.mla_rope(x, pos, spec)
+    ref, mag = P.rotate(x.cpu().double()[:, None], pos.cpu(), INV, AXES[1], False)
+    close(y[:, None], ref, mag)
+    cache = torch.zeros((16, 656), dtype=torch.uint8, device=D)
+    M.mla_rope_kv_write(cache, torch.empty(0, dtype=torch.int64, device=D), torch.empty((0, 512), dtype=torch.bfloat16, device=D),
+                        torch.empty((0, 64), dtype=torch.bfloat16, device=D), pos[:0], spec)
+    assert (cache == 0).all()
