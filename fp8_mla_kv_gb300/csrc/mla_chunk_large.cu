@@ -421,6 +421,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             const Meta& mt = meta[b % kMeta];
             // A wait that ran out only skips work up to the vote, which all four warps take.
             ok = warp_wait(&mfull[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
+            int state = mt.state[key];
             uint64_t s[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) s[j] = 0ull;
@@ -435,7 +436,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 uint32_t v[16], w[16];
                 tmem_ld16(lane_base + kColS + kRows * slot + c0, v);
                 tmem_ld16(lane_base + kColS + kRows * slot + c0 + 16, w);
-                const uint32_t f = t < 0 ? 0x3f800000u : __float_as_uint(mt.sc[t][key]);
+                const uint32_t f = __float_as_uint(t < 0 ? args.sm_scale_log2 : mt.sc[t][key] * args.sm_scale_log2);
                 const uint64_t ff = two(f, f);
                 tc_wait_ld16(v, w);
                 tc_before();
@@ -446,29 +447,15 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     s[j + 8] = fma2(two(w[2 * j], w[2 * j + 1]), ff, s[j + 8]);
                 }
             }
-            // A value of the position's row that is not finite shows in its scores (0 * it is not 0).
-            uint64_t chk = 0ull;
             float d[kCols];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) {
-                chk = fma2(s[j], 0ull, chk);
-                d[2 * j] = lo_of(s[j]) * args.sm_scale_log2;
-                d[2 * j + 1] = hi_of(s[j]) * args.sm_scale_log2;
+                d[2 * j] = lo_of(s[j]);
+                d[2 * j + 1] = hi_of(s[j]);
             }
-            int state = mt.state[key];
-            if (ok && __any_sync(0xffffffffu, !(lo_of(chk) + hi_of(chk) == 0.0f))) {
-                // Rare: which rows it is. A query row that attends one gets NaN; one for which it is
-                // masked must not meet 0 * NaN in PV, so its V becomes 0.
-                const int slot = mt.slot[key];
-                if (slot >= 0 && !(lo_of(chk) + hi_of(chk) == 0.0f) && row_is_odd<kRopeOn>(args.cache + slot * args.row_bytes)) state = 2;
-#pragma unroll 1
-                for (int t = 0; t < 4; ++t) {
-                    ok = ok && warp_wait(&vfull[t], static_cast<uint32_t>(b & 1), abort_flag);
-                    if (state == 2)
-                        for (int u = 0; u < 16; ++u)
-                            *reinterpret_cast<uint4*>(smem + kOffV + 2 * t * kVChunk + swz(kN, key, u)) = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
+            // A value of the position's row that is not finite shows in its score with any finite query
+            // row (0 * it is not 0), so with the first. (Looked into after the vote.)
+            const bool odd = !(fabsf(d[0]) <= FLT_MAX);
             if (shifted) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) d[c] *= rd.shift[c0 + c];
@@ -480,7 +467,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     if (state == 0 || kN * b + key >= rd.lim[c0 + c]) d[c] = -INFINITY;
                 }
             }
-            float top = -INFINITY;
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < kCols; c += 4) {
                 const float4 m = *reinterpret_cast<const float4*>(&rd.m[c0 + c]);
@@ -488,14 +475,15 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 d[c + 1] -= m.y;
                 d[c + 2] -= m.z;
                 d[c + 3] -= m.w;
-                top = fmaxf(fmaxf(top, fmaxf(d[c], d[c + 1])), fmaxf(d[c + 2], d[c + 3]));
+                tops[(c >> 2) & 3] = fmaxf(fmaxf(tops[(c >> 2) & 3], fmaxf(d[c], d[c + 1])), fmaxf(d[c + 2], d[c + 3]));
             }
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             // P of the block before has been read, and O^T is complete up to it.
             if (b > 0) {
                 ok = ok && warp_wait(pvdone, static_cast<uint32_t>((b - 1) & 1), abort_flag);
                 tc_after();
             }
-            const bool moved = bar_sync_or(1 + half, 128, unseen || top > kRescaleSlack || !ok);
+            const bool moved = bar_sync_or(1 + half, 128, unseen || top > kRescaleSlack || odd || !ok);
             const float f0 = mt.f[0], f1 = mt.f[1], f2 = mt.f[2], f3 = mt.f[3];
             const bool sigma_moved = b > 0 && (f0 != 1.0f || f1 != 1.0f || f2 != 1.0f || f3 != 1.0f);
             if (moved) {
@@ -504,6 +492,24 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 if (bar_sync_or(1 + half, 128, !ok)) {
                     ok = false;
                     break;
+                }
+                if (__any_sync(0xffffffffu, odd)) {
+                    // A query row that attends such a row gets NaN; one for which it is masked must not
+                    // meet 0 * NaN in PV, so its V becomes 0.
+                    const int slot = mt.slot[key];
+                    if (slot >= 0 && odd && row_is_odd<kRopeOn>(args.cache + slot * args.row_bytes)) {
+                        state = 2;
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c)
+                            if (kN * b + key < rd.lim[c0 + c]) d[c] = __int_as_float(0x7FC00000);
+                    }
+#pragma unroll 1
+                    for (int t = 0; t < 4; ++t) {
+                        ok = ok && warp_wait(&vfull[t], static_cast<uint32_t>(b & 1), abort_flag);
+                        if (state == 2)
+                            for (int u = 0; u < 16; ++u)
+                                *reinterpret_cast<uint4*>(smem + kOffV + 2 * t * kVChunk + swz(kN, key, u)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) {
