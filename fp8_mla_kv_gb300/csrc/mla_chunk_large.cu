@@ -26,7 +26,7 @@
 //
 // Roles: warps 0-7 softmax (lane quarter w % 4, query rows 32 (w / 4) ..), 8-15 turn cache
 // rows into operands (straight from global memory, the next tile's loads in flight; each
-// warp 16 positions), 16 issues the MMAs, 17 walks the block table ahead of them: slots,
+// warp 16 positions), 16 issues the MMAs, 17 and 18 walk the block table ahead of them: slots,
 // scales, sigma, prefetches into L2.
 #include <cfloat>
 #include <climits>
@@ -43,11 +43,12 @@ constexpr int kN = kLargeBlock;              // positions per block (M of the MM
 constexpr int kRows = kLargeRows;            // query rows per tile (N of the MMAs)
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kMetaWarp = kMmaWarp + 1;
-constexpr int kThreads = 20 * 32;            // five warpgroups (two warps idle)
-// Registers per thread: launched as 96 each and dealt out again.
-constexpr int kSoftRegs = 128, kConvRegs = 80, kAuxRegs = 64;
-static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * 96, "registers");
+constexpr int kMetaWarp = kMmaWarp + 1, kMetaWarps = 2;
+constexpr int kThreads = 20 * 32;            // five warpgroups (one warp idle)
+// Registers per thread: launched as kLaunchRegs each and dealt out again.
+constexpr int kLaunchRegs = 96;
+constexpr int kSoftRegs = 112, kConvRegs = 88, kAuxRegs = 80;
+static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * kLaunchRegs, "registers");
 constexpr int kCols = kRows / 2;             // query rows per softmax warp
 constexpr int kMeta = 2;                     // blocks the meta warp may be ahead
 constexpr float kRescaleSlack = 8.0f;        // log2 units: p <= 2^8
@@ -79,6 +80,7 @@ struct __align__(16) RowData {               // per query row
     int lim[kRows];                          // positions it attends, counted from the piece's first
     int unseen[kRows];                       // attends something, but nothing so far
     float wmax[4][kRows];                    // by lane quarter: maxima; at the end sums of p
+    float smax[kMetaWarps][4];               // largest scales, where a sigma moves
     int any_unseen[2], pad[2];
 };
 constexpr int kOffBars = kOffRow + static_cast<int>(sizeof(RowData));
@@ -190,6 +192,12 @@ __device__ __forceinline__ void tmem_st_16x256_x4(uint32_t taddr, const uint32_t
         : "memory");
 }
 
+template <int kRegs>
+__device__ __forceinline__ void deal_registers() {
+    if (kRegs > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegs));
+    if (kRegs < kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegs));
+}
+
 // Byte offset of 16-byte unit u of row r in a swizzled tile of `rows` rows.
 __device__ __forceinline__ uint32_t swz(int rows, int r, int u) {
     return static_cast<uint32_t>((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
@@ -282,7 +290,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     uint64_t* vfree = bars + 12;       // [4] its PV is done (commit)
     uint64_t* pfull = bars + 16;       // P written, O^T corrected (8 softmax warps)
     uint64_t* pvdone = bars + 17;      // PV of a block done (commit)
-    uint64_t* mfull = bars + 18;       // [2] meta stage written (meta warp)
+    uint64_t* mfull = bars + 18;       // [2] meta stage written (2 meta warps)
     uint64_t* mfree = bars + 21;       // [2] meta stage read (8 softmax, 8 converting warps)
     uint64_t* fin = bars + 27;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -316,7 +324,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         mbar_init(pfull, kSoftWarps);
         mbar_init(pvdone, 1);
         for (int i = 0; i < kMeta; ++i) {
-            mbar_init(&mfull[i], 1);
+            mbar_init(&mfull[i], kMetaWarps);
             mbar_init(&mfree[i], kSoftWarps + kConvWarps);
         }
         mbar_init(fin, 1);
@@ -400,7 +408,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     constexpr int kGroups = kRopeOn ? 5 : 4;          // S partials per block: [RoPE,] tiles 0 .. 3
 
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
+        deal_registers<kSoftRegs>();
         // ---- softmax: thread = position 32 quarter + lane, query rows c0 .. c0 + 31 ----
         const int quarter = warp & 3, half = warp >> 2;
         const int key = 32 * quarter + lane;
@@ -411,9 +419,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         const int lim_min = __reduce_min_sync(0xffffffffu, my_lim);
         const bool shifted = __any_sync(0xffffffffu, rd.shift[c0 + lane] != 1.0f);
         bool unseen = true;                            // some row has seen nothing yet: take maxima
-        float l[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) l[c] = 0.0f;
+        float l = 0.0f;                                // sum of p of query row c0 + lane, over the warp's positions
         float sig[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         bool ok = true;
         int g = 0;
@@ -534,10 +540,8 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 bar_sync_or(1 + half, 128, false);
                 unseen = rd.any_unseen[half] != 0;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    d[c] -= rd.wmax[0][c0 + c];
-                    l[c] *= rd.alpha[c0 + c];
-                }
+                for (int c = 0; c < kCols; ++c) d[c] -= rd.wmax[0][c0 + c];
+                l *= rd.alpha[c0 + lane];
             }
             if (b > 0 && (moved || sigma_moved)) {
 #pragma unroll 1
@@ -558,12 +562,9 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             for (int u = 0; u < kCols / 8; ++u) {
                 uint32_t h[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p0 = ex2_approx(d[8 * u + 2 * k]), p1 = ex2_approx(d[8 * u + 2 * k + 1]);
-                    l[8 * u + 2 * k] += p0;
-                    l[8 * u + 2 * k + 1] += p1;
-                    h[k] = pack_f16x2(p0, p1);
-                }
+                for (int k = 0; k < 8; ++k) d[8 * u + k] = ex2_approx(d[8 * u + k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(d[8 * u + 2 * k], d[8 * u + 2 * k + 1]);
                 *reinterpret_cast<uint4*>(prow + (((4 * half + u) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
 #pragma unroll
@@ -572,6 +573,18 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             tc_before();
             warp_arrive(pfull);
             warp_arrive(&mfree[b % kMeta]);
+            // The sums of P over the warp's positions, while PV runs: at each step half of the rows go
+            // to the lane across, so lane x ends with row x.
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) {
+                const bool up = (lane & x) != 0;
+#pragma unroll
+                for (int c = 0; c < x; ++c) {
+                    const float keep = up ? d[c + x] : d[c], give = up ? d[c] : d[c + x];
+                    d[c] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+                }
+            }
+            l += d[0];
         }
         // ---- epilogue: l over the positions, then O^T * sigma / l ----
         if (ok && nblk > 0) {
@@ -579,13 +592,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             tc_after();
         }
         if (!bar_sync_or(1 + half, 128, !ok)) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-                float v = l[c];
-#pragma unroll
-                for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-                if (lane == c) rd.wmax[quarter][c0 + c] = v;
-            }
+            rd.wmax[quarter][c0 + lane] = l;
             bar_sync_or(1 + half, 128, false);
             if (quarter == 0) {
                 const int c = c0 + lane;
@@ -624,7 +631,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             tc_before();
         }
     } else if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvRegs));
+        deal_registers<kConvRegs>();
         // ---- conversion: lane (rows r0 and r0 + 8, 16-byte pieces c of each 64) ----
         const int quarter = warp & 3, hh = (warp - kSoftWarps) >> 2;
         const int c = lane & 3;
@@ -683,8 +690,8 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                             e4m3x4_to_f16x2x2(v[e][p].z, w[16 * p + 8 + 2 * e], w[16 * p + 9 + 2 * e]);
                             e4m3x4_to_f16x2x2(v[e][p].w, w[16 * p + 12 + 2 * e], w[16 * p + 13 + 2 * e]);
                         }
-                    if (more) load(t < 3 ? t + 1 : kFirst);
                     tmem_st_16x256_x8(a_base + 64 * as, w);
+                    if (more) load(t < 3 ? t + 1 : kFirst);
                 }
                 tc_wait_st();
                 tc_before();
@@ -713,7 +720,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             warp_arrive(&mfree[b % kMeta]);
         }
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kAuxRegs));
+    deal_registers<kAuxRegs>();
     if (warp == kMmaWarp) {
         // ---- MMAs, one elected thread: RoPE's QK of the next block runs beside this one's softmax ----
         if (elect_one()) {
@@ -769,24 +776,27 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             (void)mbar_wait_bounded(fin, 0);
         }
         __syncwarp();
-    } else if (warp == kMetaWarp) {
-        // ---- meta: slots, scales and sigma, ahead of the others: block b + 1's scales and block
-        // b + 2's table entries are on their way before the stage of block b + 1 is waited for ----
+    } else if (warp < kMetaWarp + kMetaWarps) {
+        // ---- meta: slots, scales and sigma, ahead of the others, each warp for half of a block's
+        // positions: block b + 1's scales and block b + 2's table entries are on their way
+        // before the stage of block b + 1 is waited for ----
+        constexpr int kPer = kN / 32 / kMetaWarps;     // positions per lane
+        const int mw = warp - kMetaWarp;
         const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
         const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
         float sigma[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        int slot[4], slot1[4];                         // positions 32 i + lane of blocks b and b + 1
-        uint4 u[4];                                    // their scales
+        int slot[kPer], slot1[kPer];                   // of blocks b and b + 1
+        uint4 u[kPer];                                 // their scales
         auto look_up = [&](int b) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = kN * b + 32 * i + lane;
+            for (int i = 0; i < kPer; ++i) {
+                const int j = kN * b + 32 * (kPer * mw + i) + lane;
                 slot1[i] = j < n_keys ? static_cast<int>(chunk_slot(args, bt, pc.k0 + j)) : -1;
             }
         };
         auto fetch = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kPer; ++i) {
                 slot[i] = slot1[i];
                 u[i] = ld_row(args.cache, slot[i], row_bytes, kScaleOff);
                 if (slot[i] >= 0) {
@@ -805,46 +815,67 @@ mla_chunk_large_kernel(const ChunkArgs args) {
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
             Meta& mt = meta[b % kMeta];
-            int state[4];
+            int state[kPer];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kPer; ++i) {
                 const bool odd = !(isfinite(__uint_as_float(u[i].x)) && isfinite(__uint_as_float(u[i].y)) &&
                                    isfinite(__uint_as_float(u[i].z)) && isfinite(__uint_as_float(u[i].w)));
                 state[i] = slot[i] < 0 ? 0 : odd ? 2 : 1;
                 if (odd) u[i] = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (b >= kMeta && !warp_wait(&mfree[b % kMeta], static_cast<uint32_t>((b / kMeta - 1) & 1), abort_flag)) break;
+            bool ok = true;
+            if (b >= kMeta) ok = warp_wait(&mfree[b % kMeta], static_cast<uint32_t>((b / kMeta - 1) & 1), abort_flag);
+            // Whether a sigma moves (the first scale that is not 0, and later ones far above it): a
+            // decision of both warps.
+            bool far = false;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) far = far || fabsf(__uint_as_float(word4(u[i], t))) > sigma[t] * kSigmaSlack;
+            const bool move = bar_sync_or(4, 32 * kMetaWarps, far || !ok);
+            if (!ok || (move && *abort_flag)) break;
+            if (move) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(__uint_as_float(word4(u[i], t))));
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    if (lane == 0) rd.smax[mw][t] = top;
+                }
+                bar_sync_or(4, 32 * kMetaWarps, false);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                float sc[4], smax = 0.0f, f = 1.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sc[i] = __uint_as_float(word4(u[i], t));
-                    smax = fmaxf(smax, fabsf(sc[i]));
-                    mt.sc[t][32 * i + lane] = sc[i];
-                }
-                // the first scale that is not 0, and later ones far above it, set sigma
-                if (__any_sync(0xffffffffu, smax > sigma[t] * kSigmaSlack)) {
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
-                    f = sigma[t] / smax;
-                    sigma[t] = smax;
+                float f = 1.0f;
+                if (move) {
+                    const float top = fmaxf(rd.smax[0][t], rd.smax[1][t]);
+                    if (top > sigma[t] * kSigmaSlack) {
+                        f = sigma[t] / top;
+                        sigma[t] = top;
+                    }
                 }
                 const float inv = sigma[t] > 0.0f ? 1.0f / sigma[t] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float r = inv <= FLT_MAX ? sc[i] * inv : __fdiv_rn(sc[i], sigma[t]);
-                    mt.rs[t][32 * i + lane] = static_cast<uint16_t>(pack_f16x2(r, 0.0f));
+                for (int i = 0; i < kPer; ++i) {
+                    const int j = 32 * (kPer * mw + i) + lane;
+                    const float sc = __uint_as_float(word4(u[i], t));
+                    const float r = inv <= FLT_MAX ? sc * inv : __fdiv_rn(sc, sigma[t]);
+                    mt.sc[t][j] = sc;
+                    mt.rs[t][j] = static_cast<uint16_t>(pack_f16x2(r, 0.0f));
                 }
-                if (lane == 0) {
+                if (mw == 0 && lane == 0) {
                     mt.f[t] = f;
                     mt.sigma[t] = sigma[t];
                 }
             }
+            if (move) bar_sync_or(4, 32 * kMetaWarps, false);      // the maxima have been read
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mt.slot[32 * i + lane] = slot[i];
-                mt.state[32 * i + lane] = static_cast<uint8_t>(state[i]);
+            for (int i = 0; i < kPer; ++i) {
+                const int j = 32 * (kPer * mw + i) + lane;
+                mt.slot[j] = slot[i];
+                mt.state[j] = static_cast<uint8_t>(state[i]);
             }
             warp_arrive(&mfull[b % kMeta]);
             if (b + 1 < nblk) fetch();
