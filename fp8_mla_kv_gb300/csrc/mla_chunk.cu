@@ -477,6 +477,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m_ref[2] = {-INFINITY, -INFINITY};   // exp2 offset per row (log2 units); -inf: nothing seen yet
     float l_run[2] = {0.0f, 0.0f};             // sum of p over this warp's positions
+    const int lim_all = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
     float sigma = FLT_MIN;                     // running max of tile `warp`'s row scales
     float inv_sigma = 1.0f / FLT_MIN;
     bool failed = false;
@@ -554,14 +555,15 @@ qk_again:
             rs[kb][0] = pack_f16x2(sc[2 * kb][0] * inv_sigma, sc[2 * kb][1] * inv_sigma);
             rs[kb][1] = pack_f16x2(sc[2 * kb + 1][0] * inv_sigma, sc[2 * kb + 1][1] * inv_sigma);
         }
-        // A value that is not finite in a staged row shows in its products. Then (rare)
+        // A value that is not finite in a staged row shows in its products with any finite
+        // query row (0 * it is not 0), so with rows 0 .. 7. Then (rare)
         // such rows are found, marked and zeroed, so that a position masked for a query
         // row cannot reach it through 0 * NaN in PV; the block's QK is done again.
         bool odd = false;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) odd = odd || !(fabsf(fmaf(acc[nt][i], sc[nt][i & 1], accr[nt][i])) <= FLT_MAX);
+            for (int i = 0; i < 2; ++i) odd = odd || !(fabsf(fmaf(acc[nt][i], sc[nt][i], accr[nt][i])) <= FLT_MAX);
         // Barrier 1 also carries a timeout of any warp, or such a value, to all of them.
         if (bar_sync_or(1, kConsumerThreads, !ok || (odd && !again))) {
             if (bar_sync_or(1, kConsumerThreads, !ok)) { failed = true; break; }
@@ -588,11 +590,13 @@ qk_again:
             a.x += bq.x; a.y += bq.y; a.z += bq.z; a.w += bq.w;
         }
         float sv[4] = {a.x * rowf[0], a.y * rowf[0], a.z * rowf[1], a.w * rowf[1]};
+        if ((~present | poison) != 0u || kNB * (b + 1) > lim_all) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = 8 * warp + 2 * c + (i & 1);
-            if (((poison >> j) & 1u) != 0u) sv[i] = __int_as_float(0x7FC00000);
-            if (((present >> j) & 1u) == 0u || kNB * b + j >= lim[i >> 1]) sv[i] = -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+                const int j = 8 * warp + 2 * c + (i & 1);
+                if (((poison >> j) & 1u) != 0u) sv[i] = __int_as_float(0x7FC00000);
+                if (((present >> j) & 1u) == 0u || kNB * b + j >= lim[i >> 1]) sv[i] = -INFINITY;
+            }
         }
         const float bm0 = quad_max(fmaxf(sv[0], sv[1]));
         const float bm1 = quad_max(fmaxf(sv[2], sv[3]));
