@@ -57,16 +57,21 @@ __device__ __forceinline__ float quad_max(float v) {
 
 // Plan of the work (one CTA): how many pieces each sequence's tiles are cut into, and
 // the prefixes by which a CTA finds its piece and the merge its rows. C, the longest
-// piece, is at least a wave-th of all positions that tiles read, so the pieces number
-// at most tiles + wave, and those of split tiles (each more than C, so cut into less
-// than 2 x its length / C) at most 2 wave: the sizes of the grid and the workspace.
+// piece, is at least so many eighths (first_eighth) of a wave-th of all positions that
+// tiles read, so the pieces number at most tiles + 8 / first_eighth wave, and those of
+// split tiles (each more than C, so cut into less than 2 x its length / C) at most twice
+// the latter: the sizes of the grid and the workspace.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanTries = kPlanThreads / 32;
 
-// The k-th piece length tried: C, then an eighth of it more each time.
-__device__ __forceinline__ int try_piece(int C, int k, int align) {
-    const int64_t c = (C + ((static_cast<int64_t>(C) * k) >> 3) + align - 1) & ~static_cast<int64_t>(align - 1);
-    return static_cast<int>(min(c, static_cast<int64_t>(INT_MAX & ~(align - 1))));
+// The k-th piece length tried: first_eighth + k eighths of a wave-th of the work.
+__device__ __forceinline__ int try_piece(const ChunkArgs& a, int64_t share, int k) {
+    const int64_t most = INT_MAX & ~(a.align - 1);         // no context is longer: nothing is split then
+    const int64_t e = a.first_eighth + k;
+    int64_t c = share < most ? (share * e + 7) >> 3 : most;
+    c = (c + a.align - 1) & ~static_cast<int64_t>(a.align - 1);
+    c = c < a.min_piece ? a.min_piece : c;
+    return static_cast<int>(c < most ? c : most);
 }
 // Pieces of a tile of `len` positions. (The quotient rounds: a piece more or less.)
 __device__ __forceinline__ int pieces_of(int len, int C) {
@@ -161,32 +166,33 @@ chunk_plan_kernel(const ChunkArgs a) {
         work += static_cast<int64_t>(tiles) * len;
     }
     work = plan_sum(work, buf);                        // (its barriers order the stores above, too)
-    // C, and a few longer ones: each warp counts the pieces of one, and the one for which waves
-    // of pieces x longest piece is least is taken (64 sequences of 1..16,384 positions make 336
-    // pieces of W / 304, two waves, but 304 of a slightly longer one).
+    // Each warp counts the pieces of one C; the one with the least estimate is taken: pieces that
+    // fit one wave end with the longest, more of them (each at piece_cost more) are dealt out
+    // as CTAs become free and end half a piece apart. (64 sequences of 1..16,384 positions:
+    // 302 pieces of at most 2,400 for 304 places, a place's share being 2,116. 24 sequences
+    // of 2 x 128 heads and up to 16,384 positions: one wave would need pieces of 8,320 where
+    // a share is 5,053, so rather 456 pieces of 1,920 for 152 places: 335 us, 430 the former.)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) tries[warp] = longest;
     const int64_t share = (work + a.wave - 1) / a.wave;
-    const int64_t most = INT_MAX & ~(a.align - 1);     // no context is longer: nothing is split then
-    int C = static_cast<int>(min((share + a.align - 1) & ~static_cast<int64_t>(a.align - 1), most));
-    C = max(a.min_piece, C);
     __syncthreads();
     for (int w = 0; w < kPlanTries; ++w) longest = max(longest, tries[w]);
     {
-        const int c = try_piece(C, warp, a.align);
+        const int c = try_piece(a, share, warp), cut = min(c, longest);
         int n = 0;
         for (int s = lane; s < a.n_seq; s += 32) n += a.part0[s] * pieces_of(a.mrow0[s], c);
         n = __reduce_add_sync(0xffffffffu, n);
-        const unsigned waves = (static_cast<unsigned>(n) + a.wave - 1u) / static_cast<unsigned>(a.wave);
-        if (lane == 0) cost[warp] = static_cast<int64_t>(waves) * min(c, longest);
+        if (lane == 0)
+            cost[warp] = n <= a.wave ? cut + static_cast<int64_t>(a.piece_cost)
+                                     : (work + static_cast<int64_t>(n) * a.piece_cost) / a.wave + cut / 2;
     }
     __syncthreads();
     int best = 0;
 #pragma unroll
     for (int w = 1; w < kPlanTries; ++w)
         if (cost[w] < cost[best]) best = w;
-    C = try_piece(C, best, a.align);
+    const int C = try_piece(a, share, best);
     int p_base = 0, q_base = 0, r_base = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
         const int s = s0 + threadIdx.x;
@@ -784,6 +790,11 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPiece = 128;
 constexpr int kLargeMinPiece = 256;
+// What a piece costs beside its positions, in positions, and the shortest length tried, in
+// eighths of a place's share (many rows: 2, 3 and 8 eighths at the 24 sequences above took
+// 335, 335 and 430 us; few rows fit their tiles to one wave nearly always).
+constexpr int kPieceCost = 192, kLargePieceCost = 384;
+constexpr int kFirstEighth = 8, kLargeFirstEighth = 3;
 
 // The kernel for many rows is taken from this many query rows per sequence, on average (64
 // sequences of up to 16,384 positions: 32 rows each 243 us small, 359 large, 48 rows 388
@@ -795,7 +806,7 @@ constexpr int64_t kLargeWork = 6 << 20;
 
 struct Sizes {
     bool large;
-    int tile_rows, wave;
+    int tile_rows, wave, first_eighth;
     int64_t max_pieces;
     size_t parts_o, parts_lse, prefix;     // bytes
     size_t total() const { return parts_o + parts_lse + 4 * prefix; }
@@ -809,8 +820,10 @@ Sizes sizes_of(int T, int H, int n_seq, int64_t positions, int sms) {
     z.tile_rows = z.large ? kLargeRows : kSmallRows;
     z.wave = z.large ? sms : kCtasPerSm * sms;
     // (a few more than the plan's bounds: the quotient that counts a tile's pieces rounds)
-    z.max_pieces = rows_all / z.tile_rows + (n_seq < T ? n_seq : T) + z.wave + 16;
-    const size_t rows = (2 * static_cast<size_t>(z.wave) + 16) * z.tile_rows;
+    z.first_eighth = z.large ? kLargeFirstEighth : kFirstEighth;
+    const int extra = (8 * z.wave + z.first_eighth - 1) / z.first_eighth + 16;
+    z.max_pieces = rows_all / z.tile_rows + (n_seq < T ? n_seq : T) + extra;
+    const size_t rows = 2 * static_cast<size_t>(extra) * z.tile_rows;
     z.parts_o = rows * kLatent * sizeof(float);
     z.parts_lse = align256(rows * sizeof(float));
     z.prefix = align256((static_cast<size_t>(n_seq) + 1) * sizeof(int32_t));
@@ -897,6 +910,8 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     a.align = z.large ? kLargeBlock : kNB;
     a.wave = z.wave;
     a.min_piece = z.large ? kLargeMinPiece : kMinPiece;
+    a.first_eighth = z.first_eighth;
+    a.piece_cost = z.large ? kLargePieceCost : kPieceCost;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(w);
     w += z.parts_o;
@@ -912,9 +927,7 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
                     : rope  ? launch(mla_chunk_small_kernel<true>, z.max_pieces, kThreads, kSmemTotal, stream, a)
                             : launch(mla_chunk_small_kernel<false>, z.max_pieces, kThreads, kSmemTotal, stream, a);
     if (!ok) return MLA_ECUDA;
-    // Rows of split tiles: at most those of 2 wave pieces, in pairs at least.
-    int64_t merge = static_cast<int64_t>(z.wave) * z.tile_rows;
-    if (merge > static_cast<int64_t>(T) * H) merge = static_cast<int64_t>(T) * H;
+    int64_t merge = static_cast<int64_t>(T) * H;
     if (merge > static_cast<int64_t>(sms) * 16) merge = static_cast<int64_t>(sms) * 16;
     return launch(mla_chunk_merge_kernel, merge, 128, 0, stream, a) ? MLA_OK : MLA_ECUDA;
 }

@@ -29,13 +29,14 @@ struct ChunkArgs {
     int tile_rows, tile_shift;         // query rows per tile, a power of two
     int align;                         // positions per block, a power of two: pieces start at multiples of it
     int wave;                          // pieces that fill the GPU once
-    int min_piece;
+    int min_piece, first_eighth;       // shortest pieces: positions, eighths of a wave-th of the work
+    int piece_cost;                    // of a piece, beside its positions
     int32_t* piece0;                   // [n_seq + 1] pieces
     int32_t* part0;                    // [n_seq + 1] pieces of split tiles
     int32_t* mrow0;                    // [n_seq + 1] query rows of split tiles
     int32_t* split;                    // [n_seq] pieces per tile
-    float* part_o;                     // [2 wave, tile_rows, 512] normalised partials
-    float* part_lse;                   // [2 wave, tile_rows]
+    float* part_o;                     // [parts, tile_rows, 512] normalised partials
+    float* part_lse;                   // [parts, tile_rows]
 };
 
 // A sequence's new tokens and context, as far as they are valid.
