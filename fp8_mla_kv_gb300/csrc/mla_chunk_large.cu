@@ -524,7 +524,10 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     for (int x = 16; x > 0; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
                     if (lane == c) rd.wmax[quarter][c0 + c] = v;
                 }
-                bar_sync_or(1 + half, 128, false);
+                if (bar_sync_or(1 + half, 128, !ok)) {
+                    ok = false;
+                    break;
+                }
                 if (quarter == 0) {
                     const int c = c0 + lane;
                     const float up = fmaxf(fmaxf(rd.wmax[0][c], rd.wmax[1][c]), fmaxf(rd.wmax[2][c], rd.wmax[3][c]));
@@ -833,8 +836,8 @@ mla_chunk_large_kernel(const ChunkArgs args) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) far = far || fabsf(__uint_as_float(word4(u[i], t))) > sigma[t] * kSigmaSlack;
             const bool move = bar_sync_or(4, 32 * kMetaWarps, far || !ok);
-            if (!ok || (move && *abort_flag)) break;
             if (move) {
+                if (bar_sync_or(4, 32 * kMetaWarps, !ok)) break;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float top = 0.0f;
