@@ -144,11 +144,13 @@ __device__ __forceinline__ bool fork_rows(const ForkArgs& a, int f, int& p, int&
            static_cast<int64_t>(len) <= static_cast<int64_t>(a.max_pages) * a.page_size;
 }
 
-// The physical page that holds the parent's last, not full page; -1 if there is none.
+// The physical page that holds the parent's last, not full page; -1 if there is none (page 0,
+// whose slot 0 is absent for the parent and would not be in a copy, is none).
 __device__ __forceinline__ int fork_part(const ForkArgs& a, int p, int len) {
     if (len % a.page_size == 0) return -1;
     const int e = __ldg(a.table + static_cast<int64_t>(p) * a.max_pages + len / a.page_size);
-    return (e >= 0 && e < a.num_pages) ? e : -1;
+    if (e >= a.num_pages) atomicOr(a.err, MLA_ERR_PAGE_RANGE);
+    return (e > 0 && e < a.num_pages) ? e : -1;
 }
 
 // First launch. CTAs 0 .. n-1: fork f's shared pages, in the child's row and in the

@@ -40,7 +40,7 @@ class Host:
                     self.refs[e] += 1
             part = self.table[p][whole] if rest else -1
             row += [-1] * (width - whole)
-            if 0 <= part < len(self.refs):
+            if 0 < part < len(self.refs):
                 todo.append((c, whole, rest, part))
             self.table[c] = row
         for c, whole, rest, part in todo:
@@ -177,6 +177,26 @@ def test_fork_when_the_pool_runs_out():
     assert M.mla_get_error() == M.MLA_ERR_POOL_EMPTY
     same(h, dc, dr, dt)
     assert dt[3].tolist() == [2, -1, -1]
+
+
+def test_a_last_page_that_cannot_be_copied():
+    page, P = 8, 6
+    cache = torch.randint(0, 256, (P * page, 656), dtype=torch.uint8)
+    table = torch.tensor([[0, 3], [2, 0], [4, 9], [-1, -1], [-1, -1], [-1, -1]], dtype=torch.int32)
+    refs = torch.tensor([0, 0, 1, 1, 1, 0], dtype=torch.int32)
+    h = Host(cache, page, refs, table)
+    dc, dr, dt = cache.to(D), refs.to(D), table.to(D)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device=D)  # noqa: E731
+    M.mla_page_fork(dc, page, dr, dt, ints([0, 1]), ints([3, 4]), ints([15, 15]))       # page 0 whole, then as the last one
+    h.fork([0, 1], [3, 4], [15, 15])
+    assert M.mla_get_error() == 0
+    same(h, dc, dr, dt)
+    assert dt[3].tolist() == [0, 1] and dt[4].tolist() == [2, -1]
+    M.mla_page_fork(dc, page, dr, dt, ints([2]), ints([5]), ints([9]))                  # page 9 does not exist
+    h.fork([2], [5], [9])
+    assert M.mla_get_error() == M.MLA_ERR_PAGE_RANGE
+    same(h, dc, dr, dt)
+    assert dt[5].tolist() == [4, -1]
 
 
 def test_bad_rows_pages_and_counts_are_flagged():
