@@ -867,7 +867,9 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     if (kv.row_bytes == MLA_ROW_BYTES_NOPE && d_qk != kLatent) return MLA_EUNSUPPORTED;   // no tail to read
     if (H < 1 || H > 128) return MLA_EUNSUPPORTED;
     if (T == 0 || n_seq == 0) return MLA_OK;
-    if (static_cast<int64_t>(T) * H > INT_MAX / 4 || kv.num_slots > INT_MAX) return MLA_EUNSUPPORTED;
+    if (static_cast<int64_t>(T) * H > INT_MAX / 4 || kv.num_slots > INT_MAX ||
+        static_cast<int64_t>(max_pages) * page_size > INT_MAX - 4096)      // positions, rounded up, are an int
+        return MLA_EUNSUPPORTED;
     if (q_bf16 == nullptr || out_bf16 == nullptr || lse == nullptr || q_start == nullptr || kv_len == nullptr ||
         (max_pages > 0 && (block_table == nullptr || kv.data == nullptr)))
         return MLA_EINVAL;

@@ -384,8 +384,10 @@ int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* la
  *                which it is not is skipped and flagged MLA_ERR_CHUNK_RANGE
  *   kv_len       int32 [n_seq], device; a negative one counts as 0; positions past
  *                max_pages * page_size are absent and flagged MLA_ERR_CHUNK_RANGE
- *   block_table  int32 [n_seq, max_pages], device
- *   out_bf16     bf16 [T, H, 512], device, 16-byte aligned;  lse  fp32 [T, H], device
+ *   block_table  int32 [n_seq, max_pages], device; max_pages * page_size below 2^31 - 4096
+ *                (otherwise MLA_EUNSUPPORTED)
+ *   out_bf16     bf16 [T, H, 512], device, 16-byte aligned;  lse  fp32 [T, H], device; neither
+ *                overlaps an input
  *   workspace    device scratch of mla_chunk_attention_workspace_bytes(T, H, n_seq) bytes,
  *                16-byte aligned; its contents on entry do not matter. Calls that may
  *                overlap (other streams, graphs replayed at once) need their own.
@@ -432,7 +434,8 @@ int mla_page_free(int32_t* refcount, int num_pages, int32_t* block_table, int n_
  * absent for the child) and MLA_ERR_POOL_EMPTY is set. The child's row is overwritten:
  * free it first if it holds pages. A negative parent or child skips the fork; parent ==
  * child or a length past the table is dropped and flagged. A parent may be forked
- * many times in a call. Preconditions: every page that a parent holds is counted, no
+ * many times in a call. A last page that is not full and is page 0 or none of the pool's
+ * (flagged) is not copied: the entry stays -1. Preconditions: every page that a parent holds is counted, no
  * child is listed twice, and none is a parent of the same call.
  */
 int mla_page_fork(mla_kv_cache_t kv, int page_size, int32_t* refcount, int num_pages, int32_t* block_table, int n_seq,

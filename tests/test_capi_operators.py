@@ -83,7 +83,8 @@ def test_chunk_attention(lib):
                 dict(q=P(264)), dict(out=P(264)), dict(kv=M.KVCache(264, 16, 656)), dict(lse=P(257)), dict(qs=P(257)),
                 dict(kl=P(257)), dict(bt=P(257))):
         assert call(**bad) == M.MLA_EINVAL, bad
-    for bad in (dict(d=300), dict(H=0), dict(H=129), dict(kv=M.KVCache(256, 16, 528)), dict(T=1 << 30, H=128)):
+    for bad in (dict(d=300), dict(H=0), dict(H=129), dict(kv=M.KVCache(256, 16, 528)), dict(T=1 << 30, H=128),
+                dict(mp=1 << 20, ps=1 << 11), dict(mp=2, ps=1 << 30)):
         assert call(**bad) == M.MLA_EUNSUPPORTED, bad
     for T, H, n in ((0, 16, 1), (1, 0, 1), (1, 129, 1), (1, 16, 0)):
         assert lib.mla_chunk_attention_workspace_bytes(T, H, n) == 0
