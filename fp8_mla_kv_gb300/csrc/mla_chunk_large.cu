@@ -9,25 +9,37 @@
 // untransposed S that way took 1,536 of the SM's shared-memory cycles per 64 positions.
 //
 // Per block of 128 positions:
-//   QK   five products (the latent tiles, K = 128, and RoPE, 64): A = the positions'
-//        codes as exact f16, put into tensor memory by the converting warps, B = q
-//        (exact in f16 after an exponent-only shift) in shared memory. Each partial is
-//        exact before fp32 accumulation and goes to an S slot of its own; the softmax
-//        warps fold them with the fp32 tile scales as they come. (A K rounded to f16 with
-//        its scale in it needs one accumulator but moves a score near 20 by 3.5e-3.)
+//   QK   five products (the latent tiles, K = 128, and RoPE, 64): A = the positions' bytes as
+//        the cache holds them, E4M3 (RoPE: BF16), put into tensor memory by the converting
+//        warps without a look at them, B = q in shared memory. An E4M3 A wants an 8-bit B, so
+//        q is two of them: an E4M3 part and the rest as E5M2, each row brought to [2^7, 2^8)
+//        by a power of two first. A value of at least 2^-6 there is the sum of its parts exactly
+//        (8 bits of BF16, 4 in the first part, and the rest is at most 8 units of the last bit:
+//        E5M2 has all of those); a smaller one is off by at most 2^-14, 2^-21 of the row's largest.
+//        Each tile's partial goes to an S slot of its own; the softmax warps fold them with the fp32
+//        tile scales as they come. (A K rounded to f16 with its scale in it needs one
+//        accumulator but moves a score near 20 by 3.5e-3. f16 codes and f16 q, exact too, need
+//        the conversion before QK: it then waits for the tile's last PV, 3,817 us instead of 3,380 on
+//        the chunk below.)
 //   P    thread = position x 32 query rows. The exp2 offset of a row is an earlier maximum:
 //        it moves only when a score is more than kRescaleSlack above it, which one
 //        vote per block shows; only then maxima over the positions are taken.
 //   PV   O^T_t += V_t^T P^T: V = code x scale / sigma as f16 in shared memory (sigma_t: a
 //        scale near the largest of tile t so far), read MN-major; P as f16, MN-major
 //        too. Roundings: P, scale / sigma and their product, half a step of 2^-11 each.
-// The order of the dims within QK is the one in which a thread that loaded 16 codes of a
+// The order of the dims within QK is the one in which a thread that loaded 16 bytes of a
 // row can store them to tensor memory; q is laid out to match.
 //
 // Roles: warps 0-7 softmax (lane quarter w % 4, query rows 32 (w / 4) ..), 8-15 turn cache
-// rows into operands (straight from global memory, the next tile's loads in flight; each
-// warp 16 positions), 16 issues the MMAs, 17 and 18 walk the block table ahead of them: slots,
-// scales, sigma, prefetches into L2.
+// rows into operands (straight from global memory, a block's rows in registers until PV has
+// left their place; each warp 16 positions), 16 issues QK, 17 and 18 walk the block table ahead
+// of them (slots, scales, sigma, prefetches into L2), 19 issues PV.
+//
+// 4,096 new tokens of 16 heads after CTXTODO positions: 3,380 us, 605 TFLOP/s, 0.31 of the measured
+// dense bf16 rate. What bounds it is no single unit: tensor pipe a quarter, shared memory and issue slots
+// a half each, and the hand-offs between the roles (about 120 cycles each, a dozen in a row
+// per block) keep them from overlapping further. Without conversion, MMAs, exponentials
+// and sums a block still takes 0.9 of its time.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -44,14 +56,17 @@ constexpr int kRows = kLargeRows;            // query rows per tile (N of the MM
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kMetaWarp = kMmaWarp + 1, kMetaWarps = 2;
-constexpr int kThreads = 20 * 32;            // five warpgroups (one warp idle)
+constexpr int kPvWarp = kMetaWarp + kMetaWarps;
+constexpr int kThreads = 20 * 32;            // five warpgroups
 // Registers per thread: launched as kLaunchRegs each and dealt out again.
 constexpr int kLaunchRegs = 96;
-constexpr int kSoftRegs = 112, kConvRegs = 88, kAuxRegs = 80;
+constexpr int kSoftRegs = 104, kConvRegs = 104, kAuxRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * kLaunchRegs, "registers");
 constexpr int kCols = kRows / 2;             // query rows per softmax warp
 constexpr int kMeta = 2;                     // blocks the meta warp may be ahead
-constexpr float kRescaleSlack = 8.0f;        // log2 units: p <= 2^8
+// The exp2 offset puts the largest score at kTop (log2 units), so that f16's smallest p is 2^-32 of the
+// largest, and moves when one is kRescaleSlack above that: p <= 2^15.
+constexpr float kTop = 7.0f, kRescaleSlack = 8.0f;
 constexpr float kSigmaSlack = 64.0f;         // scale / sigma <= 2^6: code x scale / sigma < 2^15 in f16
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -59,7 +74,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // values (128 B) in 8-row groups of 1 KB, 16-byte unit u of row r at unit u ^ (r & 7);
 // wider tiles are sequences of such 64-column chunks.
 constexpr int kQChunk = kRows * 128;                       // 8 KB
-constexpr int kOffQ = 0;                                   // 8 latent chunks and RoPE
+constexpr int kOffQ = 0;                                   // a chunk per latent tile and part of q, and RoPE
 constexpr int kVChunk = kN * 128;                          // 16 KB
 constexpr int kOffV = kOffQ + 9 * kQChunk;                 // 4 tiles of 128 positions x 128 dims
 constexpr int kOffP = kOffV + 8 * kVChunk;                 // 128 positions x 64 query rows
@@ -74,9 +89,9 @@ struct __align__(16) Meta {
 };
 constexpr int kOffRow = kOffMeta + kMeta * static_cast<int>(sizeof(Meta));
 struct __align__(16) RowData {               // per query row
-    float m[kRows];                          // exp2 offset (log2 units)
+    float neg_m[kRows];                      // exp2 offset (log2 units), negated
     float alpha[kRows];                      // what O^T and l are multiplied by when it moves; at the end 1 / l
-    float shift[kRows];                      // undoes the exponent shift of q
+    float shift[kRows];                      // undoes q's power of two
     int lim[kRows];                          // positions it attends, counted from the piece's first
     int unseen[kRows];                       // attends something, but nothing so far
     float wmax[4][kRows];                    // by lane quarter: maxima; at the end sums of p
@@ -90,7 +105,8 @@ constexpr int kSmemTotal = kOffMisc + 16;
 static_assert(kSmemTotal <= 232448, "shared memory");
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColA = 4 * kRows, kColS = kColA + 128; // O^T tiles, two A slots of 64, two S slots of 64
+constexpr uint32_t kColA = 4 * kRows, kColS = kColA + 128; // O^T tiles, four A slots of 32, two S slots of 64
+constexpr int kASlots = 4;
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
@@ -101,7 +117,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t fmt, bool a_mn, bool b
     return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(a_mn) << 15) |
            (static_cast<uint32_t>(b_mn) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
-constexpr uint32_t kIdQK = idesc_f16(0, false, false, kN, kRows);     // S^T = K_t . q_t^T
+// kind::f8f6f4: the same fields; formats 0 E4M3, 1 E5M2.
+constexpr uint32_t kIdQK = idesc_f16(0, false, false, kN, kRows);     // S^T = K_t . (the E4M3 part of q_t)^T
+constexpr uint32_t kIdQK2 = kIdQK | (1u << 10);                       // + K_t . (its E5M2 part)^T
 constexpr uint32_t kIdQR = idesc_f16(1, false, false, kN, kRows);     // RoPE (bf16)
 constexpr uint32_t kIdPV = idesc_f16(0, true, true, kTile, kRows);    // O^T_t += V_t^T . P^T
 
@@ -115,6 +133,12 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)) : "memory");
+}
+__device__ __forceinline__ void umma_ts8(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
         :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)) : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -172,18 +196,8 @@ __device__ __forceinline__ void tc_wait_ld16(uint32_t* r, uint32_t* q) {
                    "+r"(q[8]), "+r"(q[9]), "+r"(q[10]), "+r"(q[11]), "+r"(q[12]), "+r"(q[13]), "+r"(q[14]), "+r"(q[15])
                  :: "memory");
 }
-// 16 lanes x 256 bits, 8 times (64 columns) or 4 (32): thread t gives lanes t / 4 and t / 4 + 8,
-// columns 8j + 2 (t % 4) + {0, 1} from r[4j], r[4j+1] (lane t / 4) and r[4j+2], r[4j+3].
-__device__ __forceinline__ void tmem_st_16x256_x8(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-           "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-           "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
+// 16 lanes x 256 bits, 4 times (32 columns): thread t gives lanes t / 4 and t / 4 + 8, columns
+// 8j + 2 (t % 4) + {0, 1} from r[4j], r[4j+1] (lane t / 4) and r[4j+2], r[4j+3].
 __device__ __forceinline__ void tmem_st_16x256_x4(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -282,17 +296,17 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     Meta* meta = reinterpret_cast<Meta*>(smem + kOffMeta);
     RowData& rd = *reinterpret_cast<RowData*>(smem + kOffRow);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
-    uint64_t* afull = bars;            // [2] A slot written (8 converting warps)
-    uint64_t* afree = bars + 2;        // [2] its QK is done (commit)
-    uint64_t* sfull = bars + 4;        // [2] S slot written (commit)
-    uint64_t* sfree = bars + 6;        // [2] S slot read (8 softmax warps)
-    uint64_t* vfull = bars + 8;        // [4] V tile written (8 converting warps)
-    uint64_t* vfree = bars + 12;       // [4] its PV is done (commit)
-    uint64_t* pfull = bars + 16;       // P written, O^T corrected (8 softmax warps)
-    uint64_t* pvdone = bars + 17;      // PV of a block done (commit)
-    uint64_t* mfull = bars + 18;       // [2] meta stage written (2 meta warps)
-    uint64_t* mfree = bars + 21;       // [2] meta stage read (8 softmax, 8 converting warps)
-    uint64_t* fin = bars + 27;
+    uint64_t* afull = bars;            // [4] A slot written (8 converting warps)
+    uint64_t* afree = bars + 4;        // [4] its QK is done (commit)
+    uint64_t* sfull = bars + 8;        // [2] S slot written (commit)
+    uint64_t* sfree = bars + 10;       // [2] S slot read (8 softmax warps)
+    uint64_t* vfull = bars + 12;       // [4] V tile written (8 converting warps)
+    uint64_t* vfree = bars + 16;       // [4] its PV is done (commit)
+    uint64_t* pfull = bars + 20;       // P written, O^T corrected (8 softmax warps)
+    uint64_t* pvdone = bars + 21;      // PV of a block done (commit)
+    uint64_t* mfull = bars + 22;       // [2] meta stage written (2 meta warps)
+    uint64_t* mfree = bars + 24;       // [2] meta stage read (8 softmax, 8 converting warps)
+    uint64_t* fin = bars + 27;         // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
 
@@ -311,9 +325,11 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     const int n_rows = min(kRows, pc.rows - pc.row0);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kASlots; ++i) {
             mbar_init(&afull[i], kConvWarps);
             mbar_init(&afree[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&sfree[i], kSoftWarps);
         }
@@ -327,7 +343,8 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             mbar_init(&mfull[i], kMetaWarps);
             mbar_init(&mfree[i], kSoftWarps + kConvWarps);
         }
-        mbar_init(fin, 1);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -356,35 +373,39 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        // Exponent-only shift so that |q| < 2^15 in f16, undone on the scores.
-        int e = 0;
-        if (mx <= FLT_MAX) frexpf(mx, &e);
-        const int k = e > 15 ? e - 15 : 0;
+        // A power of two brings the row's largest value into [2^7, 2^8); undone on the scores.
+        int e = 8;
+        if (mx <= FLT_MAX) frexpf(mx, &e);           // mx < 2^e
+        const int k = max(e - 8, -100);
         const float down = ldexpf(1.0f, -k);
         if (lane == 0) {
             const int lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
             rd.shift[r] = ldexpf(1.0f, k);
             rd.lim[r] = lim;
             rd.unseen[r] = lim > 0;
-            rd.m[r] = 0.0f;
+            rd.neg_m[r] = 0.0f;
         }
-        // Operand position of dim d of a tile: a converting thread's f16 pair m of 16 codes
-        // 64 p + 16 c .. goes to tensor-memory column 8 (m / 2) + 2 c + m % 2, so the 8 dims of
-        // a unit are two runs of 4 positions, 16 apart.
+        // Each value as an E4M3 part and the rest as an E5M2 one. Operand place of the dims: 4-byte word
+        // m of the 32 bytes that a converting thread holds of a row (16 c .. of each half) goes to tensor-memory
+        // column 8 (m / 2) + 2 c + m % 2, so the 8 dims of a unit stay together.
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t h[4];
+            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
-            const int u = lane + 32 * i, ut = u & 15;
-            const int at = 16 * (4 * (ut >> 3) + 2 * (ut & 1)) + 4 * ((ut >> 1) & 3);
-            uint8_t* q = smem + kOffQ + 2 * (u >> 4) * kQChunk;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int pos = at + 16 * j;
-                *reinterpret_cast<uint2*>(q + swz(kRows, r, pos >> 3) + ((pos & 4) << 1)) = make_uint2(h[2 * j], h[2 * j + 1]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = make_float2(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
+                const uint32_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3)));
+                const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE, __NV_E5M2);
+                hi[j >> 1] |= h << (16 * (j & 1));
+                lo[j >> 1] |= l << (16 * (j & 1));
             }
+            const int u = lane + 32 * i, ut = u & 15;
+            const int at = 4 * (16 * (ut >> 3) + 8 * (ut & 1) + 2 * ((ut >> 1) & 3));      // bytes
+            uint8_t* q = smem + kOffQ + 2 * (u >> 4) * kQChunk + swz(kRows, r, at >> 4) + (at & 8);
+            *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(q + kQChunk) = make_uint2(lo[0], lo[1]);
         }
         if (kRopeOn && lane < 8) {
             const uint32_t w[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
@@ -417,7 +438,6 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         // what is uniform over this half's query rows
         const int my_lim = rd.lim[c0 + lane];
         const int lim_min = __reduce_min_sync(0xffffffffu, my_lim);
-        const bool shifted = __any_sync(0xffffffffu, rd.shift[c0 + lane] != 1.0f);
         bool unseen = true;                            // some row has seen nothing yet: take maxima
         float l = 0.0f;                                // sum of p of query row c0 + lane, over the warp's positions
         float sig[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -453,18 +473,20 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     s[j + 8] = fma2(two(w[2 * j], w[2 * j + 1]), ff, s[j + 8]);
                 }
             }
-            float d[kCols];
-#pragma unroll
-            for (int j = 0; j < kCols / 2; ++j) {
-                d[2 * j] = lo_of(s[j]);
-                d[2 * j + 1] = hi_of(s[j]);
-            }
             // A value of the position's row that is not finite shows in its score with any finite query
             // row (0 * it is not 0), so with the first. (Looked into after the vote.)
-            const bool odd = !(fabsf(d[0]) <= FLT_MAX);
-            if (shifted) {
+            const bool odd = !(fabsf(lo_of(s[0])) <= FLT_MAX);
+            float d[kCols];
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) d[c] *= rd.shift[c0 + c];
+            for (int c = 0; c < kCols; c += 4) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&rd.shift[c0 + c]);
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&rd.neg_m[c0 + c]);
+                s[c / 2] = fma2(s[c / 2], x.x, m.x);
+                s[c / 2 + 1] = fma2(s[c / 2 + 1], x.y, m.y);
+                d[c] = lo_of(s[c / 2]);
+                d[c + 1] = hi_of(s[c / 2]);
+                d[c + 2] = lo_of(s[c / 2 + 1]);
+                d[c + 3] = hi_of(s[c / 2 + 1]);
             }
             if (__any_sync(0xffffffffu, state != 1) || kN * (b + 1) > lim_min) {
 #pragma unroll
@@ -475,21 +497,15 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             }
             float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-                const float4 m = *reinterpret_cast<const float4*>(&rd.m[c0 + c]);
-                d[c] -= m.x;
-                d[c + 1] -= m.y;
-                d[c + 2] -= m.z;
-                d[c + 3] -= m.w;
+            for (int c = 0; c < kCols; c += 4)
                 tops[(c >> 2) & 3] = fmaxf(fmaxf(tops[(c >> 2) & 3], fmaxf(d[c], d[c + 1])), fmaxf(d[c + 2], d[c + 3]));
-            }
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             // P of the block before has been read, and O^T is complete up to it.
             if (b > 0) {
                 ok = ok && warp_wait(pvdone, static_cast<uint32_t>((b - 1) & 1), abort_flag);
                 tc_after();
             }
-            const bool moved = bar_sync_or(1 + half, 128, unseen || top > kRescaleSlack || odd || !ok);
+            const bool moved = bar_sync_or(1 + half, 128, unseen || top > kTop + kRescaleSlack || odd || !ok);
             const float f0 = mt.f[0], f1 = mt.f[1], f2 = mt.f[2], f3 = mt.f[3];
             const bool sigma_moved = b > 0 && (f0 != 1.0f || f1 != 1.0f || f2 != 1.0f || f3 != 1.0f);
             if (moved) {
@@ -530,13 +546,13 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 }
                 if (quarter == 0) {
                     const int c = c0 + lane;
-                    const float up = fmaxf(fmaxf(rd.wmax[0][c], rd.wmax[1][c]), fmaxf(rd.wmax[2][c], rd.wmax[3][c]));
+                    const float up = fmaxf(fmaxf(rd.wmax[0][c], rd.wmax[1][c]), fmaxf(rd.wmax[2][c], rd.wmax[3][c])) - kTop;
                     const bool first = rd.unseen[c] != 0 && up > -INFINITY;
                     const bool move = first || up > kRescaleSlack;
                     rd.alpha[c] = move ? (first ? 0.0f : ex2_approx(-up)) : 1.0f;
                     if (first) rd.unseen[c] = 0;
                     rd.wmax[0][c] = move ? up : 0.0f;      // by how much the offset moves
-                    if (move) rd.m[c] += up;
+                    if (move) rd.neg_m[c] -= up;
                     const bool left = __any_sync(0xffffffffu, rd.unseen[c] != 0);
                     if (lane == 0) rd.any_unseen[half] = left;
                 }
@@ -603,7 +619,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 // 0: nothing attended; NaN: an attended row holds a value that is not finite
                 const float kNaN = __int_as_float(0x7FC00000);
                 rd.alpha[c] = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : kNaN);
-                const float lse = sum > 0.0f ? (rd.m[c] + log2f(sum)) * kLn2 : (sum == 0.0f ? -INFINITY : kNaN);
+                const float lse = sum > 0.0f ? (log2f(sum) - rd.neg_m[c]) * kLn2 : (sum == 0.0f ? -INFINITY : kNaN);
                 if (c < n_rows) {
                     if (pc.part < 0) args.lse[pc.grow0 + pc.row0 + c] = lse;
                     else args.part_lse[static_cast<int64_t>(pc.part) * kRows + c] = lse;
@@ -642,7 +658,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         const uint32_t a_base = tmem + (static_cast<uint32_t>(32 * quarter + 16 * hh) << 16) + kColA;
         const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
         int slot[2];
-        uint4 v[2][2];
+        uint4 v[4][2][2];                              // a block's codes; v[3] holds RoPE's values first
         bool ok = true;
         int g = 0;
         auto rows_of = [&](int b) {
@@ -651,57 +667,51 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             slot[0] = meta[b % kMeta].slot[r0];
             slot[1] = meta[b % kMeta].slot[r0 + 8];
         };
-        auto load = [&](int t) {                       // latent tile t; -1: RoPE
-            const uint32_t off = (t < 0 ? kTailOff : 128 * t) + 16 * c;
+        auto load = [&](uint4 (&x)[2][2], uint32_t off) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                v[e][0] = ld_row(args.cache, slot[e], row_bytes, off);
-                v[e][1] = ld_row(args.cache, slot[e], row_bytes, off + 64);
+                x[e][0] = ld_row(args.cache, slot[e], row_bytes, off + 16 * c);
+                x[e][1] = ld_row(args.cache, slot[e], row_bytes, off + 16 * c + 64);
             }
         };
-        constexpr int kFirst = kRopeOn ? -1 : 0;
+        auto put = [&](const uint4 (&x)[2][2]) {       // the rows' bytes as they are: an A operand of QK
+            const int as = g % kASlots;
+            if (g >= kASlots) ok = ok && warp_wait(&afree[as], static_cast<uint32_t>((g / kASlots - 1) & 1), abort_flag);
+            ++g;
+            if (!ok) return;
+            tc_after();
+            uint32_t w[16];                            // word m of row e at 4 (m / 2) + 2 e + m % 2
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    w[8 * p + 2 * e] = x[e][p].x; w[8 * p + 2 * e + 1] = x[e][p].y;
+                    w[8 * p + 4 + 2 * e] = x[e][p].z; w[8 * p + 5 + 2 * e] = x[e][p].w;
+                }
+            tmem_st_16x256_x4(a_base + 32 * as, w);
+            tc_wait_st();
+            tc_before();
+            warp_arrive(&afull[as]);
+        };
         if (nblk > 0) rows_of(0);
-        if (nblk > 0 && ok) load(kFirst);
+        if (nblk > 0 && ok) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) load(v[t], kRopeOn && t == 3 ? kTailOff : 128 * t);
+        }
         for (int b = 0; b < nblk && ok; ++b) {
             const Meta& mt = meta[b % kMeta];
-#pragma unroll 1
-            for (int t = kFirst; t < 4; ++t, ++g) {
-                const bool more = t < 3 || b + 1 < nblk;
-                if (t == 3 && more) rows_of(b + 1);
-                const int as = g & 1;
-                if (g >= 2) ok = ok && warp_wait(&afree[as], static_cast<uint32_t>(((g >> 1) - 1) & 1), abort_flag);
-                if (!ok) break;
-                tc_after();
-                uint32_t w[32];        // 16-bit pair m of row e at 4 (m / 2) + 2 e + m % 2, as they are stored
-                if (t < 0) {
+            const bool more = b + 1 < nblk;
+            if (kRopeOn) {
+                put(v[3]);
+                load(v[3], 128 * 3);
+            }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+            for (int t = 0; t < 4; ++t) put(v[t]);
+            if (more) rows_of(b + 1);
+            // V: the product with scale / sigma, once PV of the block before has read the tile
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            w[8 * p + 2 * e] = v[e][p].x; w[8 * p + 2 * e + 1] = v[e][p].y;
-                            w[8 * p + 4 + 2 * e] = v[e][p].z; w[8 * p + 5 + 2 * e] = v[e][p].w;
-                        }
-                    load(0);                           // on its way until the next tile's turn
-                    tmem_st_16x256_x4(a_base + 64 * as, w);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            e4m3x4_to_f16x2x2(v[e][p].x, w[16 * p + 2 * e], w[16 * p + 2 * e + 1]);
-                            e4m3x4_to_f16x2x2(v[e][p].y, w[16 * p + 4 + 2 * e], w[16 * p + 5 + 2 * e]);
-                            e4m3x4_to_f16x2x2(v[e][p].z, w[16 * p + 8 + 2 * e], w[16 * p + 9 + 2 * e]);
-                            e4m3x4_to_f16x2x2(v[e][p].w, w[16 * p + 12 + 2 * e], w[16 * p + 13 + 2 * e]);
-                        }
-                    tmem_st_16x256_x8(a_base + 64 * as, w);
-                    if (more) load(t < 3 ? t + 1 : kFirst);
-                }
-                tc_wait_st();
-                tc_before();
-                warp_arrive(&afull[as]);
-                if (t < 0) continue;
-                // V: the product with scale / sigma, once PV of the block before has read the tile
-                if (b > 0) ok = warp_wait(&vfree[t], static_cast<uint32_t>((b - 1) & 1), abort_flag);
+            for (int t = 0; t < 4; ++t) {
+                if (b > 0) ok = ok && warp_wait(&vfree[t], static_cast<uint32_t>((b - 1) & 1), abort_flag);
                 if (!ok) break;
                 uint8_t* tile = smem + kOffV + 2 * t * kVChunk;
 #pragma unroll
@@ -711,11 +721,14 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     for (int p = 0; p < 2; ++p)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const uint32_t* x = w + 16 * p + 8 * u + 2 * e;
+                            uint32_t x[4];
+                            e4m3x4_to_f16x2x2(u == 0 ? v[t][e][p].x : v[t][e][p].z, x[0], x[1]);
+                            e4m3x4_to_f16x2x2(u == 0 ? v[t][e][p].y : v[t][e][p].w, x[2], x[3]);
                             *reinterpret_cast<uint4*>(tile + swz(kN, r0 + 8 * e, 8 * p + 2 * c + u)) =
-                                make_uint4(hmul2(x[0], f), hmul2(x[1], f), hmul2(x[4], f), hmul2(x[5], f));
+                                make_uint4(hmul2(x[0], f), hmul2(x[1], f), hmul2(x[2], f), hmul2(x[3], f));
                         }
                 }
+                if (more) load(v[t], kRopeOn && t == 3 ? kTailOff : 128 * t);
                 fence_proxy_async_smem();
                 warp_arrive(&vfull[t]);
             }
@@ -725,39 +738,52 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     } else {
     deal_registers<kAuxRegs>();
     if (warp == kMmaWarp) {
-        // ---- MMAs, one elected thread: RoPE's QK of the next block runs beside this one's softmax ----
+        // ---- QK, one elected thread ----
         if (elect_one()) {
-            const uint32_t base = smem_u32(smem);
-            const uint64_t dq = sw128_desc(base + kOffQ, 16, 1024);
-            const uint64_t dp = sw128_desc(base + kOffP, 16, 1024);
+            const uint64_t dq = sw128_desc(smem_u32(smem) + kOffQ, 16, 1024);
+            const int n_groups = nblk * kGroups;
             bool ok = true;
-            int g = 0;
-            auto qk = [&](int t) {                     // latent tile t; -1: RoPE
-                const int slot = g & 1;
-                ok = ok && wait_or_abort(&afull[slot], static_cast<uint32_t>((g >> 1) & 1), abort_flag);
+            int t = 4 - kGroups;                       // latent tile; -1: RoPE
+#pragma unroll 1
+            for (int g = 0; g < n_groups; ++g) {
+                const int slot = g & 1, as = g % kASlots;
+                ok = wait_or_abort(&afull[as], static_cast<uint32_t>((g / kASlots) & 1), abort_flag);
                 if (g >= 2) ok = ok && wait_or_abort(&sfree[slot], static_cast<uint32_t>(((g >> 1) - 1) & 1), abort_flag);
-                if (!ok) return;
+                if (!ok) break;
                 tc_after();
-                const uint32_t d = tmem + kColS + kRows * slot, a = tmem + kColA + 64 * slot;
+                const uint32_t d = tmem + kColS + kRows * slot, a = tmem + kColA + 32 * as;
                 const uint64_t dt = dq + static_cast<uint64_t>(((t >= 0 ? 2 * t : 8) * kQChunk) >> 4);
-                const uint32_t id = t >= 0 ? kIdQK : kIdQR;
+                if (t < 0) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) umma_ts(d, a + 8 * ks, dt + static_cast<uint64_t>(2 * ks), id, ks > 0);
-                if (t >= 0) {
+                    for (int ks = 0; ks < 4; ++ks) umma_ts(d, a + 8 * ks, dt + static_cast<uint64_t>(2 * ks), kIdQR, ks > 0);
+                } else {
 #pragma unroll
-                    for (int ks = 4; ks < 8; ++ks)
-                        umma_ts(d, a + 8 * ks, dt + static_cast<uint64_t>((kQChunk >> 4) + 2 * (ks - 4)), id, true);
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ts8(d, a + 8 * (ks & 3), dt + static_cast<uint64_t>((ks >> 2) * (kQChunk >> 4) + 2 * (ks & 3)),
+                                 ks < 4 ? kIdQK : kIdQK2, ks > 0);
                 }
                 umma_commit(&sfull[slot]);
-                umma_commit(&afree[slot]);
-                ++g;
-            };
-            auto pv = [&](int b) {
-                ok = ok && wait_or_abort(pfull, static_cast<uint32_t>(b & 1), abort_flag);
+                umma_commit(&afree[as]);
+                if (++t == 4) t = 4 - kGroups;
+            }
+            // Every MMA issued has completed before tensor memory is freed.
+            umma_commit(&fin[0]);
+            (void)mbar_wait_bounded(&fin[0], 0);
+        }
+        __syncwarp();
+    } else if (warp == kPvWarp) {
+        // ---- PV, one elected thread ----
+        if (elect_one()) {
+            const uint32_t base = smem_u32(smem);
+            const uint64_t dp = sw128_desc(base + kOffP, 16, 1024);
+            bool ok = true;
+#pragma unroll 1
+            for (int b = 0; b < nblk && ok; ++b) {
+                ok = wait_or_abort(pfull, static_cast<uint32_t>(b & 1), abort_flag);
 #pragma unroll 1
                 for (int t = 0; t < 4 && ok; ++t) {
                     ok = wait_or_abort(&vfull[t], static_cast<uint32_t>(b & 1), abort_flag);
-                    if (!ok) return;
+                    if (!ok) break;
                     tc_after();
                     const uint64_t dv = sw128_desc(base + kOffV + 2 * t * kVChunk, kVChunk, 1024);
 #pragma unroll
@@ -765,18 +791,11 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                         umma_ss(tmem + kRows * t, dv + static_cast<uint64_t>(ks * 128), dp + static_cast<uint64_t>(ks * 128), kIdPV,
                                 b > 0 || ks > 0);
                     umma_commit(&vfree[t]);
+                    if (t == 3) umma_commit(pvdone);
                 }
-                umma_commit(pvdone);
-            };
-            if (kRopeOn && nblk > 0) qk(-1);
-            for (int b = 0; b < nblk && ok; ++b) {
-#pragma unroll 1
-                for (int t = 0; t < (kRopeOn && b + 1 < nblk ? 5 : 4) && ok; ++t) qk(t < 4 ? t : -1);
-                if (ok) pv(b);
             }
-            // Every MMA issued has completed before tensor memory is freed.
-            umma_commit(fin);
-            (void)mbar_wait_bounded(fin, 0);
+            umma_commit(&fin[1]);
+            (void)mbar_wait_bounded(&fin[1], 0);
         }
         __syncwarp();
     } else if (warp < kMetaWarp + kMetaWarps) {

@@ -325,6 +325,20 @@ def test_query_rows_of_very_different_sizes(n):
     run(b)
 
 
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("dim", [5, 300, 570])
+@pytest.mark.parametrize("log2", [8, 12, 16, 24])
+def test_one_large_value_in_every_query_row(n, dim, log2):
+    """Values far below their row's largest: what the many-rows kernel rounds of them (2^-21 of the largest, where
+    they are below 2^-13 of it) is within the bound, which is relative to the sum of |q| |K|."""
+    b = batch([(n, 300)], 16, 576, 16, 656, seed=17)
+    q = b["q"].double()
+    q[..., dim] = torch.where(q[..., dim] < 0, -1.0, 1.0) * 2.0 ** log2
+    b["q"] = q.to(torch.bfloat16)
+    b["scale"] = 2.0 ** -max(5, log2 - 4)
+    run(b)
+
+
 def test_a_cache_whose_offsets_pass_32_bits():
     """Rows beyond 4 GiB of the cache (7 million slots of 656 bytes)."""
     slots, page = 7_000_000, 64
