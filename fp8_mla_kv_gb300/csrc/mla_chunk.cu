@@ -171,7 +171,7 @@ chunk_plan_kernel(const ChunkArgs a) {
     // as CTAs become free and end half a piece apart. (64 sequences of 1..16,384 positions:
     // 302 pieces of at most 2,400 for 304 places, a place's share being 2,116. 24 sequences
     // of 2 x 128 heads and up to 16,384 positions: one wave would need pieces of 8,320 where
-    // a share is 5,053, so rather 456 pieces of 1,920 for 152 places: 335 us, 430 the former.)
+    // a share is 5,053, so rather more and shorter ones: 333 us, 430 the former.)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) tries[warp] = longest;
@@ -790,19 +790,21 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPiece = 128;
 constexpr int kLargeMinPiece = 256;
-// What a piece costs beside its positions, in positions, and the shortest length tried, in
-// eighths of a place's share (many rows: 2, 3 and 8 eighths at the 24 sequences above took
-// 335, 335 and 430 us; few rows fit their tiles to one wave nearly always).
-constexpr int kPieceCost = 192, kLargePieceCost = 384;
+// What a piece costs beside its positions, in positions (many rows: about 17 us, 500
+// positions; 384, 768 and 1,024 took 345, 337 and 338 us at the 24 sequences above and 90, 86 and
+// 86 at 32 mixed ones), and the shortest length tried, in eighths of a place's share (many rows: 2,
+// 3 and 8 eighths took 335, 335 and 430 us there; few rows fit their tiles to one wave
+// nearly always).
+constexpr int kPieceCost = 192, kLargePieceCost = 768;
 constexpr int kFirstEighth = 8, kLargeFirstEighth = 3;
 
 // The kernel for many rows is taken from this many query rows per sequence, on average (64
-// sequences of up to 16,384 positions: 32 rows each 243 us small, 359 large, 48 rows 388
-// and 363, 64 rows 547 and 322), and from so many (row, position) pairs at most in the
-// batch: it starts about 20 us later (4 sequences of 64 rows and up to 700 positions: 18
-// us small, 37 large).
-constexpr int kLargeFrom = 48;
-constexpr int64_t kLargeWork = 6 << 20;
+// sequences of up to 16,384 positions: 32 rows each 234 us small, 292 large, 36 rows 428
+// and 291, 64 rows 551 and 253), and from so many (row, position) pairs at most in the
+// batch: it starts about 15 us later (64 rows each, pairs in millions: 4 sequences, 0.2: 18 us
+// small, 30 large; 16 sequences, 2.9: 35 and 38; 64 sequences, 2.8: 48 and 40; 4 sequences, 5.9: 62 and 59).
+constexpr int kLargeFrom = 36;
+constexpr int64_t kLargeWork = 5 << 19;
 
 struct Sizes {
     bool large;

@@ -353,65 +353,70 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                      :: "r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (threadIdx.x < kRows) {
+        const int r = threadIdx.x, lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
+        rd.lim[r] = lim;
+        rd.unseen[r] = lim > 0;
+        rd.neg_m[r] = 0.0f;
+    }
     // ---- q of the tile's rows as operand tiles: a warp per row, lane l the 16-byte units
-    // l and l + 32 of the latent and, l < 8, unit l of RoPE ----
-    for (int r = warp; r < kRows; r += kThreads / 32) {
-        uint4 v[3];
-        v[0] = v[1] = v[2] = make_uint4(0u, 0u, 0u, 0u);
+    // l and l + 32 of the latent and, l < 8, unit l of RoPE; the next row's on their way ----
+    uint4 ahead[3];
+    auto load_q = [&](int r) {
+        ahead[0] = ahead[1] = ahead[2] = make_uint4(0u, 0u, 0u, 0u);
         if (r < n_rows) {
             const uint8_t* src = reinterpret_cast<const uint8_t*>(args.q + (pc.grow0 + pc.row0 + r) * args.d_qk);
-            v[0] = ld_nc_v4(src + 16 * lane);
-            v[1] = ld_nc_v4(src + 512 + 16 * lane);
-            if (kRopeOn && lane < 8) v[2] = ld_nc_v4(src + 1024 + 16 * lane);
+            ahead[0] = ld_nc_v4(src + 16 * lane);
+            ahead[1] = ld_nc_v4(src + 512 + 16 * lane);
+            if (kRopeOn && lane < 8) ahead[2] = ld_nc_v4(src + 1024 + 16 * lane);
         }
-        float mx = 0.0f;
+    };
+    load_q(warp);
+#pragma unroll 1
+    for (int r = warp; r < kRows; r += kThreads / 32) {
+        const uint4 v[3] = {ahead[0], ahead[1], ahead[2]};
+        load_q(r + kThreads / 32);
+        // The row's largest value (as bits: |bf16| are ordered like integers) and the power of two that
+        // brings it into [2^7, 2^8); undone on the scores.
+        uint32_t top = 0u;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        // A power of two brings the row's largest value into [2^7, 2^8); undone on the scores.
-        int e = 8;
-        if (mx <= FLT_MAX) frexpf(mx, &e);           // mx < 2^e
-        const int k = max(e - 8, -100);
-        const float down = ldexpf(1.0f, -k);
-        if (lane == 0) {
-            const int lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
-            rd.shift[r] = ldexpf(1.0f, k);
-            rd.lim[r] = lim;
-            rd.unseen[r] = lim > 0;
-            rd.neg_m[r] = 0.0f;
-        }
+        const int mx = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        const int k = mx >= 0x7f80 ? 0 : max((mx >> 7) - 134, -100);
+        const __nv_bfloat162 down = __float2bfloat162_rn(__int_as_float((127 - k) << 23));
+        if (lane == 0) rd.shift[r] = __int_as_float((127 + k) << 23);
         // Each value as an E4M3 part and the rest as an E5M2 one. Operand place of the dims: 4-byte word
         // m of the 32 bytes that a converting thread holds of a row (16 c .. of each half) goes to tensor-memory
         // column 8 (m / 2) + 2 c + m % 2, so the 8 dims of a unit stay together.
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 x = make_float2(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
-                const uint32_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3)));
-                const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE, __NV_E5M2);
-                hi[j >> 1] |= h << (16 * (j & 1));
-                lo[j >> 1] |= l << (16 * (j & 1));
+                const __half2 x = __float22half2_rn(__bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down)));
+                hi[j] = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                const __half2 y(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[j]), __NV_E4M3));
+                lo[j] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, y), __NV_SATFINITE, __NV_E5M2);
             }
             const int u = lane + 32 * i, ut = u & 15;
             const int at = 4 * (16 * (ut >> 3) + 8 * (ut & 1) + 2 * ((ut >> 1) & 3));      // bytes
             uint8_t* q = smem + kOffQ + 2 * (u >> 4) * kQChunk + swz(kRows, r, at >> 4) + (at & 8);
-            *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(q + kQChunk) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(q) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(q + kQChunk) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
         if (kRopeOn && lane < 8) {
             const uint32_t w[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
             uint32_t h[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = pack_bf16x2(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down);
+                h[j] = *reinterpret_cast<const uint32_t*>(&x);
+            }
             const int at = 16 * (2 * (lane >> 2)) + 4 * (lane & 3);
             uint8_t* q = smem + kOffQ + 8 * kQChunk;
 #pragma unroll
@@ -626,6 +631,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 }
             }
             bar_sync_or(1 + half, 128, false);
+            const int left = n_rows - c0;              // query rows of this half that there are
 #pragma unroll 1
             for (int t = 0; t < 4; ++t) {
                 uint32_t o[kCols];
@@ -637,14 +643,16 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 }
                 const float f = t == 0 ? sig[0] : t == 1 ? sig[1] : t == 2 ? sig[2] : sig[3];
                 const int dim = kTile * t + key;           // here the lane is a dim
+                if (pc.part < 0) {
+                    __nv_bfloat16* to = args.out + (pc.grow0 + pc.row0 + c0) * kLatent + dim;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    if (c0 + c >= n_rows) break;
-                    const float x = __uint_as_float(o[c]) * (f * rd.alpha[c0 + c]);
-                    if (pc.part < 0)
-                        args.out[(pc.grow0 + pc.row0 + c0 + c) * kLatent + dim] = __float2bfloat16_rn(x);
-                    else
-                        args.part_o[(static_cast<int64_t>(pc.part) * kRows + c0 + c) * kLatent + dim] = x;
+                    for (int c = 0; c < kCols; ++c)
+                        if (c < left) to[c * kLatent] = __float2bfloat16_rn(__uint_as_float(o[c]) * (f * rd.alpha[c0 + c]));
+                } else {
+                    float* to = args.part_o + (static_cast<int64_t>(pc.part) * kRows + c0) * kLatent + dim;
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+                        if (c < left) to[c * kLatent] = __uint_as_float(o[c]) * (f * rd.alpha[c0 + c]);
                 }
             }
             tc_before();
