@@ -65,9 +65,11 @@ constexpr int kSoftRegs = 104, kConvRegs = 104, kAuxRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * kLaunchRegs, "registers");
 constexpr int kCols = kRows / 2;             // query rows per softmax warp
 constexpr int kMeta = 2;                     // blocks the meta warp may be ahead
-// The exp2 offset puts the largest score at kTop (log2 units), so that f16's smallest p is 2^-32 of the
-// largest, and moves when one is kRescaleSlack above that: p <= 2^15.
-constexpr float kTop = 7.0f, kRescaleSlack = 8.0f;
+// The exp2 offset puts the largest score at kTop (log2 units) and moves when one is kRescaleSlack above
+// that: p <= 2^15, and f16's smallest p is 2^-28 of the largest (a million positions below half of that are
+// together less than the rounding of the output). A move costs most of a block: 24 sequences of
+// two tokens at 128 heads take 297, 279 and 273 us with kTop 7, 4 and 0.
+constexpr float kTop = 4.0f, kRescaleSlack = 11.0f;
 constexpr float kSigmaSlack = 64.0f;         // scale / sigma <= 2^6: code x scale / sigma < 2^15 in f16
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -539,13 +541,24 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                                 *reinterpret_cast<uint4*>(smem + kOffV + 2 * t * kVChunk + swz(kN, key, u)) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
+                // Maxima over the warp's positions, as the sums below: lane x ends with row x.
+                float v[kCols / 2];
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    float v = d[c];
-#pragma unroll
-                    for (int x = 16; x > 0; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-                    if (lane == c) rd.wmax[quarter][c0 + c] = v;
+                for (int c = 0; c < 16; ++c) {
+                    const bool up = (lane & 16) != 0;
+                    const float keep = up ? d[c + 16] : d[c], give = up ? d[c] : d[c + 16];
+                    v[c] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 16));
                 }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) {
+                    const bool up = (lane & x) != 0;
+#pragma unroll
+                    for (int c = 0; c < x; ++c) {
+                        const float keep = up ? v[c + x] : v[c], give = up ? v[c] : v[c + x];
+                        v[c] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, x));
+                    }
+                }
+                rd.wmax[quarter][c0 + lane] = v[0];
                 if (bar_sync_or(1 + half, 128, !ok)) {
                     ok = false;
                     break;
@@ -565,7 +578,13 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 bar_sync_or(1 + half, 128, false);
                 unseen = rd.any_unseen[half] != 0;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) d[c] -= rd.wmax[0][c0 + c];
+                for (int c = 0; c < kCols; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(&rd.wmax[0][c0 + c]);
+                    d[c] -= m.x;
+                    d[c + 1] -= m.y;
+                    d[c + 2] -= m.z;
+                    d[c + 3] -= m.w;
+                }
                 l *= rd.alpha[c0 + lane];
             }
             if (b > 0 && (moved || sigma_moved)) {
@@ -575,9 +594,20 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     tmem_ld32(lane_base + kRows * t + c0, o);
                     tc_wait_ld(o);
                     const float f = t == 0 ? f0 : t == 1 ? f1 : t == 2 ? f2 : f3;
+                    if (f != 1.0f) {
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c)
-                        o[c] = __float_as_uint(__uint_as_float(o[c]) * (moved ? f * rd.alpha[c0 + c] : f));
+                        for (int c = 0; c < kCols; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                    }
+                    if (moved) {
+#pragma unroll
+                        for (int c = 0; c < kCols; c += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(&rd.alpha[c0 + c]);
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * a.x);
+                            o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * a.y);
+                            o[c + 2] = __float_as_uint(__uint_as_float(o[c + 2]) * a.z);
+                            o[c + 3] = __float_as_uint(__uint_as_float(o[c + 3]) * a.w);
+                        }
+                    }
                     tmem_st32(lane_base + kRows * t + c0, o);
                 }
                 tc_wait_st();
