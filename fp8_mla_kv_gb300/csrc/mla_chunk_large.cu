@@ -222,16 +222,18 @@ __device__ __forceinline__ uint32_t swz(int rows, int r, int u) {
 
 // A bounded wait that also ends as soon as another role has given up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (int i = 0;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15) == 15) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > kWaitCycles) {
-                *abort_flag = 1;
-                return false;
-            }
+    // (the clock's upper bits are enough, in a register)
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    const int t0 = static_cast<int>(clock64() >> 16);
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (static_cast<int>(clock64() >> 16) - t0 > static_cast<int>(kWaitCycles >> 16)) {
+            *abort_flag = 1;
+            return false;
         }
     }
 }
@@ -263,8 +265,10 @@ __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(stat
 template <bool kRopeOn>
 __device__ __noinline__ bool row_is_odd(const uint8_t* row) {
     uint32_t odd = 0u;
+#pragma unroll 4
     for (int i = 0; i < kLatent / 4; ++i) odd |= ((__ldg(reinterpret_cast<const uint32_t*>(row) + i) & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
     if (kRopeOn)
+#pragma unroll 4
         for (int i = 0; i < kRope / 2; ++i)
             odd |= ((__ldg(reinterpret_cast<const uint32_t*>(row + kTailOff) + i) & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
     return odd != 0u;
@@ -496,7 +500,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 d[c + 2] = lo_of(s[c / 2 + 1]);
                 d[c + 3] = hi_of(s[c / 2 + 1]);
             }
-            if (__any_sync(0xffffffffu, state != 1) || kN * (b + 1) > lim_min) {
+            if (__builtin_expect(__any_sync(0xffffffffu, state != 1) || kN * (b + 1) > lim_min, 0)) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) {
                     if (state == 2) d[c] = __int_as_float(0x7FC00000);
@@ -516,14 +520,14 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             const bool moved = bar_sync_or(1 + half, 128, unseen || top > kTop + kRescaleSlack || odd || !ok);
             const float f0 = mt.f[0], f1 = mt.f[1], f2 = mt.f[2], f3 = mt.f[3];
             const bool sigma_moved = b > 0 && (f0 != 1.0f || f1 != 1.0f || f2 != 1.0f || f3 != 1.0f);
-            if (moved) {
+            if (__builtin_expect(moved, 0)) {
                 // Rare after the first block: maxima over the positions, new offsets for the rows
                 // whose scores ran ahead, l and O^T rescaled.
                 if (bar_sync_or(1 + half, 128, !ok)) {
                     ok = false;
                     break;
                 }
-                if (__any_sync(0xffffffffu, odd)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
                     // A query row that attends such a row gets NaN; one for which it is masked must not
                     // meet 0 * NaN in PV, so its V becomes 0.
                     const int slot = mt.slot[key];
@@ -537,6 +541,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     for (int t = 0; t < 4; ++t) {
                         ok = ok && warp_wait(&vfull[t], static_cast<uint32_t>(b & 1), abort_flag);
                         if (state == 2)
+#pragma unroll 1
                             for (int u = 0; u < 16; ++u)
                                 *reinterpret_cast<uint4*>(smem + kOffV + 2 * t * kVChunk + swz(kN, key, u)) = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -587,7 +592,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 }
                 l *= rd.alpha[c0 + lane];
             }
-            if (b > 0 && (moved || sigma_moved)) {
+            if (__builtin_expect(b > 0 && (moved || sigma_moved), 0)) {
 #pragma unroll 1
                 for (int t = 0; t < 4; ++t) {
                     uint32_t o[kCols];
@@ -845,7 +850,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         const int mw = warp - kMetaWarp;
         const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
         const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
-        float sigma[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float sigma[4] = {0.0f, 0.0f, 0.0f, 0.0f}, inv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         int slot[kPer], slot1[kPer];                   // of blocks b and b + 1
         uint4 u[kPer];                                 // their scales
         auto look_up = [&](int b) {
@@ -868,13 +873,8 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 }
             }
         };
-        if (nblk > 0) {
-            look_up(0);
-            fetch();
-            look_up(1);
-        }
-#pragma unroll 1
-        for (int b = 0; b < nblk; ++b) {
+        // Block b's stage from its slots and scales; false when the call has failed.
+        auto stage = [&](int b) {
             Meta& mt = meta[b % kMeta];
             int state[kPer];
 #pragma unroll
@@ -895,7 +895,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 for (int i = 0; i < kPer; ++i) far = far || fabsf(__uint_as_float(word4(u[i], t))) > sigma[t] * kSigmaSlack;
             const bool move = bar_sync_or(4, 32 * kMetaWarps, far || !ok);
             if (move) {
-                if (bar_sync_or(4, 32 * kMetaWarps, !ok)) break;
+                if (bar_sync_or(4, 32 * kMetaWarps, !ok)) return false;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float top = 0.0f;
@@ -907,27 +907,30 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 }
                 bar_sync_or(4, 32 * kMetaWarps, false);
             }
+            float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+            if (move) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float f = 1.0f;
-                if (move) {
+                for (int t = 0; t < 4; ++t) {
                     const float top = fmaxf(rd.smax[0][t], rd.smax[1][t]);
                     if (top > sigma[t] * kSigmaSlack) {
-                        f = sigma[t] / top;
-                        sigma[t] = top;
+                        const float now = fmaxf(top, FLT_MIN);       // its reciprocal is finite
+                        inv[t] = 1.0f / now;
+                        f[t] = sigma[t] * inv[t];
+                        sigma[t] = now;
                     }
                 }
-                const float inv = sigma[t] > 0.0f ? 1.0f / sigma[t] : 0.0f;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const int j = 32 * (kPer * mw + i) + lane;
                     const float sc = __uint_as_float(word4(u[i], t));
-                    const float r = inv <= FLT_MAX ? sc * inv : __fdiv_rn(sc, sigma[t]);
                     mt.sc[t][j] = sc;
-                    mt.rs[t][j] = static_cast<uint16_t>(pack_f16x2(r, 0.0f));
+                    mt.rs[t][j] = static_cast<uint16_t>(pack_f16x2(sc * inv[t], 0.0f));
                 }
                 if (mw == 0 && lane == 0) {
-                    mt.f[t] = f;
+                    mt.f[t] = f[t];
                     mt.sigma[t] = sigma[t];
                 }
             }
@@ -939,7 +942,12 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 mt.state[j] = static_cast<uint8_t>(state[i]);
             }
             warp_arrive(&mfull[b % kMeta]);
-            if (b + 1 < nblk) fetch();
+            return true;
+        };
+#pragma unroll 1
+        for (int b = -2; b < nblk; ++b) {
+            if (b >= 0 && !stage(b)) break;
+            if (b >= -1 && b + 1 < nblk) fetch();
             if (b + 2 < nblk) look_up(b + 2);
         }
     }
