@@ -61,8 +61,11 @@ constexpr int kPvWarp = kMetaWarp + kMetaWarps;
 constexpr int kThreads = 20 * 32;            // five warpgroups
 // Registers per thread: launched as kLaunchRegs each and dealt out again.
 constexpr int kLaunchRegs = 96;
-constexpr int kSoftRegs = 104, kConvRegs = 104, kAuxRegs = 64;
-static_assert(2 * kSoftRegs + 2 * kConvRegs + kAuxRegs <= 5 * kLaunchRegs, "registers");
+constexpr int kSoftRegs = 104;
+template <bool kRopeOn> constexpr int kConvRegs = kRopeOn ? 112 : 104;   // (104 with RoPE: 2,969 instead of 2,929 us)
+template <bool kRopeOn> constexpr int kAuxRegs = kRopeOn ? 48 : 64;      // (48 without: 84 instead of 79 us, spills)
+static_assert(2 * kSoftRegs + 2 * kConvRegs<true> + kAuxRegs<true> <= 5 * kLaunchRegs &&
+              2 * kSoftRegs + 2 * kConvRegs<false> + kAuxRegs<false> <= 5 * kLaunchRegs, "registers");
 constexpr int kCols = kRows / 2;             // query rows per softmax warp
 constexpr int kMeta = 2;                     // blocks the meta warp may be ahead
 // The exp2 offset puts the largest score at kTop (log2 units) and moves when one is kRescaleSlack above
@@ -694,7 +697,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             tc_before();
         }
     } else if (warp < kMmaWarp) {
-        deal_registers<kConvRegs>();
+        deal_registers<kConvRegs<kRopeOn>>();
         // ---- conversion: lane (rows r0 and r0 + 8, 16-byte pieces c of each 64) ----
         const int quarter = warp & 3, hh = (warp - kSoftWarps) >> 2;
         const int c = lane & 3;
@@ -780,7 +783,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             warp_arrive(&mfree[b % kMeta]);
         }
     } else {
-    deal_registers<kAuxRegs>();
+    deal_registers<kAuxRegs<kRopeOn>>();
     if (warp == kMmaWarp) {
         // ---- QK, one elected thread ----
         if (elect_one()) {
