@@ -179,7 +179,7 @@ chunk_plan_kernel(const ChunkArgs a) {
     // as CTAs become free and end half a piece apart. (64 sequences of 1..16,384 positions:
     // 302 pieces of at most 2,400 for 304 places, a place's share being 2,116. 24 sequences
     // of 2 x 128 heads and up to 16,384 positions: one wave would need pieces of 8,320 where
-    // a share is 5,053, so rather more and shorter ones: 333 us, 430 the former.)
+    // a share is 5,053, so rather more and shorter ones: 335 us, 430 the former.)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) tries[warp] = longest;
@@ -798,9 +798,8 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPiece = 128;
 constexpr int kLargeMinPiece = 256;
-// What a piece costs beside its positions, in positions (many rows: about 17 us, 500
-// positions; 384, 768 and 1,024 took 345, 337 and 338 us at the 24 sequences above and 90, 86 and
-// 86 at 32 mixed ones), and the shortest length tried, in eighths of a place's share (many rows: 2,
+// What a piece costs beside its positions, in positions (many rows: 384, 768 and 1,024
+// took 345, 337 and 338 us at the 24 sequences above and 90, 86 and 86 at 9 mixed ones), and the shortest length tried, in eighths of a place's share (many rows: 2,
 // 3 and 8 eighths took 335, 335 and 430 us there; few rows fit their tiles to one wave
 // nearly always).
 constexpr int kPieceCost = 192, kLargePieceCost = 768;

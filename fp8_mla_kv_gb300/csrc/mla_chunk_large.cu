@@ -19,8 +19,8 @@
 //        Each tile's partial goes to an S slot of its own; the softmax warps fold them with the fp32
 //        tile scales as they come. (A K rounded to f16 with its scale in it needs one
 //        accumulator but moves a score near 20 by 3.5e-3. f16 codes and f16 q, exact too, need
-//        the conversion before QK: it then waits for the tile's last PV, 3,817 us instead of 3,390 on
-//        the chunk below.)
+//        the conversion before QK: it then waits for the tile's last PV, and took 3,817 us instead of
+//        3,390 on the chunk below.)
 //   P    thread = position x 32 query rows. The exp2 offset of a row is an earlier maximum:
 //        it moves only when a score is more than kRescaleSlack above it, which one
 //        vote per block shows; only then maxima over the positions are taken.
@@ -35,12 +35,12 @@
 // left their place; each warp 16 positions), 16 issues QK, 17 and 18 walk the block table ahead
 // of them (slots, scales, sigma, prefetches into L2), 19 issues PV.
 //
-// 4,096 new tokens of 16 heads behind 12,288 positions: 3,390 us, 603 TFLOP/s, 0.31 of the
-// measured dense bf16 rate. No single unit bounds it: the tensor pipe is busy 27 % of the time, the
-// L1 and shared memory 60 % (V is written there once and read by PV, q by QK), the issue slots 49 %,
-// and a block is a chain of about a dozen hand-offs between the roles, 120 cycles each, which keeps
-// these from overlapping further. With the conversion, all but one step of each MMA, the
-// exponentials and the sums left out a block still takes 0.9 of its time.
+// 4,096 new tokens of 16 heads behind 12,288 positions: 2,940 us, 695 TFLOP/s, 0.36 of the
+// measured dense bf16 rate. What bounds it: L1 and shared memory are busy 72 % of the time (V is written
+// there once and read by PV, q and P by the MMAs, the rows come through it), the issue slots
+// 53 %, the tensor pipe 31 %; and a block is a chain of about a dozen hand-offs between the roles,
+// 120 cycles each, which keeps these from overlapping further. 24 sequences of two tokens of 128 heads
+// and up to 16,384 positions: 262 us, of which starting and ending a piece take about 12 us each of three.
 #include <cfloat>
 #include <climits>
 #include <cmath>
