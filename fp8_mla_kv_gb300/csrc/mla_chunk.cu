@@ -54,9 +54,9 @@ constexpr int kSmemMisc = 2 * kStages * 8 + kStages * 4 + 16 + 16;   // barriers
 constexpr int kSmemTotal = kSmemStages + kSmemRed + kSmemP + kSmemQmax + kSmemMisc;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The running max used as the exp2 offset is only moved when a score exceeds it
-// by more than this (log2 units): p <= 2^8 keeps the f16 P operand in range.
-constexpr float kRescaleSlack = 8.0f;
+// The exp2 offset puts the largest score at kTop (log2 units) and moves only when one is
+// kRescaleSlack above that: p <= 2^15 stays in f16's range, whose smallest is 2^-28 of the largest p.
+constexpr float kTop = 4.0f, kRescaleSlack = 11.0f;
 
 __device__ __forceinline__ float quad_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -549,7 +549,7 @@ qk_again:
                 make_float4(fmaf(acc[nt][0], sc[nt][0], accr[nt][0]), fmaf(acc[nt][1], sc[nt][1], accr[nt][1]),
                             fmaf(acc[nt][2], sc[nt][0], accr[nt][2]), fmaf(acc[nt][3], sc[nt][1], accr[nt][3]));
         // The part of PV that does not need P, ahead of the barriers: sigma (the
-        // running max of tile `warp`'s scales, so p * scale / sigma <= 2^8 in f16),
+        // running max of tile `warp`'s scales, so p * scale / sigma <= 2^15 in f16),
         // O rescaled when it moves, and the rows' scale / sigma as f16 pairs.
         float smax = 0.0f;
 #pragma unroll
@@ -618,7 +618,7 @@ qk_again:
             rmax_s[warp * kHeads + g] = bm0;
             rmax_s[warp * kHeads + g + 8] = bm1;
         }
-        const bool need = bm0 > m_ref[0] + kRescaleSlack || bm1 > m_ref[1] + kRescaleSlack;
+        const bool need = bm0 > m_ref[0] + (kTop + kRescaleSlack) || bm1 > m_ref[1] + (kTop + kRescaleSlack);
         float p[4];
         // nothing seen yet: any finite offset makes the masked scores 0
         const float off0 = m_ref[0] == -INFINITY ? 0.0f : m_ref[0];
@@ -645,8 +645,8 @@ qk_again:
                 M0 = fmaxf(M0, rmax_s[w * kHeads + g]);
                 M1 = fmaxf(M1, rmax_s[w * kHeads + g + 8]);
             }
-            const float mn0 = (M0 > m_ref[0] + kRescaleSlack) ? M0 : m_ref[0];
-            const float mn1 = (M1 > m_ref[1] + kRescaleSlack) ? M1 : m_ref[1];
+            const float mn0 = (M0 > m_ref[0] + (kTop + kRescaleSlack)) ? M0 - kTop : m_ref[0];
+            const float mn1 = (M1 > m_ref[1] + (kTop + kRescaleSlack)) ? M1 - kTop : m_ref[1];
             const float a0 = mn0 == m_ref[0] ? 1.0f : ex2_approx(m_ref[0] - mn0);     // -inf -> 0
             const float a1 = mn1 == m_ref[1] ? 1.0f : ex2_approx(m_ref[1] - mn1);
 #pragma unroll
