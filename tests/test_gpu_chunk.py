@@ -376,3 +376,45 @@ def test_refusals():
         M.mla_chunk_attention(t["q"].cpu(), *args[1:], 16, 0.1)
     with pytest.raises(AssertionError):
         M.mla_chunk_attention(t["q"].repeat(1, 1, 2)[..., :576], *args[1:], 16, 0.1)
+
+
+@pytest.mark.parametrize("seqs", [[(40, 9000)], [(3, 20000), (40, 700)], [(1, 30000), (1, 5), (9, 12000)]], ids=str)
+@pytest.mark.parametrize("row,d_qk", [(656, 576), (528, 512)])
+def test_long_contexts_cut_into_pieces(seqs, row, d_qk):
+    run(batch(seqs, 16, d_qk, 64, row, seed=18))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_one_high_score_over_many_low_ones(n):
+    """Half of the softmax in one position, the other half spread over thousands, each 2^-12 of it and less."""
+    b = batch([(n, 4000)], 16, 576, 64, 656, seed=19)
+    b["q"] = torch.zeros_like(b["q"])
+    b["q"][..., 512] = 1.0
+    rope = b["cache"][:, 528:].view(torch.bfloat16)
+    rope[:, 0] = 0.0
+    page = int(b["table"][0, 20])
+    rope[page * 64 + 11, 0] = math.log(4000.0)              # the position 20 * 64 + 11
+    b["scale"] = 1.0
+    run(b, causal=False)
+
+
+def test_two_calls_at_once():
+    """Many and few rows on two streams over one cache, a workspace each, again and again."""
+    b = batch([(40, 900), (40, 1100)], 16, 576, 64, 656, seed=20)
+    want = call(b)
+    few = dict(b, q=b["q"][:2].contiguous(), q_start=torch.tensor([0, 1, 2], dtype=torch.int32))
+    want_few = call(few)
+    calls = []
+    for c, w in ((b, want), (few, want_few)):
+        t = {k: v.to(D) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+        calls.append((torch.cuda.Stream(), t, M.alloc_chunk_workspace(t["q"].shape[0], 16, 2), w, []))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, t, ws, _, got in calls:
+            got.append(M.mla_chunk_attention(t["q"], t["cache"], t["q_start"], t["kv_len"], t["table"], 64, t["scale"],
+                                             workspace=ws, stream=s))
+    torch.cuda.synchronize()
+    assert M.mla_get_error() == 0
+    for _, _, _, (wo, wl), got in calls:
+        for o, l in got:
+            assert torch.equal(o.view(torch.int16), wo.view(torch.int16)) and torch.equal(l, wl)
