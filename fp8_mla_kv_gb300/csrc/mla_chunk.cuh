@@ -25,12 +25,14 @@ struct ChunkArgs {
     int T, H, d_qk, causal;
     float sm_scale_log2;
     int* err;
-    // The plan (workspace): exclusive prefixes over the sequences, and pieces per tile.
+    // The plan (workspace): an order of the sequences, exclusive prefixes in that order, and pieces per
+    // tile.
     int tile_rows, tile_shift;         // query rows per tile, a power of two
     int align;                         // positions per block, a power of two: pieces start at multiples of it
     int wave;                          // pieces that fill the GPU once
     int min_piece, first_eighth;       // shortest pieces: positions, eighths of a wave-th of the work
     int piece_cost;                    // of a piece, beside its positions
+    int32_t* order;                    // [n_seq] sequences; longest pieces first, where there is more than a wave
     int32_t* piece0;                   // [n_seq + 1] pieces
     int32_t* part0;                    // [n_seq + 1] pieces of split tiles
     int32_t* mrow0;                    // [n_seq + 1] query rows of split tiles
@@ -97,10 +99,11 @@ __device__ __forceinline__ Piece find_piece(const ChunkArgs& a, int b, int lane)
     Piece p;
     p.seq = -1;
     if (b >= a.piece0[a.n_seq]) return p;
-    p.seq = find_seq(a.piece0, a.n_seq, b, lane);
+    const int at = find_seq(a.piece0, a.n_seq, b, lane);
+    p.seq = a.order[at];
     p.s = load_seq(a, p.seq);
-    const int nk = a.split[p.seq];
-    const int local = b - a.piece0[p.seq];
+    const int nk = a.split[at];
+    const int local = b - a.piece0[at];
     p.rows = p.s.n * a.H;
     const int tiles = tiles_of(a, p.s);
     const int back = local / nk;
@@ -113,7 +116,7 @@ __device__ __forceinline__ Piece find_piece(const ChunkArgs& a, int b, int lane)
     const int per = ((lim + nk - 1) / nk + a.align - 1) & ~(a.align - 1);
     p.k0 = static_cast<int>(min(static_cast<int64_t>(lim), static_cast<int64_t>(k) * per));
     p.k1 = min(lim, p.k0 + per);
-    p.part = nk > 1 ? a.part0[p.seq] + tile * nk + k : -1;
+    p.part = nk > 1 ? a.part0[at] + tile * nk + k : -1;
     return p;
 }
 
