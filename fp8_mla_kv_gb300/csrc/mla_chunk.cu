@@ -176,11 +176,10 @@ chunk_plan_kernel(const ChunkArgs a) {
     }
     work = plan_sum(work, buf);                        // (its barriers order the stores above, too)
     // Each warp counts the pieces of one C; the one with the least estimate is taken: pieces that
-    // fit one wave end with the longest, more of them (each at piece_cost more) are dealt out
-    // as CTAs become free and end half a piece apart. (64 sequences of 1..16,384 positions:
-    // 302 pieces of at most 2,400 for 304 places, a place's share being 2,116. 24 sequences
-    // of 2 x 128 heads and up to 16,384 positions: one wave would need pieces of 8,320 where
-    // a share is 5,053, so rather more and shorter ones: 335 us, 430 the former.)
+    // fit one wave end with the longest, more of them (each at piece_cost more) come in waves of
+    // average ones. (One token each, 200 sequences of up to 16,384 positions: 249 us, 319 when pieces were at
+    // least a place's share; 24 sequences of 2 x 128 heads: 246 and 430. An estimate of all work by the places and
+    // half a piece instead of whole waves: 285 and 247.)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) tries[warp] = longest;
@@ -195,7 +194,7 @@ chunk_plan_kernel(const ChunkArgs a) {
         if (lane == 0) counts[warp] = n;
         if (lane == 0)
             cost[warp] = n <= a.wave ? cut + static_cast<int64_t>(a.piece_cost)
-                                     : (work + static_cast<int64_t>(n) * a.piece_cost) / a.wave + cut / 2;
+                                     : (n + a.wave - 1) / a.wave * (work / n + a.piece_cost);
     }
     __syncthreads();
     int best = 0;
@@ -825,20 +824,20 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPiece = 128;
 constexpr int kLargeMinPiece = 256;
-// What a piece costs beside its positions, in positions (many rows: 384, 768 and 1,024
-// took 345, 337 and 338 us at the 24 sequences above and 90, 86 and 86 at 9 mixed ones), and the shortest length tried, in eighths of a place's share (many rows: 2,
-// 3 and 8 eighths took 335, 335 and 430 us there; few rows fit their tiles to one wave
-// nearly always).
-constexpr int kPieceCost = 192, kLargePieceCost = 768;
-constexpr int kFirstEighth = 8, kLargeFirstEighth = 3;
+// What a piece costs beside its positions, in positions (few rows: 192 took 146 us for 90 sequences of up to
+// 16,384, 300 and 400 140; many: 384 to 640 are alike), and the shortest length tried, in eighths of
+// a place's share (few rows: 3 and 4 alike, 8 took 319 instead of 249 us for 200 sequences; many: 2 and 3
+// alike, 8 took 430 instead of 335 for the 24).
+constexpr int kPieceCost = 300, kLargePieceCost = 512;
+constexpr int kFirstEighth = 4, kLargeFirstEighth = 3;
 
 // The kernel for many rows is taken from this many query rows per sequence, on average (64
-// sequences of up to 16,384 positions: 32 rows each 234 us small, 292 large, 36 rows 428
-// and 291, 64 rows 551 and 253), and from so many (row, position) pairs at most in the
-// batch: it starts about 15 us later (64 rows each, pairs in millions: 4 sequences, 0.2: 18 us
-// small, 30 large; 16 sequences, 2.9: 35 and 38; 64 sequences, 2.8: 48 and 40; 4 sequences, 5.9: 62 and 59).
+// sequences of up to 16,384 positions: 32 rows each 211 us small, 270 large, 36 rows 292
+// and 270, 64 rows 418 and 247), and from so many (row, position) pairs at most in the
+// batch: it starts about 10 us later (64 rows each, pairs in millions: 4 sequences, 1.5: 29 us
+// small, 34 large, 2.9: 41 and 43, 5.9: 62 and 59; 64 sequences, 2.8: 39 and 38).
 constexpr int kLargeFrom = 36;
-constexpr int64_t kLargeWork = 5 << 19;
+constexpr int64_t kLargeWork = 4 << 20;
 
 struct Sizes {
     bool large;
