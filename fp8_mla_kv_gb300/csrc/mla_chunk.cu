@@ -149,6 +149,10 @@ chunk_plan_kernel(const ChunkArgs a) {
     __shared__ int64_t cost[kPlanTries];
     __shared__ int tries[kPlanTries], counts[kPlanTries];
     __shared__ int lengths[kPlanThreads], place[kPlanThreads];
+    __shared__ int32_t tiles_s[kPlanThreads], lens_s[kPlanThreads];
+    // Each sequence's tiles and mean length, until the prefixes take their place.
+    int32_t* const tile_counts = a.n_seq <= kPlanThreads ? tiles_s : a.part0;
+    int32_t* const lens = a.n_seq <= kPlanThreads ? lens_s : a.mrow0;
     pdl_wait();
     pdl_launch_dependents();
     // A sequence is taken if its start is not below any earlier one, nor its end below its
@@ -169,8 +173,8 @@ chunk_plan_kernel(const ChunkArgs a) {
         if (!taken || static_cast<int64_t>(q.len) > static_cast<int64_t>(a.max_pages) * a.page_size)
             atomicOr(a.err, MLA_ERR_CHUNK_RANGE);
         const int tiles = taken ? tiles_of(a, q) : 0, len = mean_limit(a, q);
-        a.part0[s] = tiles;                            // for the next step; the prefixes come last
-        a.mrow0[s] = len;
+        tile_counts[s] = tiles;
+        lens[s] = len;
         if (tiles > 0) longest = max(longest, len);
         work += static_cast<int64_t>(tiles) * len;
     }
@@ -189,7 +193,7 @@ chunk_plan_kernel(const ChunkArgs a) {
     {
         const int c = try_piece(a, share, warp), cut = min(c, longest);
         int n = 0;
-        for (int s = lane; s < a.n_seq; s += 32) n += a.part0[s] * pieces_of(a.mrow0[s], c);
+        for (int s = lane; s < a.n_seq; s += 32) n += tile_counts[s] * pieces_of(lens[s], c);
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) counts[warp] = n;
         if (lane == 0)
@@ -208,8 +212,8 @@ chunk_plan_kernel(const ChunkArgs a) {
     const bool sorted = a.n_seq <= kPlanThreads && counts[best] > a.wave;
     if (sorted) {
         int mine = -1;
-        if (threadIdx.x < a.n_seq && a.part0[threadIdx.x] > 0) {
-            const int len = a.mrow0[threadIdx.x];
+        if (threadIdx.x < a.n_seq && tile_counts[threadIdx.x] > 0) {
+            const int len = lens[threadIdx.x];
             mine = len / pieces_of(len, C);
         }
         lengths[threadIdx.x] = mine;
@@ -230,8 +234,8 @@ chunk_plan_kernel(const ChunkArgs a) {
         const int s = sorted && i < a.n_seq ? place[i] : i;
         int nk = 1, pieces = 0, parts = 0, rows = 0;
         if (i < a.n_seq) {
-            const int tiles = a.part0[s];
-            if (tiles > 0) nk = pieces_of(a.mrow0[s], C);
+            const int tiles = tile_counts[s];
+            if (tiles > 0) nk = pieces_of(lens[s], C);
             pieces = tiles * nk;
             if (nk > 1) {
                 parts = pieces;
