@@ -249,7 +249,7 @@ chunk_plan_kernel(const ChunkArgs a) {
         q_base += all;
         const int r = plan_scan(rows, all, buf) + r_base;
         r_base += all;
-        if (i < a.n_seq) {                             // (all of this round's have been read: the scans' barriers)
+        if (i < a.n_seq) {                             // (those of this step have been read: the scans' barriers)
             a.order[i] = s;
             a.piece0[i] = p;
             a.part0[i] = k;
