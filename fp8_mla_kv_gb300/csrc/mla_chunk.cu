@@ -265,18 +265,25 @@ chunk_plan_kernel(const ChunkArgs a) {
 }
 
 // Joins the partials of the split tiles' rows in piece order: lse = ln sum exp(lse_k),
-// out = sum exp(lse_k - lse) o_k; a NaN partial makes both NaN. A CTA takes a row at a
-// time, thread x dims 4x .. 4x + 3, the loads of kMergeBatch pieces together.
-constexpr int kMergeBatch = 8;
+// out = sum exp(lse_k - lse) o_k; a NaN partial makes both NaN. kPerRow warps take a row at a
+// time, thread x of a warp dims 128 j + 4x .. 4x + 3, the loads of a few pieces together. Bound by
+// the latency of a row's dependent loads (its place, the pieces' lse, their values): four warps a row
+// where the GPU holds them all at once (4 sequences: 17.4 us with the rest of the call, 18.6 with one),
+// one where that would take several turns (9 sequences of 10,000 rows: 72.3 us with one, 79.8 with four).
+constexpr int kMergeWarps = 4;
 
-__global__ void __launch_bounds__(128)
+template <int kPerRow>
+__global__ void __launch_bounds__(32 * kMergeWarps)
 mla_chunk_merge_kernel(const ChunkArgs a) {
+    constexpr int kDims = kMergeWarps / kPerRow;       // float4 per thread
+    constexpr int kBatch = kPerRow == 1 ? 4 : 8;       // pieces whose loads are on their way together
+    constexpr int kRows = kMergeWarps / kPerRow;       // rows of a CTA
+    const int warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int d = 4 * threadIdx.x;
     const int total = a.mrow0[a.n_seq];
-    for (int r = blockIdx.x; r < total; r += gridDim.x) {
+    for (int r = blockIdx.x * kRows + warp / kPerRow; r < total; r += gridDim.x * kRows) {
         const int at = find_seq(a.mrow0, a.n_seq, r, lane);
         const int s = a.order[at];
         const int local = r - a.mrow0[at];
@@ -287,48 +294,58 @@ mla_chunk_merge_kernel(const ChunkArgs a) {
         const int64_t grow = static_cast<int64_t>(__ldg(a.q_start + s)) * a.H + local;
         float mx = -INFINITY;
         bool nan = false;
-        for (int s0 = 0; s0 < np; s0 += kMergeBatch) {
-            float ls[kMergeBatch];
+        for (int s0 = 0; s0 < np; s0 += kBatch) {
+            float ls[kBatch];
 #pragma unroll
-            for (int q = 0; q < kMergeBatch; ++q)
+            for (int q = 0; q < kBatch; ++q)
                 ls[q] = (s0 + q < np) ? a.part_lse[row0 + static_cast<int64_t>(s0 + q) * a.tile_rows] : -INFINITY;
 #pragma unroll
-            for (int q = 0; q < kMergeBatch; ++q) {
+            for (int q = 0; q < kBatch; ++q) {
                 mx = fmaxf(mx, ls[q]);
                 nan = nan || ls[q] != ls[q];
             }
         }
         float wsum = 0.0f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mx != -INFINITY && !nan) {
-            for (int s0 = 0; s0 < np; s0 += kMergeBatch) {
-                float ls[kMergeBatch];
-                float4 v[kMergeBatch];
+        float4 acc[kDims];
 #pragma unroll
-                for (int q = 0; q < kMergeBatch; ++q) {
+        for (int j = 0; j < kDims; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mx != -INFINITY && !nan) {
+            for (int s0 = 0; s0 < np; s0 += kBatch) {
+                float ls[kBatch];
+                float4 v[kBatch][kDims];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
                     const int64_t prow = row0 + static_cast<int64_t>(min(s0 + q, np - 1)) * a.tile_rows;
                     ls[q] = (s0 + q < np) ? a.part_lse[prow] : -INFINITY;
                     // A piece with nothing attended (lse -inf) left its o unwritten.
-                    v[q] = (ls[q] == -INFINITY) ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                : *reinterpret_cast<const float4*>(a.part_o + prow * kLatent + d);
+#pragma unroll
+                    for (int j = 0; j < kDims; ++j)
+                        v[q][j] = (ls[q] == -INFINITY)
+                                      ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                      : *reinterpret_cast<const float4*>(a.part_o + prow * kLatent + 128 * (kPerRow == 1 ? j : warp) + 4 * lane);
                 }
 #pragma unroll
-                for (int q = 0; q < kMergeBatch; ++q) {
+                for (int q = 0; q < kBatch; ++q) {
                     const float w = (ls[q] == -INFINITY) ? 0.0f : expf(ls[q] - mx);
                     wsum += w;
-                    acc.x = fmaf(w, v[q].x, acc.x);
-                    acc.y = fmaf(w, v[q].y, acc.y);
-                    acc.z = fmaf(w, v[q].z, acc.z);
-                    acc.w = fmaf(w, v[q].w, acc.w);
+#pragma unroll
+                    for (int j = 0; j < kDims; ++j) {
+                        acc[j].x = fmaf(w, v[q][j].x, acc[j].x);
+                        acc[j].y = fmaf(w, v[q][j].y, acc[j].y);
+                        acc[j].z = fmaf(w, v[q][j].z, acc[j].z);
+                        acc[j].w = fmaf(w, v[q][j].w, acc[j].w);
+                    }
                 }
             }
         }
         float lse = mx + logf(wsum), inv = 1.0f / wsum;
         if (mx == -INFINITY) { lse = -INFINITY; inv = 0.0f; }
         if (nan) lse = inv = __int_as_float(0x7FC00000);
-        *reinterpret_cast<uint2*>(a.out + grow * kLatent + d) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (threadIdx.x == 0) a.lse[grow] = lse;
+#pragma unroll
+        for (int j = 0; j < kDims; ++j)
+            *reinterpret_cast<uint2*>(a.out + grow * kLatent + 128 * (kPerRow == 1 ? j : warp) + 4 * lane) =
+                make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+        if (lane == 0 && warp % kPerRow == 0) a.lse[grow] = lse;
     }
 }
 
@@ -968,7 +985,8 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
                     : rope  ? launch(mla_chunk_small_kernel<true>, z.max_pieces, kThreads, kSmemTotal, stream, a)
                             : launch(mla_chunk_small_kernel<false>, z.max_pieces, kThreads, kSmemTotal, stream, a);
     if (!ok) return MLA_ECUDA;
-    int64_t merge = static_cast<int64_t>(T) * H;
-    if (merge > static_cast<int64_t>(sms) * 16) merge = static_cast<int64_t>(sms) * 16;
-    return launch(mla_chunk_merge_kernel, merge, 128, 0, stream, a) ? MLA_OK : MLA_ECUDA;
+    const int64_t rows = static_cast<int64_t>(T) * H, held = static_cast<int64_t>(sms) * 16;
+    if (rows <= held) return launch(mla_chunk_merge_kernel<4>, rows, 32 * kMergeWarps, 0, stream, a) ? MLA_OK : MLA_ECUDA;
+    const int64_t ctas = (rows + kMergeWarps - 1) / kMergeWarps;
+    return launch(mla_chunk_merge_kernel<1>, ctas < held ? ctas : held, 32 * kMergeWarps, 0, stream, a) ? MLA_OK : MLA_ECUDA;
 }

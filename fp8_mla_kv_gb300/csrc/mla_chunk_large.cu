@@ -40,7 +40,7 @@
 // there once and read by PV, q and P by the MMAs, the rows come through it), the issue slots
 // 53 %, the tensor pipe 31 %; and a block is a chain of about a dozen hand-offs between the roles,
 // 120 cycles each, which keeps these from overlapping further. 24 sequences of two tokens of 128 heads
-// and up to 16,384 positions: 247 us, of which starting and ending a piece take about 12 us each of three.
+// and up to 16,384 positions: 242 us, of which starting and ending a piece take about 12 us each of three.
 #include <cfloat>
 #include <climits>
 #include <cmath>
