@@ -269,7 +269,7 @@ chunk_plan_kernel(const ChunkArgs a) {
 // time, thread x of a warp dims 128 j + 4x .. 4x + 3, the loads of a few pieces together. Bound by
 // the latency of a row's dependent loads (its place, the pieces' lse, their values): four warps a row
 // where the GPU holds them all at once (4 sequences: 17.4 us with the rest of the call, 18.6 with one),
-// one where that would take several turns (9 sequences of 10,000 rows: 72.3 us with one, 79.8 with four).
+// one where that would take several turns (9 sequences, 7,664 rows: 72.3 us with one, 79.8 with four).
 constexpr int kMergeWarps = 4;
 
 template <int kPerRow>
