@@ -206,6 +206,11 @@ int check_rope(const mla_rope_t* rope) {
     return MLA_OK;
 }
 
+// Axes are apart, or one row of positions that all of them read.
+bool axes_ok(int n_axes, int64_t pos_stride, int64_t n_rows) {
+    return n_axes == 1 || pos_stride == 0 || pos_stride >= n_rows;
+}
+
 // Strided view of rows x heads x 64 values: every 16-byte piece aligned. Strides of a
 // single row or head are never used.
 bool view_ok(const void* p, int64_t row, int64_t head, int64_t rows, int heads) {
@@ -269,7 +274,7 @@ extern "C" int mla_rope(const void* x_bf16, int64_t x_row, int64_t x_head, void*
     if (const int rc = check_rope(rope)) return rc;
     if (n_rows == 0 || n_heads == 0) return MLA_OK;
     if (!view_ok(x_bf16, x_row, x_head, n_rows, n_heads) || !view_ok(y_bf16, y_row, y_head, n_rows, n_heads) ||
-        pos == nullptr || !aligned(pos, 4) || (rope->n_axes > 1 && pos_stride < n_rows))
+        pos == nullptr || !aligned(pos, 4) || !axes_ok(rope->n_axes, pos_stride, n_rows))
         return MLA_EINVAL;
     RotArgs a = {static_cast<const uint16_t*>(x_bf16), static_cast<uint16_t*>(y_bf16), x_row, x_head, y_row, y_head,
                  pos, pos_stride, n_rows, n_heads, 0, 0};
@@ -289,7 +294,7 @@ extern "C" int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, con
     if (kv.data == nullptr || slot_idx == nullptr || latent_bf16 == nullptr || k_pe_bf16 == nullptr || pos == nullptr)
         return MLA_EINVAL;
     if (!aligned(kv.data, 16) || !aligned(latent_bf16, 16) || !aligned(k_pe_bf16, 4) || !aligned(slot_idx, 8) ||
-        !aligned(pos, 4) || (rope->n_axes > 1 && pos_stride < n_rows))
+        !aligned(pos, 4) || !axes_ok(rope->n_axes, pos_stride, n_rows))
         return MLA_EINVAL;
     if ((q_bf16 == nullptr) != (q_out_bf16 == nullptr)) return MLA_EINVAL;
     if (q_bf16 != nullptr && n_heads > 0 &&

@@ -334,13 +334,18 @@ def _same_device(*ts) -> None:
 
 
 def _positions(pos: torch.Tensor, n: int, n_axes: int) -> int:
-    """Checks positions int32 [n] or [axes, n]; returns the stride between axes."""
+    """Checks positions int32 [n] or [axes, n]; returns the stride between axes (0: one row of positions for all)."""
     shape = pos.shape
     if pos.dtype != torch.int32 or len(shape) not in (1, 2) or shape[-1] != n or (n > 1 and pos.stride(-1) != 1):
         raise ValueError("positions must be int32 [n] or [axes, n], contiguous along n")
     if (1 if len(shape) == 1 else shape[0]) < n_axes:
         raise ValueError(f"positions for {n_axes} axes expected")
-    return n if len(shape) == 1 else max(n, pos.stride(0))
+    if n_axes == 1:
+        return 0                                            # never used
+    stride = pos.stride(0)
+    if 0 < stride < n:
+        raise ValueError("the axes of positions may not overlap, unless they are one row for all (stride 0)")
+    return stride
 
 
 def _rope_view(x: torch.Tensor, n: int):
@@ -356,7 +361,7 @@ def _rope_view(x: torch.Tensor, n: int):
 def mla_rope(x: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, out: torch.Tensor | None = None,
              stream=None) -> torch.Tensor:
     """Rotates x bf16 [n, heads, 64] (or [n, 64], any row and head strides that are multiples of 8) by positions
-    int32 [n] or [axes, n]; out may be x."""
+    int32 [n] or [axes, n] (a broadcast row, pos.expand(3, n), too); out may be x."""
     if out is None:
         with _on(stream):
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)

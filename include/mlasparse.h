@@ -330,7 +330,7 @@ typedef struct {
  *                   or one head)
  *   n_rows, n_heads >= 0 (0 launches nothing)
  *   pos             int32 [n_axes, n_rows], device; axis k at pos + k * pos_stride
- *                   (pos_stride >= n_rows when n_axes > 1)
+ *                   (with n_axes > 1: pos_stride >= n_rows, or 0 for one row that all axes read)
  * Launched with programmatic stream serialization like the writer.
  * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
  */
