@@ -495,9 +495,10 @@ mla_chunk_small_kernel(const ChunkArgs args) {
         qmax_s[warp * kHeads + g + 8] = qm[1];
     }
     bar_sync_or(1, kConsumerThreads, false);
-    // Exponent-only rescale so that |q| < 2^15 in f16 (exact in f16's normal
-    // range); the same power of two scales the RoPE part, and is undone on the
-    // scores through the per-row softmax factor.
+    // A power of two per row brings its largest |q| into [2^7, 2^15): f16's range then holds every value
+    // of at least 2^-17 exactly (8 bits of BF16, f16's smallest step is 2^-24), so down to 2^-24 of the row's
+    // largest; a smaller one is off by at most 2^-25, 2^-32 of the largest. The RoPE part takes the same power,
+    // which is undone on the scores through the per-row softmax factor.
     float qdown[2], rowf[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -506,7 +507,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, qmax_s[w * kHeads + g + 8 * r]);
         int e = 0;
         if (mx <= FLT_MAX) frexpf(mx, &e);           // mx < 2^e
-        const int k = (e > 15) ? (e - 15) : 0;
+        const int k = e > 15 ? e - 15 : e < 8 ? max(e - 8, -126) : 0;
         qdown[r] = ldexpf(1.0f, -k);
         rowf[r] = args.sm_scale_log2 * ldexpf(1.0f, k);
     }

@@ -396,7 +396,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
         }
         const int mx = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        const int k = mx >= 0x7f80 ? 0 : max((mx >> 7) - 134, -100);
+        const int k = mx >= 0x7f80 ? 0 : max((mx >> 7) - 134, -126);
         const __nv_bfloat162 down = __float2bfloat162_rn(__int_as_float((127 - k) << 23));
         if (lane == 0) rd.shift[r] = __int_as_float((127 + k) << 23);
         // Each value as an E4M3 part and the rest as an E5M2 one. Operand place of the dims: 4-byte word

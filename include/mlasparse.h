@@ -374,8 +374,9 @@ int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* la
  * gets out = 0 and lse = -inf. A row that holds a value that is not finite (a NaN code, a NaN
  * or infinite scale or RoPE value) makes out and lse NaN for exactly the tokens that
  * attend it; a query row that holds one gets unspecified values, and no other row does.
- * Scores are sums in fp32 of exact products, except that in batches of many query rows per
- * sequence q values below 2^-13 of their row's largest are rounded, to 2^-21 of that.
+ * Scores are sums in fp32 of exact products, except that q values far below their row's
+ * largest are rounded: below 2^-24 of it, to 2^-32 of it; in batches of many query rows per
+ * sequence below 2^-13 of it, to 2^-21 of it (largest values of 2^-119 and more).
  * Tokens outside every sequence keep their out and lse. The result does not
  * depend on what slot 0, absent pages or positions past kv_len hold.
  *

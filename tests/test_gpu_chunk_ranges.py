@@ -1,0 +1,78 @@
+"""mla_chunk_attention at the ends of its ranges: small queries, scales far apart, contexts near 2^31 positions. Every
+case for few query rows (one token a sequence) and for many."""
+import math
+
+import pytest
+import torch
+
+from fp8_mla_kv_gb300 import mlasparse as M
+
+import _plain as P
+
+pytestmark = pytest.mark.gpu
+D = "cuda:0"
+MANY = 8_000_000                     # pairs of query rows and positions that are many for the choice of the kernel
+
+
+def batch(seqs, H, d_qk, page, row, seed):
+    """seqs: (new tokens, context length). Random pages, a table wide enough for the kernel for many rows where the
+    rows are many."""
+    g = torch.Generator().manual_seed(seed)
+    pages = [-(-L // page) for _, L in seqs]
+    cache = P.make_cache((sum(pages) + 2) * page, row, g, rope=d_qk == 576)
+    order = torch.randperm(sum(pages) + 1, generator=g).to(torch.int32) + 1
+    T = sum(n for n, _ in seqs)
+    width = max(pages) + 2
+    if T * H >= 64 * len(seqs):
+        width = max(width, MANY // (T * H * page) + 1)
+    table = torch.full((len(seqs), width), -1, dtype=torch.int32)
+    at = 0
+    for i, k in enumerate(pages):
+        table[i, :k] = order[at:at + k]
+        at += k
+    start = torch.tensor([0] + [n for n, _ in seqs], dtype=torch.int32).cumsum(0).to(torch.int32)
+    return dict(q=torch.randn((T, H, d_qk), generator=g).to(torch.bfloat16), cache=cache, q_start=start,
+                kv_len=torch.tensor([L for _, L in seqs], dtype=torch.int32), table=table, page=page,
+                scale=1.0 / math.sqrt(d_qk))
+
+
+def call(b, causal=True):
+    t = {k: v.to(D) if isinstance(v, torch.Tensor) else v for k, v in b.items()}
+    out, lse = M.mla_chunk_attention(t["q"], t["cache"], t["q_start"], t["kv_len"], t["table"], t["page"], t["scale"],
+                                     causal=causal)
+    torch.cuda.synchronize()
+    assert M.mla_get_error() == 0
+    return out, lse
+
+
+def ref(b, causal=True):
+    return P.chunk(b["q"], b["cache"], b["q_start"], b["kv_len"], b["table"], b["page"], b["scale"], causal)
+
+
+def run(b, causal=True):
+    P.check_chunk(*call(b, causal), ref(b, causal))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("d_qk,row", [(576, 656), (512, 528)])
+@pytest.mark.parametrize("log2", [-10, -14, -20, -24, -40, -90])
+def test_small_query_rows(n, d_qk, row, log2):
+    """Every query row small, and a softmax scale that makes its scores as large as usual."""
+    b = batch([(n, 300), (n, 77)], 16, d_qk, 16, row, seed=1)
+    b["q"] = (b["q"].double() * 2.0 ** log2).to(torch.bfloat16)
+    b["scale"] = 2.0 ** -log2 / 24
+    run(b)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_rows_of_equal_scores_at_any_size(n):
+    """Powers of two that q and the softmax scale give and take change nothing, bit for bit."""
+    b = batch([(n, 300)], 16, 576, 16, 656, seed=2)
+    # (f16's range holds these values exactly at every one of the sizes)
+    b["q"] = torch.where(b["q"].abs() < 2.0 ** -9, torch.zeros_like(b["q"]), b["q"])
+    want = call(b)
+    q, scale = b["q"], b["scale"]
+    for log2 in (-60, -24, -8, 3, 20):
+        b["q"], b["scale"] = (q.double() * 2.0 ** log2).to(torch.bfloat16), scale * 2.0 ** -log2
+        out, lse = call(b)
+        assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
