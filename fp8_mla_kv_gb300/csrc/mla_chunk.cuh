@@ -115,7 +115,7 @@ __device__ __forceinline__ Piece find_piece(const ChunkArgs& a, int b, int lane)
     const int lim = token_limit(a, p.s, last / a.H);
     const int per = ((lim + nk - 1) / nk + a.align - 1) & ~(a.align - 1);
     p.k0 = static_cast<int>(min(static_cast<int64_t>(lim), static_cast<int64_t>(k) * per));
-    p.k1 = min(lim, p.k0 + per);
+    p.k1 = static_cast<int>(min(static_cast<int64_t>(lim), static_cast<int64_t>(p.k0) + per));   // (k0 + per may pass 2^31)
     p.part = nk > 1 ? a.part0[at] + tile * nk + k : -1;
     return p;
 }

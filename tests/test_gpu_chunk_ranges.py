@@ -76,3 +76,30 @@ def test_rows_of_equal_scores_at_any_size(n):
         b["q"], b["scale"] = (q.double() * 2.0 ** log2).to(torch.bfloat16), scale * 2.0 ** -log2
         out, lse = call(b)
         assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("n", [1, 4])                   # 16 and 64 query rows: both kernels
+@pytest.mark.parametrize("less", [0, 1000])
+def test_contexts_near_2_to_31_positions(n, less):
+    """A table of nothing but a few pages, at the context's start, within it and at its end, where the end of the last
+    piece, rounded up to whole blocks, passes 2^31."""
+    page = 4093
+    g = torch.Generator().manual_seed(3)
+    cache = P.make_cache(6 * page, 656, g)
+    width = ((1 << 31) - 4097) // page
+    L = width * page - less
+    table = torch.full((1, width), -1, dtype=torch.int32)
+    at = [0, width // 3, width - 700, width - 2, width - 1]
+    for i, k in enumerate(at):
+        table[0, k] = i + 1
+    q = torch.randn((n, 16, 576), generator=g).to(torch.bfloat16)
+    out, lse = M.mla_chunk_attention(q.to(D), cache.to(D), torch.tensor([0, n], dtype=torch.int32, device=D),
+                                     torch.tensor([L], dtype=torch.int32, device=D), table.to(D), page, 1 / 24)
+    torch.cuda.synchronize()
+    assert M.mla_get_error() == 0
+    # the formula over the positions that are there, as a context of their own
+    pos = torch.cat([torch.arange(k * page, (k + 1) * page) for k in at])
+    slot = torch.arange(page, 6 * page)[pos < L]
+    rows = torch.cat([cache[:1], cache[slot]])
+    P.check_chunk(out, lse, P.chunk(q, rows, torch.tensor([0, n]), torch.tensor([len(slot)]),
+                                    torch.arange(1, len(slot) + 1, dtype=torch.int32)[None], 1, 1 / 24))
