@@ -597,11 +597,11 @@ qk_again:
                 make_float4(fmaf(acc[nt][0], sc[nt][0], accr[nt][0]), fmaf(acc[nt][1], sc[nt][1], accr[nt][1]),
                             fmaf(acc[nt][2], sc[nt][0], accr[nt][2]), fmaf(acc[nt][3], sc[nt][1], accr[nt][3]));
         // The part of PV that does not need P, ahead of the barriers: sigma (the
-        // running max of tile `warp`'s scales, so p * scale / sigma <= 2^15 in f16),
+        // running max of tile `warp`'s scales, by size, so p * |scale| / sigma <= 2^15 in f16),
         // O rescaled when it moves, and the rows' scale / sigma as f16 pairs.
         float smax = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) smax = fmaxf(smax, fmaxf(sc[nt][0], sc[nt][1]));
+        for (int nt = 0; nt < 4; ++nt) smax = fmaxf(smax, fmaxf(fabsf(sc[nt][0]), fabsf(sc[nt][1])));
         smax = quad_max(smax);                 // all 32 rows: the same in every lane
         if (smax > sigma && smax <= FLT_MAX) {   // an infinite scale's row is zeroed below
             const float f = sigma / smax;

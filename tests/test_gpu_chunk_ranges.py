@@ -103,3 +103,15 @@ def test_contexts_near_2_to_31_positions(n, less):
     rows = torch.cat([cache[:1], cache[slot]])
     P.check_chunk(out, lse, P.chunk(q, rows, torch.tensor([0, n]), torch.tensor([len(slot)]),
                                     torch.arange(1, len(slot) + 1, dtype=torch.int32)[None], 1, 1 / 24))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("some", [False, True])
+def test_negative_scales(n, some):
+    """A scale's sign is the values' (the writer makes none; a cache from elsewhere may): all negative, or every third
+    and those eight times as large."""
+    b = batch([(n, 300), (n, 33)], 16, 576, 16, 656, seed=4)
+    sc = b["cache"][:, 512:528].contiguous().view(torch.float32)
+    sign = torch.where((torch.arange(sc.numel()) % 3 == 0) | (not some), -8.0 if some else -1.0, 1.0).view(sc.shape)
+    b["cache"][:, 512:528] = (sc * sign).contiguous().view(torch.uint8)
+    run(b)
