@@ -115,3 +115,56 @@ def test_negative_scales(n, some):
     sign = torch.where((torch.arange(sc.numel()) % 3 == 0) | (not some), -8.0 if some else -1.0, 1.0).view(sc.shape)
     b["cache"][:, 512:528] = (sc * sign).contiguous().view(torch.uint8)
     run(b)
+
+
+def rows_of(lat, rope):
+    """Cache rows as the writer makes them (a tile of zeros has the scale 1)."""
+    t = lat.to(torch.bfloat16).float().view(-1, 4, 128)
+    amax = t.abs().amax(-1)
+    sc = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+    codes = (t / sc[..., None]).to(torch.float8_e4m3fn).view(-1, 512).view(torch.uint8)
+    return torch.cat([codes, sc.contiguous().view(torch.uint8), rope.to(torch.bfloat16).view(torch.uint8)], 1)
+
+
+def held_to(n_keys, scale):
+    """What values lose beside a tile scale: their own scale is off by at most 2^-25 of the larger one, codes are at
+    most 448, and few rows' P (at least 16 at the largest score) times the ratio is held to 2^-25 too, per position."""
+    return (1 + n_keys / 16) * 449 * 2.0 ** -25 * scale
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("which", ["first", "middle", "last", "tiles"])
+@pytest.mark.parametrize("log2", [0, -6, -12])
+def test_rows_of_zeros_beside_small_values(n, which, log2):
+    """Tiles of zeros have the scale 1."""
+    L = 200
+    b = batch([(n, L)], 16, 576, 1, 656, seed=5)
+    g = torch.Generator().manual_seed(5)
+    lat = torch.randn((L, 512), generator=g) * 2.0 ** log2
+    if which == "first":
+        lat[:70] = 0
+    elif which == "middle":
+        lat[100] = 0
+        lat[133:136] = -0.0
+    elif which == "last":
+        lat[-1] = 0
+    else:
+        lat.view(L, 4, 128)[torch.rand((L, 4), generator=g) < 0.1] = 0
+    b["cache"][b["table"][0, :L].long()] = rows_of(lat, torch.randn((L, 64), generator=g))
+    out, lse = call(b)
+    ro, rl, to, tl = ref(b)
+    P.check_chunk(out, lse, (ro, rl, to + held_to(L, 1.0), tl))
+
+
+@pytest.mark.parametrize("n,H", [(3, 5), (40, 16)])
+@pytest.mark.parametrize("log2", [6, 12, 20])
+def test_a_large_scale_in_the_last_token_only(n, H, log2):
+    """The tokens before it do not attend its row, but share a tile with it."""
+    b = batch([(n, 100)], H, 576, 16, 656, seed=6)
+    slot = int(b["table"][0, 99 // 16]) * 16 + 99 % 16
+    sc = b["cache"][slot, 512:528].view(torch.float32) * 2.0 ** log2
+    b["cache"][slot, 512:528] = sc.view(torch.uint8)
+    b["q"] = b["q"] * 2.0 ** -10                        # the last token's own score stays within reach
+    out, lse = call(b)
+    ro, rl, to, tl = ref(b)
+    P.check_chunk(out, lse, (ro, rl, to + held_to(100, sc.double().repeat_interleave(128)), tl))
