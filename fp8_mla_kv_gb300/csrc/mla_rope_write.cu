@@ -219,6 +219,22 @@ bool view_ok(const void* p, int64_t row, int64_t head, int64_t rows, int heads) 
     return heads <= 1 || head % 8 == 0;
 }
 
+// Whether no two of a view's 64 values lie on one another: i outer strides and j inner ones are never
+// within 64 values of each other. A view that is written has to be so (in place, values that several
+// heads share would be turned again and again); one that is only read need not.
+bool apart(int64_t row, int64_t head, int64_t rows, int64_t heads) {
+    const uint64_t r = row < 0 ? 0 - static_cast<uint64_t>(row) : row, h = head < 0 ? 0 - static_cast<uint64_t>(head) : head;
+    if ((rows > 1 && r < kRope) || (heads > 1 && h < kRope)) return false;
+    if (rows <= 1 || heads <= 1) return true;
+    const unsigned __int128 outer = r > h ? r : h, inner = r > h ? h : r, reach = inner * ((r > h ? heads : rows) - 1) + kRope;
+    const int64_t n_outer = r > h ? rows : heads;
+    for (int64_t i = 1; i < n_outer && outer * i < reach; ++i) {   // (rows or heads behind one another: not once)
+        const unsigned __int128 off = outer * i % inner;
+        if (off < kRope || inner - off < kRope) return false;
+    }
+    return true;
+}
+
 RopeParams make_params(const mla_rope_t& rope) {
     RopeParams p;
     for (int i = 0; i < kRope / 2; ++i) {
@@ -274,7 +290,7 @@ extern "C" int mla_rope(const void* x_bf16, int64_t x_row, int64_t x_head, void*
     if (const int rc = check_rope(rope)) return rc;
     if (n_rows == 0 || n_heads == 0) return MLA_OK;
     if (!view_ok(x_bf16, x_row, x_head, n_rows, n_heads) || !view_ok(y_bf16, y_row, y_head, n_rows, n_heads) ||
-        pos == nullptr || !aligned(pos, 4) || !axes_ok(rope->n_axes, pos_stride, n_rows))
+        !apart(y_row, y_head, n_rows, n_heads) || pos == nullptr || !aligned(pos, 4) || !axes_ok(rope->n_axes, pos_stride, n_rows))
         return MLA_EINVAL;
     RotArgs a = {static_cast<const uint16_t*>(x_bf16), static_cast<uint16_t*>(y_bf16), x_row, x_head, y_row, y_head,
                  pos, pos_stride, n_rows, n_heads, 0, 0};
@@ -298,7 +314,8 @@ extern "C" int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, con
         return MLA_EINVAL;
     if ((q_bf16 == nullptr) != (q_out_bf16 == nullptr)) return MLA_EINVAL;
     if (q_bf16 != nullptr && n_heads > 0 &&
-        (!view_ok(q_bf16, q_row, q_head, n_rows, n_heads) || !view_ok(q_out_bf16, q_out_row, q_out_head, n_rows, n_heads)))
+        (!view_ok(q_bf16, q_row, q_head, n_rows, n_heads) || !view_ok(q_out_bf16, q_out_row, q_out_head, n_rows, n_heads) ||
+         !apart(q_out_row, q_out_head, n_rows, n_heads)))
         return MLA_EINVAL;
     int* err = mla_host::device_error_word();
     if (err == nullptr) return MLA_ECUDA;

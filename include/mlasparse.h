@@ -327,7 +327,7 @@ typedef struct {
  *   x_bf16, y_bf16  first rotary value of row 0, head 0; 16-byte aligned; y may be x
  *                   with the same strides (in place), otherwise they may not overlap
  *   *_row, *_head   strides in values, multiples of 8 (unused where there is one row
- *                   or one head)
+ *                   or one head); x may repeat rows or heads (stride 0), y's do not overlap
  *   n_rows, n_heads >= 0 (0 launches nothing)
  *   pos             int32 [n_axes, n_rows], device; axis k at pos + k * pos_stride
  *                   (with n_axes > 1: pos_stride >= n_rows, or 0 for one row that all axes read)

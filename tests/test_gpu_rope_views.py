@@ -49,3 +49,34 @@ def test_a_column_of_a_wider_table_of_positions():
     want = M.mla_rope(x, pos[:, 7:8].contiguous(), spec)
     for p in (pos[:, 7:8], pos.t().contiguous().t()[:, 7:8]):
         assert torch.equal(M.mla_rope(x, p, spec), want)
+
+
+def test_views_with_heads_outside_rows_and_heads_that_repeat():
+    g = torch.Generator().manual_seed(2)
+    spec = M.rope_spec(INV)
+    n, heads = 37, 6
+    pos = torch.randint(0, 9000, (n,), generator=g).to(torch.int32).to(D)
+    x = torch.randn((n, heads, 64), generator=g).to(torch.bfloat16).to(D)
+    want = M.mla_rope(x, pos, spec)
+    # heads first; in wider buffers; rows with room behind them
+    for out in (torch.zeros((heads, n, 64), dtype=torch.bfloat16, device=D).transpose(0, 1),
+                torch.zeros((n, heads, 128), dtype=torch.bfloat16, device=D)[..., 64:],
+                torch.zeros((heads, n, 200), dtype=torch.bfloat16, device=D)[..., 8:72].transpose(0, 1),
+                torch.as_strided(torch.zeros(40000, dtype=torch.bfloat16, device=D), (n, heads, 64), (7 * 64, 64, 1))):
+        assert torch.equal(M.mla_rope(x, pos, spec, out=out), want)
+    # 3 rows 256 apart, 2 heads 384 apart: neither lies within the other's, and nothing overlaps
+    buf = torch.zeros(2048, dtype=torch.bfloat16, device=D)
+    out = torch.as_strided(buf, (3, 2, 64), (256, 384, 1))
+    assert torch.equal(M.mla_rope(x[:3, :2], pos[:3], spec, out=out), want[:3, :2])
+    one = x[:, :1].expand(n, heads, 64)
+    assert torch.equal(M.mla_rope(one, pos, spec), want[:, :1].expand(n, heads, 64))
+    with pytest.raises(M.MlaError):
+        M.mla_rope(one, pos, spec, out=one)
+    cache = torch.zeros((64, 656), dtype=torch.uint8, device=D)
+    args = (cache, torch.arange(1, n + 1, device=D), torch.zeros((n, 512), dtype=torch.bfloat16, device=D),
+            torch.zeros((n, 64), dtype=torch.bfloat16, device=D), pos, spec)
+    with pytest.raises(M.MlaError):
+        M.mla_rope_kv_write(*args, q_pe=one)
+    got = torch.empty((n, heads, 64), dtype=torch.bfloat16, device=D)
+    M.mla_rope_kv_write(*args, q_pe=one, q_out=got)
+    assert torch.equal(got, want[:, :1].expand(n, heads, 64))

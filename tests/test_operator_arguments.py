@@ -41,3 +41,15 @@ def test_axes_that_overlap_are_refused_by_the_library(lib):
         assert lib.mla_rope(P(256), 64, 64, P(256), 64, 64, 4, 1, P(256), stride, s, None) == M.MLA_EINVAL
         assert lib.mla_rope_kv_write(kv, P(256), P(256), P(256), 4, 0, P(256), stride, s, None, 0, 0, None, 0, 0, 0,
                                      None) == M.MLA_EINVAL
+
+
+@pytest.mark.parametrize("row,head,n,heads", [(0, 64, 4, 2), (128, 0, 4, 2), (56, 1024, 4, 2), (1024, 8, 4, 2), (64, 64, 4, 2),
+                                              (-64, 64, 4, 2), (128, 64, 4, 3), (192, 128, 4, 4), (320, 192, 9, 9), (0, 0, 2, 1),
+                                              (0, 0, 1, 2)])
+def test_views_that_overlap_themselves_are_not_written(lib, row, head, n, heads):
+    """In place, a broadcast head would be turned once for each of its copies."""
+    s = ctypes.byref(M.rope_spec([1.0] * 32))
+    kv = M.KVCache(256, 16, 656)
+    assert lib.mla_rope(P(256), 1024, 64, P(256), row, head, n, heads, P(256), 0, s, None) == M.MLA_EINVAL
+    assert lib.mla_rope_kv_write(kv, P(256), P(256), P(256), n, 0, P(256), 0, s, P(256), 1024, 64, P(256), row, head, heads,
+                                 None) == M.MLA_EINVAL
