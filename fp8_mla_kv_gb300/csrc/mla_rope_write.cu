@@ -238,11 +238,11 @@ bool apart(int64_t row, int64_t head, int64_t rows, int64_t heads) {
 RopeParams make_params(const mla_rope_t& rope) {
     RopeParams p;
     for (int i = 0; i < kRope / 2; ++i) {
-        double f = rope.inv_freq[i] / 6.283185307179586476925286766559;
-        if (rope.inverse) f = -f;
-        f -= std::floor(f);                                   // [0, 1]
-        if (f >= 1.0) f = 0.0;
-        p.turn[i] = static_cast<uint64_t>(std::ldexp(f, 64));
+        double f = std::fabs(rope.inv_freq[i]) / 6.283185307179586476925286766559;
+        f -= std::floor(f);                                   // [0, 1)
+        const uint64_t turn = static_cast<uint64_t>(std::ldexp(f, 64));
+        // the other way round: the negative modulo 2^64 exactly (1 - f would be rounded to 2^-54 of a turn)
+        p.turn[i] = (rope.inv_freq[i] < 0) != (rope.inverse != 0) ? 0 - turn : turn;
         p.axis[i] = rope.axis[i];
     }
     p.scale = rope.scale;

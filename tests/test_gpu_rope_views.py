@@ -80,3 +80,20 @@ def test_views_with_heads_outside_rows_and_heads_that_repeat():
     got = torch.empty((n, heads, 64), dtype=torch.bfloat16, device=D)
     M.mla_rope_kv_write(*args, q_pe=one, q_out=got)
     assert torch.equal(got, want[:, :1].expand(n, heads, 64))
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_the_inverse_turns_back_by_the_same_angle(interleaved):
+    """At any position, near and far: the inverse, the negative frequency and the negative position are one rotation,
+    bit for bit."""
+    g = torch.Generator().manual_seed(3)
+    n = 4000
+    x = torch.randn((n, 8, 64), generator=g).to(torch.bfloat16).to(D)
+    pos = torch.randint(-(1 << 31) + 1, (1 << 31) - 1, (3, n), generator=g).to(torch.int32)
+    pos[:, :100] = torch.arange(100, dtype=torch.int32)
+    pos = pos.to(D)
+    kw = dict(interleaved=interleaved, scale=0.75)
+    want = M.mla_rope(x, -pos, M.rope_spec(INV, AXIS3, **kw))
+    assert torch.equal(M.mla_rope(x, pos, M.rope_spec(INV, AXIS3, inverse=True, **kw)), want)
+    assert torch.equal(M.mla_rope(x, pos, M.rope_spec([-f for f in INV], AXIS3, **kw)), want)
+    assert torch.equal(M.mla_rope(x, -pos, M.rope_spec([-f for f in INV], AXIS3, inverse=True, **kw)), want)
