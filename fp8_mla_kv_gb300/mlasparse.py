@@ -152,7 +152,10 @@ def _on(stream):
     hands their memory to nothing else before those are done."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    if not hasattr(stream, "cuda_stream"):
+        # (an ExternalStream of 0 would be a new stream, not the default one)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) != 0 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def kv_cache(cache: torch.Tensor) -> KVCache:
