@@ -349,20 +349,37 @@ mla_chunk_merge_kernel(const ChunkArgs a) {
     }
 }
 
-// Whether a staged row holds a value that is not finite: a NaN code, or a tile scale
-// or RoPE value that is NaN or infinite (one warp; every lane gets it).
-__device__ __forceinline__ bool row_not_finite(const uint8_t* row, bool rope, int lane) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * lane);
-    uint32_t bad = 0;
-    bad |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u);
-    bad |= ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
-    bool b = (bad & 0x80808080u) != 0u;
-    if (lane < 4) b = b || !isfinite(*reinterpret_cast<const float*>(row + kScaleOff + 4 * lane));
-    if (rope) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + kTailOff + 4 * lane);
-        b = b || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Of a stage's 32 rows (lane l takes row l), the part that warp `warp` works on: its latent tile, that tile's scale
+// and its 16 RoPE values. Rows where that holds a value that is not finite (a NaN code, a scale or RoPE value that is
+// NaN or infinite) are returned; their codes of the tile and its scale become 0. So does the scale of a tile of
+// zeros where it is 1, which is what the writer gives it.
+template <bool kRopeOn>
+__device__ __forceinline__ unsigned mend_part(uint8_t* st, int stride, int warp, int lane) {
+    uint8_t* row = st + lane * stride;
+    uint32_t odd = 0u, used = 0u;
+#pragma unroll 1
+    for (int k = 0; k < kTile / 16; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + kTile * warp + 16 * k);
+        const uint32_t x = v.x & 0x7f7f7f7fu, y = v.y & 0x7f7f7f7fu, z = v.z & 0x7f7f7f7fu, w = v.w & 0x7f7f7f7fu;
+        odd |= (x + 0x01010101u) | (y + 0x01010101u) | (z + 0x01010101u) | (w + 0x01010101u);
+        used |= x | y | z | w;
     }
-    return __any_sync(0xffffffffu, b);
+    odd &= 0x80808080u;
+    uint32_t* scale = reinterpret_cast<uint32_t*>(row + kScaleOff + 4 * warp);
+    odd |= ((*scale & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+    if (kRopeOn) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(row + kTailOff + 32 * warp + 4 * k);
+            odd |= ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        }
+    }
+    if (odd != 0u || (used == 0u && *scale == 0x3f800000u)) *scale = 0u;
+    if (odd != 0u) {
+#pragma unroll 1
+        for (int k = 0; k < kTile / 16; ++k) *reinterpret_cast<uint4*>(row + kTile * warp + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return __ballot_sync(0xffffffffu, odd != 0u);
 }
 
 template <bool kRopeOn>
@@ -380,7 +397,8 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSmemStages + kSmemRed + kSmemP + kSmemQmax);
     uint64_t* empty = full + kStages;
     uint32_t* vmask = reinterpret_cast<uint32_t*>(empty + kStages);   // present positions of each stage
-    uint32_t* poison_s = vmask + kStages;                             // [4] bytes of 8 rows each, by warp
+    uint32_t* poison_s = vmask + kStages;                             // [2] blocks in turn: positions whose row is not finite
+    uint32_t* late_s = poison_s + 2;                                  // a wait ran out
     int* issued_s = reinterpret_cast<int*>(poison_s + 4);
 
     const int warp = threadIdx.x >> 5;
@@ -549,12 +567,9 @@ mla_chunk_small_kernel(const ChunkArgs args) {
         const bool ok = mbar_wait_bounded(&full[s], static_cast<uint32_t>((b / kStages) & 1));
         uint8_t* st = stages + s * kStageBytes;
         const uint32_t present = vmask[s];
-        uint32_t poison = 0;                   // positions whose row holds a value that is not finite
-        bool again = false;
         float acc[4][4], accr[4][4];
         float sc[4][2];
         uint32_t rs[2][2];
-qk_again:
         // (1) QK^T of tile `warp`: latent on f16 MMA, RoPE slice on bf16 MMA.
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
@@ -603,46 +618,76 @@ qk_again:
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) smax = fmaxf(smax, fmaxf(fabsf(sc[nt][0]), fabsf(sc[nt][1])));
         smax = quad_max(smax);                 // all 32 rows: the same in every lane
-        if (smax > sigma && smax <= FLT_MAX) {   // an infinite scale's row is zeroed below
-            const float f = sigma / smax;
+        // A value that is not finite in a row's part of this warp shows in its products with any finite query
+        // row (0 * it is not 0), so with rows 0 .. 7. A tile of zeros has the scale 1, which beside small values
+        // would take the bits of their scale / sigma for nothing. Both are rare and looked into behind barrier 1.
+        bool odd = false;
+        if (smax > sigma) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+            for (int nt = 0; nt < 4; ++nt) odd |= (sc[nt][0] == 1.0f) | (sc[nt][1] == 1.0f);
+            odd = __any_sync(0xffffffffu, odd) | !(smax <= FLT_MAX);
+            if (!odd) {
+                const float f = sigma / smax;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+                }
+                sigma = smax;
+                inv_sigma = 1.0f / smax;
             }
-            sigma = smax;
-            inv_sigma = 1.0f / smax;
         }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             rs[kb][0] = pack_f16x2(sc[2 * kb][0] * inv_sigma, sc[2 * kb][1] * inv_sigma);
             rs[kb][1] = pack_f16x2(sc[2 * kb + 1][0] * inv_sigma, sc[2 * kb + 1][1] * inv_sigma);
         }
-        // A value that is not finite in a staged row shows in its products with any finite
-        // query row (0 * it is not 0), so with rows 0 .. 7. Then (rare)
-        // such rows are found, marked and zeroed, so that a position masked for a query
-        // row cannot reach it through 0 * NaN in PV; the block's QK is done again.
-        bool odd = false;
+        float sum[4];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
+            sum[nt] = fabsf(fmaf(acc[nt][0], sc[nt][0], accr[nt][0])) + fabsf(fmaf(acc[nt][1], sc[nt][1], accr[nt][1]));
+        odd |= !((sum[0] + sum[1]) + (sum[2] + sum[3]) <= FLT_MAX);
+        if (!ok) *late_s = 1u;
+        uint32_t poison = 0u;                  // positions whose row holds a value that is not finite
+        // Barrier 1 also carries that, or a timeout of any warp, to all of them (one answer per warp: it takes whole warps).
+        if (bar_sync_or(1, kConsumerThreads, __any_sync(0xffffffffu, odd | !ok))) {
+            if (*late_s != 0u) { failed = true; break; }
+            // Each warp takes such rows out of its part: their codes become zeros, so that a position masked for a
+            // query row cannot reach it through 0 * NaN in PV, and their products 0 (the other rows' stand: the
+            // MMA's columns are apart); their scores become NaN below. Then sigma and the ratios again.
+            const unsigned gone = mend_part<kRopeOn>(st, kStride, warp, lane);
+            if (lane == 0 && gone != 0u) atomicOr(&poison_s[b & 1], gone);
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) odd = odd || !(fabsf(fmaf(acc[nt][i], sc[nt][i], accr[nt][i])) <= FLT_MAX);
-        // Barrier 1 also carries a timeout of any warp, or such a value, to all of them.
-        if (bar_sync_or(1, kConsumerThreads, !ok || (odd && !again))) {
-            if (bar_sync_or(1, kConsumerThreads, !ok)) { failed = true; break; }
-            uint32_t mine = 0;
-            for (int j = 0; j < 8; ++j) {
-                uint8_t* row = st + (8 * warp + j) * kStride;
-                if (!row_not_finite(row, kRopeOn, lane)) continue;
-                mine |= 1u << j;
-                __syncwarp();
-                for (int k = lane; k < kStride / 16; k += 32) *reinterpret_cast<uint4*>(row + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+            for (int nt = 0; nt < 4; ++nt) {
+                float4 part = red[(warp * 4 + nt) * 32 + lane];
+                if (((gone >> (nt * 8 + 2 * c)) & 1u) != 0u) part.x = part.z = 0.0f;
+                if (((gone >> (nt * 8 + 2 * c + 1)) & 1u) != 0u) part.y = part.w = 0.0f;
+                red[(warp * 4 + nt) * 32 + lane] = part;
             }
-            if (lane == 0) poison_s[warp] = mine;
+            const float* scale = reinterpret_cast<const float*>(st + kScaleOff + 4 * warp);
+            const float large = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(scale[lane * (kStride / 4)]))));
+            if (large > sigma) {
+                const float f = sigma / large;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[i][0] *= f; o[i][1] *= f; o[i][2] *= f; o[i][3] *= f;
+                }
+                sigma = large;
+                inv_sigma = 1.0f / large;
+            }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 16 * kb + 8 * h + 2 * c;
+                    rs[kb][h] = pack_f16x2(scale[row * (kStride / 4)] * inv_sigma, scale[(row + 1) * (kStride / 4)] * inv_sigma);
+                }
+            __syncwarp();
             bar_sync_or(1, kConsumerThreads, false);
-            poison = poison_s[0] | (poison_s[1] << 8) | (poison_s[2] << 16) | (poison_s[3] << 24);
-            again = true;
-            goto qk_again;
+            poison = poison_s[b & 1];
         }
+        // (that word was last read ahead of the barrier 2 before, and is next written after this block's)
+        if (threadIdx.x == 0) poison_s[(b + 1) & 1] = 0u;
 
         // (2) scores of n-tile `warp`: positions 8*warp + 2c + {0,1}, rows g and g+8.
         float4 a = red[warp * 32 + lane];

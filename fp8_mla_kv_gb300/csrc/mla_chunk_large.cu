@@ -277,6 +277,16 @@ __device__ __noinline__ bool row_is_odd(const uint8_t* row) {
     return odd != 0u;
 }
 
+// Those of the tiles (bits 0 .. 3) of a cache row whose codes are all zeros.
+__device__ __forceinline__ uint32_t zero_tiles(const uint8_t* row, uint32_t tiles) {
+#pragma unroll 1
+    for (int i = 0; i < kLatent / 16; ++i) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(row) + i);
+        if (((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) != 0u) tiles &= ~(1u << (i >> 3));
+    }
+    return tiles;
+}
+
 // A row's 16 bytes, zeros where the row is absent (slot < 0): a predicate, not a branch.
 __device__ __forceinline__ uint4 ld_row(const uint8_t* cache, int slot, uint32_t row_bytes, uint32_t off) {
     const uint8_t* p = cache + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * row_bytes + off;
@@ -290,6 +300,7 @@ __device__ __forceinline__ uint4 ld_row(const uint8_t* cache, int slot, uint32_t
 }
 
 __device__ __forceinline__ uint32_t word4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ void clear4(uint4& v, int i) { (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = 0u; }
 
 // One thread of the warp; ptxas knows that it is one, so the MMAs' operands need no loop
 // over the active threads.
@@ -899,6 +910,21 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             const bool move = bar_sync_or(4, 32 * kMetaWarps, far || !ok);
             if (move) {
                 if (bar_sync_or(4, 32 * kMetaWarps, !ok)) return false;
+                // The writer gives a tile of zeros the scale 1, which beside small values would take the bits
+                // of their scale / sigma for nothing: a tile of zeros counts with 0.
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    uint32_t ones = 0u;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) ones |= (word4(u[i], t) == 0x3f800000u ? 1u : 0u) << t;
+                    if (__builtin_expect(ones != 0u, 0)) {
+                        ones = zero_tiles(args.cache + static_cast<uint64_t>(static_cast<uint32_t>(slot[i])) * row_bytes, ones);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (((ones >> t) & 1u) != 0u) clear4(u[i], t);
+                    }
+                }
+                __syncwarp();
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float top = 0.0f;

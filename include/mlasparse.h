@@ -377,10 +377,9 @@ int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* la
  * Scores are sums in fp32 of exact products, except that q values far below their row's
  * largest are rounded: below 2^-24 of it, to 2^-32 of it; in batches of many query rows per
  * sequence below 2^-13 of it, to 2^-21 of it (largest values of 2^-119 and more).
- * Values are held in f16 relative to the largest tile scale (by size) among the positions that
- * up to 64 neighbouring (token, head) rows attend, whichever of them: scales of at least 2^-14
- * of that one to half an f16 step, smaller ones to 2^-25 of it. The scale 1 that the writer
- * gives a tile of zeros is one of them.
+ * Values are held in f16 relative to the largest tile scale (by size; tiles of zeros do not
+ * count) among the positions that up to 64 neighbouring (token, head) rows attend, whichever
+ * of them: scales of at least 2^-14 of that one to half an f16 step, smaller ones to 2^-25 of it.
  * Tokens outside every sequence keep their out and lse. The result does not
  * depend on what slot 0, absent pages or positions past kv_len hold.
  *

@@ -168,3 +168,63 @@ def test_a_large_scale_in_the_last_token_only(n, H, log2):
     out, lse = call(b)
     ro, rl, to, tl = ref(b)
     P.check_chunk(out, lse, (ro, rl, to + held_to(100, sc.double().repeat_interleave(128)), tl))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("which", ["first", "middle", "last", "tiles", "most"])
+@pytest.mark.parametrize("log2", [-6, -24])
+def test_rows_of_zeros_take_no_bits(n, which, log2):
+    """Tiles of zeros do not count, whatever the others' size; rows whose scale is 1 because their largest value is 448
+    count like any."""
+    L = 500
+    b = batch([(n, L)], 16, 576, 1, 656, seed=5)
+    g = torch.Generator().manual_seed(5)
+    lat = torch.randn((L, 512), generator=g) * 2.0 ** log2
+    if which == "first":
+        lat[:150] = 0
+    elif which == "middle":
+        lat[200] = 0
+        lat[401:404] = -0.0
+    elif which == "last":
+        lat[-1] = 0
+    elif which == "tiles":
+        lat.view(L, 4, 128)[torch.rand((L, 4), generator=g) < 0.1] = 0
+    else:
+        lat[torch.rand(L, generator=g) < 0.97] = 0
+    b["cache"][b["table"][0, :L].long()] = rows_of(lat, torch.randn((L, 64), generator=g))
+    run(b)
+    # a row that is not zeros but has the scale 1 in one tile: a value of 448
+    lat[:, 128:256] = lat[:, 128:256].sign() * 0.25
+    lat[77, 200] = 448.0
+    b["cache"][b["table"][0, :L].long()] = rows_of(lat, torch.randn((L, 64), generator=g))
+    assert b["cache"][int(b["table"][0, 77]), 516:520].view(torch.float32) == 1.0
+    run(b)
+
+
+@pytest.mark.parametrize("n,H", [(1, 16), (3, 5), (40, 16)])
+@pytest.mark.parametrize("d_qk,row", [(512, 528), (512, 656), (576, 656)])
+@pytest.mark.parametrize("where", [(0,), (31, 32, 63), (64, 65, 66, 67), "block", "all"], ids=str)
+def test_rows_that_are_not_finite_anywhere(n, H, d_qk, row, where):
+    """Several in a block, a whole block of them, nothing else; by codes and by scales of different tiles, beside rows
+    of zeros; the second sequence has none."""
+    L = 200
+    b = batch([(n, L), (n, L)], H, d_qk, 1, row, seed=7)
+    at = range(96, 128) if where == "block" else range(L) if where == "all" else where
+    cache = b["cache"]
+    for i, p in enumerate(at):
+        r = int(b["table"][0, p])
+        if i % 3 == 0:
+            cache[r, (131 * i) % 512] = 0xFF if i % 2 else 0x7F
+        elif i % 3 == 1:
+            cache[r, 512 + 4 * (i % 4):516 + 4 * (i % 4)] = torch.tensor([math.nan if i % 2 else -math.inf]).view(torch.uint8)
+        elif d_qk == 576:
+            cache[r, 528 + 2 * (i % 64):530 + 2 * (i % 64)] = torch.tensor([math.inf], dtype=torch.bfloat16).view(torch.uint8)
+        else:
+            cache[r, 511] = 0x7F
+    for p in (5, 97, 150):
+        if p not in at:
+            r = int(b["table"][0, p])
+            cache[r, :512], cache[r, 512:528] = 0, torch.ones(4).view(torch.uint8)
+    run(b)
+    b["kv_len"][0] = 160
+    run(b)
