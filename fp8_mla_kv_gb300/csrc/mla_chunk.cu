@@ -10,15 +10,17 @@
 // call share (the plan of the work and the merge of split tiles) and the kernel for
 // few query rows, where reading the cache is what costs: tiles of 16 rows (one token
 // of 16 heads) on m16n8k16, the same arithmetic as the sparse decode, with q.K exact
-// before fp32 accumulation (codes as exact f16, the fp32 tile scale applied to each
-// tile's partial afterwards). Positions come in order, so a block of 32 that lies in
+// before fp32 accumulation (codes and, down to 2^-24 of a row's largest value, q as exact
+// f16, the fp32 tile scale applied to each tile's partial afterwards). Positions come in order, so a block of 32 that lies in
 // one page is a single bulk copy.
 //
 // The host knows the sizes of the arrays, not the lengths in them: a first launch of
 // one CTA reads the lengths and plans the pieces (chunk_plan_kernel), so a captured
-// graph serves any lengths. A tile is cut into pieces of about a place's share of all work
-// and at least kMinPiece positions; pieces of a cut tile write normalised partials that
-// mla_chunk_merge_kernel joins in piece order.
+// graph serves any lengths. A sequence's tiles are cut into as many pieces each as make the pieces of
+// a tile of mean length about as long as was found best for the whole batch (half of a place's share of
+// all work and more, at least kMinPiece positions); the pieces of one tile are equal parts of its own
+// positions, so those of a causal chunk's first tiles are shorter, or empty, and those of its last up to twice
+// as long. They write normalised partials that mla_chunk_merge_kernel joins in piece order.
 //
 // What bounds the kernel for few rows: 64 sequences of 1 .. 16,384 positions, one token of 16 heads each,
 // take 111 us with plan and merge (4 and 4 us), 3.8 TB/s or 0.56 of the measured copy
@@ -26,7 +28,8 @@
 // barrier, softmax, a barrier, PV) is as long: 115 instead of 120 us when all of it is
 // made to come from L2, tensor pipe 40 %, issue slots 39 %. Two CTAs an SM is what shared
 // memory and registers (168) hold. The look for values that are not finite and the masks
-// cost 5 us as long as every block paid for them: they are off the usual path.
+// cost 5 us as long as every block paid for them. Whole blocks of full tiles are free of both; a tile of fewer than
+// 16 rows (a token of 5 heads) still takes the masks, because the rows that fill it up attend nothing.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -64,11 +67,12 @@ __device__ __forceinline__ float quad_max(float v) {
 }
 
 // Plan of the work (one CTA): how many pieces each sequence's tiles are cut into, and
-// the prefixes by which a CTA finds its piece and the merge its rows. C, the longest
-// piece, is at least so many eighths (first_eighth) of a wave-th of all positions that
-// tiles read, so the pieces number at most tiles + 8 / first_eighth wave, and those of
-// split tiles (each more than C, so cut into less than 2 x its length / C) at most twice
-// the latter: the sizes of the grid and the workspace.
+// the prefixes by which a CTA finds its piece and the merge its rows. A sequence's tiles are
+// counted with their mean length. C, the length aimed at for a piece of such a tile, is at least min_piece (the
+// pieces themselves may be shorter: 129 positions at C = 128 are 96 and 33), and at least so many eighths
+// (first_eighth) of a wave-th of all positions that tiles read, so the pieces number at most tiles +
+// 8 / first_eighth wave, and those of split tiles (each more than C, so cut into less than 2 x its length
+// / C) at most twice the latter: the sizes of the grid and the workspace.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanTries = kPlanThreads / 32;
 
@@ -269,7 +273,8 @@ chunk_plan_kernel(const ChunkArgs a) {
 // time, thread x of a warp dims 128 j + 4x .. 4x + 3, the loads of a few pieces together. Bound by
 // the latency of a row's dependent loads (its place, the pieces' lse, their values): four warps a row
 // where the GPU holds them all at once (4 sequences: 17.4 us with the rest of the call, 18.6 with one),
-// one where that would take several turns (9 sequences, 7,664 rows: 72.3 us with one, 79.8 with four).
+// one where that would take several turns (9 sequences, 7,664 rows: 76.5 us with one, 84.1 with four;
+// 24 sequences, 6,144 rows: 246.8 and 250.6).
 constexpr int kMergeWarps = 4;
 
 template <int kPerRow>
@@ -900,9 +905,11 @@ constexpr int kFirstEighth = 4, kLargeFirstEighth = 3;
 
 // The kernel for many rows is taken from this many query rows per sequence, on average (64
 // sequences of up to 16,384 positions: 32 rows each 211 us small, 270 large, 36 rows 292
-// and 270, 64 rows 418 and 247), and from so many (row, position) pairs at most in the
-// batch: it starts about 10 us later (64 rows each, pairs in millions: 4 sequences, 1.5: 29 us
-// small, 34 large, 2.9: 41 and 43, 5.9: 62 and 59; 64 sequences, 2.8: 39 and 38).
+// and 270, 64 rows 418 and 247), and from so many pairs of query rows and positions that a context
+// may have (the table's width; the host knows no lengths): it starts about 10 us later (64 rows each, tables as
+// wide as the contexts, pairs in millions: 4 sequences, 1.5: 29 us small, 34 large, 2.9: 41 and 43, 5.9: 62 and
+// 59; 64 sequences, 2.8: 39 and 38). A table much wider than the contexts always passes: 4 sequences of 64 rows
+// and 0.2 million pairs then take 30 us and more instead of 18.
 constexpr int kLargeFrom = 36;
 constexpr int64_t kLargeWork = 4 << 20;
 

@@ -30,7 +30,7 @@ struct ChunkArgs {
     int tile_rows, tile_shift;         // query rows per tile, a power of two
     int align;                         // positions per block, a power of two: pieces start at multiples of it
     int wave;                          // pieces that fill the GPU once
-    int min_piece, first_eighth;       // shortest pieces: positions, eighths of a wave-th of the work
+    int min_piece, first_eighth;       // least length aimed at: positions, eighths of a wave-th of the work
     int piece_cost;                    // of a piece, beside its positions
     int32_t* order;                    // [n_seq] sequences; longest pieces first, where there is more than a wave
     int32_t* piece0;                   // [n_seq + 1] pieces

@@ -35,12 +35,12 @@
 // left their place; each warp 16 positions), 16 issues QK, 17 and 18 walk the block table ahead
 // of them (slots, scales, sigma, prefetches into L2), 19 issues PV.
 //
-// 4,096 new tokens of 16 heads behind 12,288 positions: 2,940 us, 695 TFLOP/s, 0.36 of the
+// 4,096 new tokens of 16 heads behind 12,288 positions: 2,960 us, 690 TFLOP/s, 0.36 of the
 // measured dense bf16 rate. What bounds it: L1 and shared memory are busy 72 % of the time (V is written
 // there once and read by PV, q and P by the MMAs, the rows come through it), the issue slots
 // 53 %, the tensor pipe 31 %; and a block is a chain of about a dozen hand-offs between the roles,
 // 120 cycles each, which keeps these from overlapping further. 24 sequences of two tokens of 128 heads
-// and up to 16,384 positions: 242 us, of which starting and ending a piece take about 12 us each of three.
+// and up to 16,384 positions: 247 us, of which starting and ending a piece take about 12 us each of three.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -62,7 +62,7 @@ constexpr int kThreads = 20 * 32;            // five warpgroups
 // Registers per thread: launched as kLaunchRegs each and dealt out again.
 constexpr int kLaunchRegs = 96;
 constexpr int kSoftRegs = 104;
-template <bool kRopeOn> constexpr int kConvRegs = kRopeOn ? 112 : 104;   // (104 with RoPE: 2,969 instead of 2,929 us)
+template <bool kRopeOn> constexpr int kConvRegs = kRopeOn ? 112 : 104;   // (104 with RoPE: 2,969 instead of 2,939 us)
 template <bool kRopeOn> constexpr int kAuxRegs = kRopeOn ? 48 : 64;      // (48 without: 84 instead of 79 us, spills)
 static_assert(2 * kSoftRegs + 2 * kConvRegs<true> + kAuxRegs<true> <= 5 * kLaunchRegs &&
               2 * kSoftRegs + 2 * kConvRegs<false> + kAuxRegs<false> <= 5 * kLaunchRegs, "registers");

@@ -54,7 +54,7 @@ extern "C" {
 #define MLA_OK             0
 #define MLA_EINVAL        (-1)   /* null pointer, negative size, misaligned pointer, bad layout */
 #define MLA_EUNSUPPORTED  (-2)   /* d_qk not in {512, 576}, H outside [1, 128] */
-#define MLA_ENOWORKSPACE  (-3)   /* workspace NULL or smaller than mla_sparse_decode_workspace_bytes() */
+#define MLA_ENOWORKSPACE  (-3)   /* workspace NULL, misaligned, or smaller than the call's *_workspace_bytes() */
 #define MLA_ECUDA         (-4)   /* a CUDA runtime call or a kernel launch failed */
 
 /* ---- device error word bits (mla_get_error) ---- */
@@ -384,8 +384,8 @@ int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* la
  * depend on what slot 0, absent pages or positions past kv_len hold.
  *
  *   q_bf16       bf16 [T, H, d_qk] row-major, device, 16-byte aligned; d_qk 576 or 512
- *   T, H         tokens (>= 0) and heads (1..128); T * H at most 2^29
- *   kv           the cache (row_bytes 656, or 528 with d_qk 512)
+ *   T, H         tokens (>= 0) and heads (1..128); T * H below 2^29
+ *   kv           the cache (row_bytes 656, or 528 with d_qk 512), of less than 2^31 slots
  *   q_start      int32 [n_seq + 1], device, nondecreasing within [0, T]; a sequence for
  *                which it is not is skipped and flagged MLA_ERR_CHUNK_RANGE
  *   kv_len       int32 [n_seq], device; a negative one counts as 0; positions past
@@ -398,7 +398,8 @@ int mla_rope_kv_write(mla_kv_cache_t kv, const int64_t* slot_idx, const void* la
  *                16-byte aligned; its contents on entry do not matter. Calls that may
  *                overlap (other streams, graphs replayed at once) need their own.
  * The lengths are read on the device: a captured call serves any lengths within the
- * arrays' sizes. Launched with programmatic stream serialization like the decode.
+ * arrays' sizes. T, H, n_seq and max_pages * page_size decide which of two kernels runs; they agree to
+ * rounding, not bit for bit, so a wider table may change an output's last bits. Launched with programmatic stream serialization like the decode.
  * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED, MLA_ENOWORKSPACE or MLA_ECUDA.
  */
 size_t mla_chunk_attention_workspace_bytes(int T, int H, int n_seq);
