@@ -1,0 +1,288 @@
+// Block-sparse attention, the parts before the attention: mla_block_keys (a mean key for each complete page of the
+// cache) and mla_block_select (the blocks that each token attends, from their scores). A block is a page.
+#include <climits>
+
+#include "mla_seq.cuh"
+
+namespace {
+
+using namespace mla;
+
+// ---- mean keys: K = (sum over the page's rows of [code x scale | rope]) / rows, BF16 ----
+//
+// A CTA takes a page that a sequence's new tokens completed, a warp every eighth row: lane l values 16 l .. 16 l + 15
+// of the latent (tile l / 8) and, l < 8, RoPE values 8 l .. 8 l + 7, kAhead rows' loads on their way; sums in fp32, the
+// warps' joined in shared memory. Bound by the bytes of the rows where there are many: TIME_KEYS.
+constexpr int kKeyThreads = 256;
+constexpr int kKeyWarps = kKeyThreads / 32;
+constexpr int kAhead = 4;
+
+template <bool kRopeOn>
+__global__ void __launch_bounds__(kKeyThreads)
+block_keys_kernel(const Batch b, const uint8_t* __restrict__ cache, int64_t num_slots, int64_t row_bytes,
+                  __nv_bfloat16* __restrict__ keys, int num_keys) {
+    constexpr int kDim = kLatent + (kRopeOn ? kRope : 0);
+    __shared__ __align__(16) float part[kKeyWarps][kDim];
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0) check_lengths(b);
+    // pages complete after the new tokens, less those before them
+    auto first_page = [&](const Sequence& q) { return max(0, q.len - q.n) / b.page_size; };
+    const int2 u = find_unit<kKeyThreads>(b.n_seq, blockIdx.x, [&](int s) {
+        const Sequence q = sequence_of(b, s);
+        return q.n > 0 ? max(0, min(q.len, capacity(b)) / b.page_size - first_page(q)) : 0;
+    });
+    if (u.x < 0) return;
+    const int page = first_page(sequence_of(b, u.x)) + u.y;
+    const int phys = __ldg(b.block_table + static_cast<int64_t>(u.x) * b.max_pages + page);
+    if (phys < 0) return;
+    const int64_t slot0 = static_cast<int64_t>(phys) * b.page_size;
+    const int there = static_cast<int>(min(static_cast<int64_t>(b.page_size), max(static_cast<int64_t>(0), num_slots - slot0)));
+    if (phys >= num_keys || there < b.page_size) {
+        if (threadIdx.x == 0) atomicOr(b.err, MLA_ERR_PAGE_RANGE);
+        if (phys >= num_keys) return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int skip = slot0 == 0 ? 1 : 0;                   // the reserved slot is no row
+    float v[16], r[8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+    for (int i0 = skip + warp; i0 < there; i0 += kAhead * kKeyWarps) {
+        uint4 code[kAhead], tail[kAhead];
+        float scale[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * kKeyWarps;
+            code[k] = tail[k] = make_uint4(0u, 0u, 0u, 0u);
+            scale[k] = 0.0f;
+            if (i < there) {
+                const uint8_t* row = cache + (slot0 + i) * row_bytes;
+                code[k] = ld_nc_v4(row + 16 * lane);
+                scale[k] = __ldg(reinterpret_cast<const float*>(row + kScaleOff) + (lane >> 3));
+                if (kRopeOn && lane < 8) tail[k] = ld_nc_v4(row + kTailOff + 16 * lane);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t lo, hi;
+                e4m3x4_to_f16x2x2(w[j], lo, hi);
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                v[4 * j] = fmaf(x.x, scale[k], v[4 * j]);
+                v[4 * j + 1] = fmaf(x.y, scale[k], v[4 * j + 1]);
+                v[4 * j + 2] = fmaf(y.x, scale[k], v[4 * j + 2]);
+                v[4 * j + 3] = fmaf(y.y, scale[k], v[4 * j + 3]);
+            }
+            if (kRopeOn) {
+                const uint32_t t[4] = {tail[k].x, tail[k].y, tail[k].z, tail[k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    r[2 * j] += bf16lo(t[j]);
+                    r[2 * j + 1] += bf16hi(t[j]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(&part[warp][16 * lane + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    if (kRopeOn && lane < 8) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<float4*>(&part[warp][kLatent + 8 * lane + 4 * j]) =
+                make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+    }
+    __syncthreads();
+    const float rows = static_cast<float>(max(1, there - skip));
+    for (int d = 2 * threadIdx.x; d < kDim; d += 2 * kKeyThreads) {
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kKeyWarps; ++w) {
+            const float2 p = *reinterpret_cast<const float2*>(&part[w][d]);
+            x += p.x;
+            y += p.y;
+        }
+        *reinterpret_cast<uint32_t*>(keys + static_cast<int64_t>(phys) * kDim + d) = pack_bf16x2(x / rows, y / rows);
+    }
+}
+
+// ---- selection ----
+//
+// A score becomes a 32-bit key that orders like it (0: not to be chosen, the largest: chosen whatever its score). The
+// W-th largest key is found two bits at a time from the top, by counting how many keys have each next digit; the keys
+// above it are taken, and of those equal to it the first ones. A CTA of kWarps warps takes a token; kWarps x 256 keys
+// stay in registers, and where there are more, each pass reads the scores again (from L2).
+// Bound by the chain of passes (16 at most, it ends when a digit's keys are exactly those wanted): TIME_SELECT.
+constexpr int kPer = 8;                                    // keys per thread at a time
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (!(x > -INFINITY)) return 0u;                       // -inf or NaN: not chosen
+    const uint32_t u = x == 0.0f ? 0u : __float_as_uint(x);       // (-0 is 0)
+    return (u >> 31) != 0u ? ~u : u | 0x80000000u;
+}
+
+template <int kWarps, bool kWide>
+__global__ void __launch_bounds__(32 * kWarps)
+block_select_kernel(const Batch b, const float* __restrict__ scores, int columns, int sink, int local, int width,
+                    int32_t* __restrict__ blocks) {
+    constexpr int kThreads = 32 * kWarps, kChunk = kThreads * kPer;
+    __shared__ uint32_t counts[2][kWarps][3];
+    __shared__ int place[kPer][kWarps];                    // keys above the threshold, and (upper half) equal to it
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (t == 0) check_lengths(b);
+    const int s = sequence_at(b, t, lane);
+    if (s < 0) return;
+    const Sequence q = sequence_of(b, s);
+    const int pos = position_of(b, q, t - q.start);
+    int32_t* out = blocks + static_cast<int64_t>(t) * width;
+    const int n = pos < 0 ? 0 : pos / b.page_size + 1;     // blocks up to the token's own
+    const float* row = scores + static_cast<int64_t>(t) * columns;
+    auto key_of = [&](int i) -> uint32_t {
+        if (i >= n) return 0u;
+        if (i < sink || i > n - 1 - local) return 0xffffffffu;
+        return order_key(__ldg(row + i));
+    };
+    uint32_t key[kPer];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) key[k] = key_of(base + k * kThreads + threadIdx.x);
+    };
+    load(0);
+    const int chunks = kWide ? (n + kChunk - 1) / kChunk : 1;
+    // The threshold's digits; `left`: how many keys that agree with it so far are still wanted.
+    uint32_t found = 0u;
+    int left = width;
+    bool all = false;                                      // every key that agrees is taken
+#pragma unroll 1
+    for (int shift = 30; shift >= 0 && !all; shift -= 2) {
+        const int turn = (shift >> 1) & 1;
+        int c3 = 0, c2 = 0, c1 = 0;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            if (kWide) load(c * kChunk);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const uint32_t d = (key[k] ^ found) >> shift;      // agrees above: 0 .. 3, the digit
+                c3 += d == 3u;
+                c2 += d == 2u;
+                c1 += d == 1u;
+            }
+        }
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        c1 = __reduce_add_sync(0xffffffffu, c1);
+        if (kWarps > 1) {
+            if (lane == 0) {
+                counts[turn][warp][0] = c1;
+                counts[turn][warp][1] = c2;
+                counts[turn][warp][2] = c3;
+            }
+            __syncthreads();
+            c1 = lane < kWarps ? counts[turn][lane][0] : 0;
+            c2 = lane < kWarps ? counts[turn][lane][1] : 0;
+            c3 = lane < kWarps ? counts[turn][lane][2] : 0;
+            c3 = __reduce_add_sync(0xffffffffu, c3);
+            c2 = __reduce_add_sync(0xffffffffu, c2);
+            c1 = __reduce_add_sync(0xffffffffu, c1);
+        }
+        int here = c3;
+        uint32_t digit = 3u;
+        if (left > here) { left -= here; here = c2; digit = 2u; }
+        if (digit == 2u && left > here) { left -= here; here = c1; digit = 1u; }
+        if (digit == 1u && left > here) { left -= here; digit = 0u; }
+        found |= digit << shift;
+        all = digit != 0u && left == here;                 // (the lower digits stay 0: any are taken)
+    }
+    // Those above the threshold and the first `left` of those equal to it, in ascending order. (Fewer keys than wanted:
+    // the threshold is 0, and a key of 0 is never taken.)
+    auto above = [&](uint32_t x) { return all ? x >= found : x > found; };
+    auto equal = [&](uint32_t x) { return !all && found != 0u && x == found; };
+    const uint32_t lower = (1u << lane) - 1u;
+    int n_above = 0, n_equal = 0;                          // before this step's
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        if (kWide) load(c * kChunk);
+        if (kWarps > 1) __syncthreads();                   // (the chunk before has been placed)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const unsigned a = __ballot_sync(0xffffffffu, above(key[k])), e = __ballot_sync(0xffffffffu, equal(key[k]));
+            if (lane == 0) place[k][warp] = __popc(a) | __popc(e) << 16;
+        }
+        if (kWarps > 1) __syncthreads();
+        else __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int row = lane < kWarps ? place[k][lane] : 0;
+            int incl = row;
+#pragma unroll
+            for (int d = 1; d < kWarps; d <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += x;
+            }
+            const int total = __shfl_sync(0xffffffffu, incl, kWarps - 1), before = __shfl_sync(0xffffffffu, incl - row, warp);
+            const bool a = above(key[k]), e = equal(key[k]);
+            const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
+            const int e_rank = n_equal + (before >> 16) + __popc(em & lower);
+            if (a || (e && e_rank < left))
+                out[n_above + (before & 0xffff) + __popc(am & lower) + min(e_rank, left)] = c * kChunk + k * kThreads + threadIdx.x;
+            n_above += total & 0xffff;
+            n_equal += total >> 16;
+        }
+    }
+    for (int i = n_above + min(n_equal, left) + threadIdx.x; i < width; i += kThreads) out[i] = -1;
+}
+
+bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace
+
+extern "C" int mla_block_keys(mla_kv_cache_t kv, int d_qk, const int32_t* q_start, const int32_t* kv_len,
+                              const int32_t* block_table, int n_seq, int max_pages, int page_size, int T, void* keys_bf16,
+                              int num_keys, void* stream) {
+    Batch b = {q_start, kv_len, block_table, n_seq, max_pages, page_size, T, nullptr};
+    if (num_keys < 0 || kv.num_slots < 0) return MLA_EINVAL;
+    if (kv.row_bytes != MLA_ROW_BYTES && kv.row_bytes != MLA_ROW_BYTES_NOPE) return MLA_EINVAL;
+    if (d_qk != kLatent && d_qk != kLatent + kRope) return MLA_EUNSUPPORTED;
+    if (kv.row_bytes == MLA_ROW_BYTES_NOPE && d_qk != kLatent) return MLA_EUNSUPPORTED;
+    const int rc = mla_host::check_batch(b);
+    if (rc != MLA_OK || T == 0 || n_seq == 0 || max_pages == 0) return rc;
+    if (kv.data == nullptr || off(kv.data, 16) || off(keys_bf16, 16) || (keys_bf16 == nullptr && num_keys > 0)) return MLA_EINVAL;
+    b.err = mla_host::device_error_word();
+    if (b.err == nullptr) return MLA_ECUDA;
+    // n tokens complete at most (n - 1) / page_size + 1 pages
+    const int64_t units = static_cast<int64_t>(T) / page_size + (n_seq < T ? n_seq : T);
+    return mla_host::launch_pdl(d_qk == kLatent ? block_keys_kernel<false> : block_keys_kernel<true>, units, kKeyThreads, 0,
+                                stream, b, static_cast<const uint8_t*>(kv.data), kv.num_slots, kv.row_bytes,
+                                static_cast<__nv_bfloat16*>(keys_bf16), num_keys)
+               ? MLA_OK : MLA_ECUDA;
+}
+
+extern "C" int mla_block_select(const float* scores, int T, int columns, const int32_t* q_start, const int32_t* kv_len,
+                                int n_seq, int page_size, int sink, int local, int width, int32_t* blocks, void* stream) {
+    // (the scores have a column for each block of the table)
+    Batch b = {q_start, kv_len, nullptr, n_seq, 0, page_size, T, nullptr};
+    if (columns < 0 || sink < 0 || local < 1 || width < 0 || static_cast<int64_t>(sink) + local > width) return MLA_EINVAL;
+    const int rc = mla_host::check_batch(b);
+    if (rc != MLA_OK || T == 0 || n_seq == 0 || columns == 0) return rc;
+    if (static_cast<int64_t>(columns) * page_size > INT_MAX - 4096) return MLA_EUNSUPPORTED;
+    if (scores == nullptr || blocks == nullptr || off(scores, 4) || off(blocks, 4)) return MLA_EINVAL;
+    b.max_pages = columns;
+    b.err = mla_host::device_error_word();
+    if (b.err == nullptr) return MLA_ECUDA;
+    void (*kernel)(const Batch, const float*, int, int, int, int, int32_t*) = block_select_kernel<32, true>;
+    int warps = 32;
+    if (columns <= 256) { kernel = block_select_kernel<1, false>; warps = 1; }
+    else if (columns <= 1024) { kernel = block_select_kernel<4, false>; warps = 4; }
+    else if (columns <= 2048) { kernel = block_select_kernel<8, false>; warps = 8; }
+    else if (columns <= 8192) { kernel = block_select_kernel<32, false>; warps = 32; }
+    return mla_host::launch_pdl(kernel, T, 32 * warps, 0, stream, b, scores, columns, sink, local, width, blocks) ? MLA_OK
+                                                                                                                : MLA_ECUDA;
+}

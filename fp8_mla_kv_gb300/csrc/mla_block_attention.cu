@@ -1,0 +1,285 @@
+// mla_block_attention: attention over the blocks (pages) that are listed for each token.
+//
+// The kernels are chunk attention's (mla_chunk.cu, mla_chunk_large.cu); what differs is which positions they
+// walk and which of a tile's tokens attend each. A tile's query rows are the (token, head) pairs of a group of
+// consecutive tokens (one token where it has 16 heads and more, for few rows, or 64, for many); its positions are those of
+// the blocks that any of the group's tokens lists, one after the other, and each block carries a bit per
+// token. Neighbouring tokens of a prompt want mostly the same blocks, so a group of four reads and multiplies a
+// block once that would be read four times token by token. Tokens of different sequences may share a group: their
+// blocks stand side by side then.
+//
+// A first launch makes the groups' lists (block_lists_kernel): a CTA per group marks the listed blocks in a bit
+// map, so that a block counts once however often and in whatever order it is listed, and ranks them by prefix counts.
+// The pieces of the tiles are planned on the host: it knows how long lists are at most. A captured call serves any
+// lengths and lists.
+#include <climits>
+#include <cmath>
+
+#include "mla_chunk.cuh"
+#include "mla_seq.cuh"
+
+namespace {
+
+using namespace mla;
+using namespace mla_chunk;
+
+constexpr int kThreads = 256;
+constexpr int kWords = 2048;                           // of the bit map: 65,536 blocks at a time
+constexpr int kPerThread = kWords / kThreads;
+
+// Blocks of the group's tokens, ascending by sequence and block. TIME_LISTS.
+__global__ void __launch_bounds__(kThreads)
+block_lists_kernel(const Batch b, const int32_t* __restrict__ blocks, int width, int group_tokens, int64_t num_slots,
+                   BlockEntry* __restrict__ entries, int entry_cap, int2* __restrict__ groups) {
+    __shared__ uint32_t bits[kWords];
+    __shared__ int before[kWords];                     // set bits in the words before
+    __shared__ int seq_s[32], pos_s[32];
+    __shared__ int sums[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0) check_lengths(b);
+    const int first = blockIdx.x * group_tokens, n_tokens = min(group_tokens, b.T - first);
+    for (int k = warp; k < n_tokens; k += kThreads / 32) {
+        const int s = sequence_at(b, first + k, lane);
+        int pos = -1;
+        if (s >= 0) {
+            const Sequence q = sequence_of(b, s);
+            pos = position_of(b, q, first + k - q.start);
+        }
+        if (lane == 0) {
+            seq_s[k] = s;
+            pos_s[k] = pos;
+        }
+    }
+    __syncthreads();
+    BlockEntry* out = entries + static_cast<int64_t>(blockIdx.x) * entry_cap;
+    uint32_t live = 0u;
+    int count = 0;                                     // entries so far
+    for (int k0 = 0, k1; k0 < n_tokens; k0 = k1) {     // the group's tokens of one sequence
+        const int s = seq_s[k0];
+        for (k1 = k0 + 1; k1 < n_tokens && seq_s[k1] == s;) ++k1;
+        if (s < 0) continue;
+        live |= (k1 - k0 == 32 ? 0xffffffffu : (1u << (k1 - k0)) - 1u) << k0;
+        const int ahead0 = k0 - pos_s[k0];             // position p is that of the group's token p + ahead0
+        const int last = pos_s[k1 - 1] / b.page_size;  // (their positions ascend)
+        if (pos_s[k1 - 1] < 0) continue;
+        const int32_t* bt = b.block_table + static_cast<int64_t>(s) * b.max_pages;
+        for (int w0 = 0;; w0 += 32 * kWords) {
+            const int words = min(kWords, (last - w0) / 32 + 1);
+            __syncthreads();                           // (the step before has read them)
+            for (int i = threadIdx.x; i < words; i += kThreads) bits[i] = 0u;
+            __syncthreads();
+            // Listed, at or before the token's own block, and with a page.
+            auto listed = [&](int i, int& block, int& k, int& phys) {
+                k = k0 + i / width;
+                block = __ldg(blocks + (static_cast<int64_t>(first) + k0) * width + i);
+                if (block >= b.max_pages && w0 == 0) atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
+                if (block < w0 || block - w0 >= 32 * words || pos_s[k] < 0 || block > pos_s[k] / b.page_size) return false;
+                phys = __ldg(bt + block);
+                if (phys < 0) return false;
+                if (static_cast<int64_t>(phys) * b.page_size >= num_slots) {
+                    atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
+                    return false;
+                }
+                return true;
+            };
+            const int total = (k1 - k0) * width;
+            for (int i = threadIdx.x; i < total; i += kThreads) {
+                int block, k, phys;
+                if (listed(i, block, k, phys)) atomicOr(&bits[(block - w0) >> 5], 1u << (block & 31));
+            }
+            __syncthreads();
+            // Prefix counts: kPerThread words a thread.
+            int mine = 0;
+#pragma unroll
+            for (int j = 0; j < kPerThread; ++j) {
+                const int w = threadIdx.x * kPerThread + j;
+                mine += w < words ? __popc(bits[w]) : 0;
+            }
+            int incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += x;
+            }
+            if (lane == 31) sums[warp] = incl;
+            __syncthreads();
+            int at = count + incl - mine, found = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                at += w < warp ? sums[w] : 0;
+                found += sums[w];
+            }
+#pragma unroll
+            for (int j = 0; j < kPerThread; ++j) {
+                const int w = threadIdx.x * kPerThread + j;
+                if (w >= words) break;
+                before[w] = at;
+                for (uint32_t left = bits[w]; left != 0u; left &= left - 1u) {
+                    const int block = w0 + 32 * w + __ffs(left) - 1;
+                    BlockEntry e;
+                    e.slot0 = __ldg(bt + block) * b.page_size;
+                    e.ahead = block * b.page_size + ahead0;
+                    e.tokens = k1 - k0 == 1 ? 1u << k0 : 0u;
+                    e.pad = 0;
+                    *reinterpret_cast<int4*>(out + at++) = *reinterpret_cast<const int4*>(&e);
+                }
+            }
+            __syncthreads();
+            if (k1 - k0 > 1)
+                for (int i = threadIdx.x; i < total; i += kThreads) {
+                    int block, k, phys;
+                    if (listed(i, block, k, phys)) {
+                        const int w = (block - w0) >> 5;
+                        const int rank = before[w] + __popc(bits[w] & ((1u << (block & 31)) - 1u));
+                        atomicOr(&out[rank].tokens, 1u << k);
+                    }
+                }
+            count += found;
+            if (last - w0 < 32 * kWords) break;
+        }
+    }
+    if (threadIdx.x == 0) groups[blockIdx.x] = make_int2(count, static_cast<int>(live));
+}
+
+// What a piece costs beside its positions, in positions, as in chunk attention's plan.
+constexpr int kPieceCost = 300, kLargePieceCost = 512;
+// The kernel for many rows, as there: from so many query rows per sequence on average, and so many pairs of rows and listed
+// positions.
+constexpr int kLargeFrom = 36;
+constexpr int64_t kLargeWork = 4 << 20;
+
+struct Sizes {
+    bool large;
+    int tile_rows, group_tokens, group_tiles, nk;
+    int64_t groups, tiles;
+    size_t parts_o, parts_lse, heads, entries;         // bytes
+    size_t total() const { return parts_o + parts_lse + heads + entries; }
+};
+
+// nk: the pieces per tile that make the least of waves x (positions of a piece + its cost); without positions, as many
+// as are ever taken.
+Sizes sizes_of(int T, int H, int width, int64_t positions, bool large, int sms) {
+    Sizes z;
+    z.large = large;
+    z.tile_rows = large ? kLargeRows : kSmallRows;
+    z.group_tokens = H < z.tile_rows ? z.tile_rows / H : 1;
+    if (z.group_tokens > 32) z.group_tokens = 32;      // a bit each
+    z.group_tiles = (H + z.tile_rows - 1) / z.tile_rows;
+    z.groups = (static_cast<int64_t>(T) + z.group_tokens - 1) / z.group_tokens;
+    z.tiles = z.groups * z.group_tiles;
+    const int64_t wave = large ? sms : kCtasPerSm * sms, most = 4 * wave / z.tiles + 1;
+    const int cost = large ? kLargePieceCost : kPieceCost, least = large ? kLargeMinPiece : kMinPiece;
+    z.nk = positions < 0 ? static_cast<int>(most) : 1;
+    int64_t best = INT64_MAX;
+    for (int64_t nk = 1; positions >= 0 && nk <= most; ++nk) {
+        const int64_t per = (positions + nk - 1) / nk;
+        if (nk > 1 && per < least) break;
+        const int64_t waves = (z.tiles * nk + wave - 1) / wave, time = waves * (per + cost);
+        if (time < best) {
+            best = time;
+            z.nk = static_cast<int>(nk);
+        }
+    }
+    const size_t rows = z.nk > 1 ? static_cast<size_t>(z.tiles) * z.nk * z.tile_rows : 0;
+    z.parts_o = rows * kLatent * sizeof(float);
+    z.parts_lse = align256(rows * sizeof(float));
+    z.heads = align256(z.groups * sizeof(int2));
+    z.entries = static_cast<size_t>(z.groups) * z.group_tokens * width * sizeof(BlockEntry);
+    return z;
+}
+
+bool takes_large(int T, int H, int n_seq, int64_t positions) {
+    const int64_t rows = static_cast<int64_t>(T) * H;
+    return rows >= static_cast<int64_t>(kLargeFrom) * n_seq && rows * positions >= kLargeWork;
+}
+
+}  // namespace
+
+extern "C" size_t mla_block_attention_workspace_bytes(int T, int H, int width) {
+    if (T <= 0 || H < 1 || H > 128 || width < 0) return 0;
+    const int sms = mla_host::sm_count();
+    if (sms <= 0) return 0;
+    // whatever the page size: the most pieces, of either kernel
+    size_t most = 0;
+    for (const bool large : {false, true}) {
+        const Sizes z = sizes_of(T, H, width, -1, large, sms);
+        if (z.total() > most) most = z.total();
+    }
+    return most;
+}
+
+extern "C" int mla_block_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* blocks,
+                                   int width, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                   int n_seq, int max_pages, int page_size, float sm_scale, void* out_bf16, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    Batch b = {q_start, kv_len, block_table, n_seq, max_pages, page_size, T, nullptr};
+    if (width < 0 || kv.num_slots < 0 || !std::isfinite(sm_scale)) return MLA_EINVAL;
+    if (kv.row_bytes != MLA_ROW_BYTES && kv.row_bytes != MLA_ROW_BYTES_NOPE) return MLA_EINVAL;
+    if (d_qk != kLatent && d_qk != kLatent + kRope) return MLA_EUNSUPPORTED;
+    if (kv.row_bytes == MLA_ROW_BYTES_NOPE && d_qk != kLatent) return MLA_EUNSUPPORTED;   // no tail to read
+    if (H < 1 || H > 128) return MLA_EUNSUPPORTED;
+    const int rc = mla_host::check_batch(b);
+    if (rc != MLA_OK || T == 0 || n_seq == 0) return rc;
+    if (static_cast<int64_t>(T) * H > INT_MAX / 4 || kv.num_slots > INT_MAX) return MLA_EUNSUPPORTED;
+    if (q_bf16 == nullptr || out_bf16 == nullptr || lse == nullptr || (width > 0 && blocks == nullptr) ||
+        (max_pages > 0 && kv.data == nullptr))
+        return MLA_EINVAL;
+    if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16) || !aligned(kv.data, 16) || !aligned(lse, 4) || !aligned(blocks, 4))
+        return MLA_EINVAL;
+    // (a token's blocks are at most the table's, however many entries its list has)
+    const int64_t listed = width < max_pages ? width : max_pages, positions = listed * page_size;
+    const int sms = mla_host::sm_count();
+    b.err = mla_host::device_error_word();
+    if (b.err == nullptr || sms <= 0) return MLA_ECUDA;
+    const Sizes z = sizes_of(T, H, width, positions, takes_large(T, H, n_seq, positions), sms);
+    if (positions * z.group_tokens > INT_MAX - 4096 || z.tiles * z.nk > INT_MAX ||
+        static_cast<int64_t>(z.group_tokens) * width > INT_MAX)
+        return MLA_EUNSUPPORTED;
+    if (z.total() > 0 && (workspace == nullptr || !aligned(workspace, 16) ||
+                          workspace_bytes < mla_block_attention_workspace_bytes(T, H, width)))
+        return MLA_ENOWORKSPACE;
+
+    ChunkArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q_bf16);
+    a.cache = static_cast<const uint8_t*>(kv.data);
+    a.out = static_cast<__nv_bfloat16*>(out_bf16);
+    a.lse = lse;
+    a.num_slots = kv.num_slots;
+    a.row_bytes = kv.row_bytes;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.block_table = block_table;
+    a.n_seq = n_seq;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.T = T;
+    a.H = H;
+    a.d_qk = d_qk;
+    a.sm_scale_log2 = sm_scale * kLog2e;
+    a.err = b.err;
+    a.tile_rows = z.tile_rows;
+    a.tile_shift = z.large ? 6 : 4;
+    a.align = z.large ? kLargeBlock : 32;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    a.part_o = reinterpret_cast<float*>(w);
+    w += z.parts_o;
+    a.part_lse = reinterpret_cast<float*>(w);
+    w += z.parts_lse;
+    int2* groups = reinterpret_cast<int2*>(w);
+    w += z.heads;
+    BlockEntry* entries = reinterpret_cast<BlockEntry*>(w);
+    a.groups = groups;
+    a.entries = entries;
+    a.entry_cap = z.group_tokens * width;
+    a.group_tokens = z.group_tokens;
+    a.group_tiles = z.group_tiles;
+    a.nk = z.nk;
+    if (!mla_host::launch_pdl(block_lists_kernel, z.groups, kThreads, 0, stream, b, blocks, width, z.group_tokens,
+                              kv.num_slots, entries, a.entry_cap, groups))
+        return MLA_ECUDA;
+    const bool ok = z.large ? mla_host::launch_chunk_large(a, kBlocks, z.tiles * z.nk, stream)
+                            : mla_host::launch_chunk_small(a, kBlocks, z.tiles * z.nk, stream);
+    return ok && (z.nk == 1 || mla_host::launch_chunk_merge(a, kBlocks, stream)) ? MLA_OK : MLA_ECUDA;
+}

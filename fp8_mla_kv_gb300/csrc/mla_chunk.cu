@@ -54,8 +54,8 @@ constexpr int kSmemRed = kWarps * 4 * 32 * 16;       // QK tile partials: float4
 constexpr int kSmemP = 4 * 32 * 8;                   // P (f16): uint2 [n-tile][lane], A-fragment order
 constexpr int kSmemQmax = 3 * kWarps * kHeads * 4;   // |q| maxima, block score maxima, l partials
 constexpr int kSmemMisc = 2 * kStages * 8 + kStages * 4 + 16 + 16;   // barriers, present masks, poisoned rows, issued
+constexpr int kSmemTokens = kStages * kNB * 4;       // where a position has a mask of tokens
 constexpr int kSmemTotal = kSmemStages + kSmemRed + kSmemP + kSmemQmax + kSmemMisc;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The exp2 offset puts the largest score at kTop (log2 units) and moves only when one is
 // kRescaleSlack above that: p <= 2^15 stays in f16's range, whose smallest is 2^-28 of the largest p.
@@ -277,7 +277,7 @@ chunk_plan_kernel(const ChunkArgs a) {
 // 24 sequences, 6,144 rows: 246.8 and 250.6).
 constexpr int kMergeWarps = 4;
 
-template <int kPerRow>
+template <int kPerRow, int kForm>
 __global__ void __launch_bounds__(32 * kMergeWarps)
 mla_chunk_merge_kernel(const ChunkArgs a) {
     constexpr int kDims = kMergeWarps / kPerRow;       // float4 per thread
@@ -287,16 +287,27 @@ mla_chunk_merge_kernel(const ChunkArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int total = a.mrow0[a.n_seq];
+    const int total = kForm == kBlocks ? a.T * a.H : a.mrow0[a.n_seq];
     for (int r = blockIdx.x * kRows + warp / kPerRow; r < total; r += gridDim.x * kRows) {
-        const int at = find_seq(a.mrow0, a.n_seq, r, lane);
-        const int s = a.order[at];
-        const int local = r - a.mrow0[at];
-        const int np = a.split[at];
-        const int tile = local >> a.tile_shift;
-        const int64_t row0 = (static_cast<int64_t>(a.part0[at]) + static_cast<int64_t>(tile) * np) * a.tile_rows +
-                             (local - tile * a.tile_rows);
-        const int64_t grow = static_cast<int64_t>(__ldg(a.q_start + s)) * a.H + local;
+        int np;
+        int64_t row0, grow;
+        if (kForm == kBlocks) {
+            const int group_rows = a.group_tokens * a.H, group = r / group_rows, local = r - group * group_rows;
+            if (((static_cast<uint32_t>(__ldg(&a.groups[group].y)) >> (local / a.H)) & 1u) == 0u) continue;
+            const int tile = local >> a.tile_shift;
+            np = a.nk;
+            row0 = (static_cast<int64_t>(group) * a.group_tiles + tile) * np * a.tile_rows + (local - tile * a.tile_rows);
+            grow = r;
+        } else {
+            const int at = find_seq(a.mrow0, a.n_seq, r, lane);
+            const int s = a.order[at];
+            const int local = r - a.mrow0[at];
+            np = a.split[at];
+            const int tile = local >> a.tile_shift;
+            row0 = (static_cast<int64_t>(a.part0[at]) + static_cast<int64_t>(tile) * np) * a.tile_rows +
+                   (local - tile * a.tile_rows);
+            grow = static_cast<int64_t>(__ldg(a.q_start + s)) * a.H + local;
+        }
         float mx = -INFINITY;
         bool nan = false;
         for (int s0 = 0; s0 < np; s0 += kBatch) {
@@ -387,7 +398,7 @@ __device__ __forceinline__ unsigned mend_part(uint8_t* st, int stride, int warp,
     return __ballot_sync(0xffffffffu, odd != 0u);
 }
 
-template <bool kRopeOn>
+template <bool kRopeOn, int kForm>
 __global__ void __launch_bounds__(kThreads, 2)
 mla_chunk_small_kernel(const ChunkArgs args) {
     constexpr uint32_t kRowRead = kRopeOn ? kRowBytes : kNopeReadBytes;
@@ -405,15 +416,18 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     uint32_t* poison_s = vmask + kStages;                             // [2] blocks in turn: positions whose row is not finite
     uint32_t* late_s = poison_s + 2;                                  // a wait ran out
     int* issued_s = reinterpret_cast<int*>(poison_s + 4);
+    // [kStages][kNB] tokens that attend a stage's positions; vmask then has those that all of them attend
+    uint32_t* tokens_s = reinterpret_cast<uint32_t*>(smem + kSmemStages + kSmemRed + kSmemP + kSmemQmax + kSmemMisc);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
 
-    const Piece pc = find_piece(args, blockIdx.x, lane);
+    const Piece pc = piece_of<kForm>(args, blockIdx.x, lane);
     if (pc.seq < 0) return;
     const int k0 = pc.k0, n_keys = pc.k1 - pc.k0;
+    const int n_rows = min(kHeads, pc.rows - pc.row0);
     const int nblk = (n_keys + kNB - 1) / kNB;
 
     if (threadIdx.x == 0) {
@@ -432,13 +446,20 @@ mla_chunk_small_kernel(const ChunkArgs args) {
         // finds the slot of position 32 b + j one block ahead of its copy ----
         const int pw = warp - kWarps;
         const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
-        int64_t slot = (pw < nblk && pw * kNB + lane < n_keys) ? chunk_slot(args, bt, k0 + pw * kNB + lane) : -1;
+        const uint32_t all = kForm == kDense ? 0u : tile_tokens(args, pc, n_rows);
+        uint32_t tokens = 0u, next_tokens = 0u;          // that attend the position, and the next block's
+        auto look_up = [&](int b, uint32_t& attending) -> int64_t {
+            attending = 0u;
+            if (b >= nblk || b * kNB + lane >= n_keys) return -1;
+            return kForm == kDense ? chunk_slot(args, bt, k0 + b * kNB + lane)
+                                   : form_slot<kForm>(args, pc, bt, k0 + b * kNB + lane, n_rows, attending);
+        };
+        int64_t slot = look_up(pw, tokens);
         int b = pw, cnt = 0;
         for (; b < nblk; b += kProducers, ++cnt) {
             const int s = b % kStages;
             const int nb = b + kProducers;
-            const int64_t next =
-                (nb < nblk && nb * kNB + lane < n_keys) ? chunk_slot(args, bt, k0 + nb * kNB + lane) : -1;
+            const int64_t next = look_up(nb, next_tokens);
             if (b >= kStages && !mbar_wait_bounded(&empty[s], static_cast<uint32_t>(((b / kStages) - 1) & 1))) {
                 if (lane == 0) atomicOr(args.err, MLA_ERR_PIPELINE_TIMEOUT);
                 break;
@@ -456,8 +477,13 @@ mla_chunk_small_kernel(const ChunkArgs args) {
             const int64_t first = __shfl_sync(0xffffffffu, slot, 0);
             // All 32 rows side by side in the cache, and nothing but rows as staged: one copy.
             const bool run = __all_sync(0xffffffffu, present && slot == first + lane) && args.row_bytes == kRowRead;
+            const unsigned whole = kForm == kDense ? mask : mask & __ballot_sync(0xffffffffu, (tokens & all) == all);
+            if (kForm != kDense) {
+                tokens_s[s * kNB + lane] = present ? tokens : 0u;
+                __syncwarp();
+            }
             if (lane == 0) {
-                vmask[s] = mask;
+                vmask[s] = whole;
                 mbar_arrive_expect_tx(&full[s], __popc(mask) * kRowRead);
             }
             __syncwarp();
@@ -467,6 +493,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
                 bulk_g2s(dst + lane * kStride, args.cache + slot * args.row_bytes, kRowRead, &full[s]);
             }
             slot = next;
+            tokens = next_tokens;
         }
         if (lane == 0) issued_s[pw] = cnt;
         __syncthreads();     // matches the consumers' final barrier
@@ -478,7 +505,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     const int c = lane & 3;
     uint32_t qraw[2][16];
     uint32_t qr[2][2];
-    int lim[2];                              // positions each row attends, counted from k0
+    int lim[2];                              // positions each row attends, counted from k0; else its token
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int row = pc.row0 + g + 8 * r;
@@ -487,7 +514,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) qraw[r][k] = 0u;
         if (row < pc.rows) {
-            lim[r] = row_limit(args, pc, row) - k0;
+            lim[r] = kForm == kDense ? row_limit(args, pc, row) - k0 : static_cast<int>(token_bit(args, pc, row));
             const __nv_bfloat16* qh = args.q + (pc.grow0 + row) * args.d_qk;
             const uint8_t* p = reinterpret_cast<const uint8_t*>(qh + 128 * warp + 32 * c);
 #pragma unroll
@@ -702,12 +729,14 @@ mla_chunk_small_kernel(const ChunkArgs args) {
             a.x += bq.x; a.y += bq.y; a.z += bq.z; a.w += bq.w;
         }
         float sv[4] = {a.x * rowf[0], a.y * rowf[0], a.z * rowf[1], a.w * rowf[1]};
-        if ((~present | poison) != 0u || kNB * (b + 1) > lim_all) {
+        if ((~present | poison) != 0u || (kForm == kDense && kNB * (b + 1) > lim_all)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = 8 * warp + 2 * c + (i & 1);
+                const bool attended = kForm == kDense ? ((present >> j) & 1u) != 0u && kNB * b + j < lim[i >> 1]
+                                                      : (tokens_s[s * kNB + j] & static_cast<uint32_t>(lim[i >> 1])) != 0u;
                 if (((poison >> j) & 1u) != 0u) sv[i] = __int_as_float(0x7FC00000);
-                if (((present >> j) & 1u) == 0u || kNB * b + j >= lim[i >> 1]) sv[i] = -INFINITY;
+                if (!attended) sv[i] = -INFINITY;
             }
         }
         const float bm0 = quad_max(fmaxf(sv[0], sv[1]));
@@ -851,7 +880,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int row = pc.row0 + g + 8 * r;
-        if (row >= pc.rows) continue;
+        if (row >= pc.rows || !row_lives<kForm>(args, pc, row)) continue;
         const float mm = lt[r] > 0.0f ? sigma / lt[r] : (lt[r] == 0.0f ? 0.0f : kNaN);
         const float lse = lt[r] > 0.0f ? (m_ref[r] + log2f(lt[r])) * kLn2 : (lt[r] == 0.0f ? -INFINITY : kNaN);
         // Thread (g, c) holds, for row r, dims 128w + 32c + 16e + 4q + i in
@@ -887,15 +916,6 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     }
 }
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-
-// Two CTAs of the kernel for few rows fit an SM, one of the kernel for many. A piece
-// shorter than the minimum saves less than its partial and its share of the merge cost.
-constexpr int kCtasPerSm = 2;
-constexpr int kMinPiece = 128;
-constexpr int kLargeMinPiece = 256;
 // What a piece costs beside its positions, in positions (few rows: 192 took 146 us for 90 sequences of up to
 // 16,384, 300 and 400 140; many: 384 to 640 are alike), and the shortest length tried, in eighths of
 // a place's share (few rows: 3 and 4 alike, 8 took 319 instead of 249 us for 200 sequences; many: 2 and 3
@@ -939,21 +959,6 @@ Sizes sizes_of(int T, int H, int n_seq, int64_t positions, int sms) {
     return z;
 }
 
-template <typename K, typename... A>
-bool launch(K kernel, int64_t grid, int threads, size_t smem, void* stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
-}
-
 }  // namespace
 
 extern "C" size_t mla_chunk_attention_workspace_bytes(int T, int H, int n_seq) {
@@ -965,10 +970,13 @@ extern "C" size_t mla_chunk_attention_workspace_bytes(int T, int H, int n_seq) {
     return few > many ? few : many;
 }
 
-extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
-                                   const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages,
-                                   int page_size, int causal, float sm_scale, void* out_bf16, float* lse,
-                                   void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+// The call of mla_chunk_attention, and of mla_tree_attention (`mask` and its words per token).
+int attend(Form form, const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
+           const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages, int page_size, int causal,
+           const uint32_t* mask, int mask_words, float sm_scale, void* out_bf16, float* lse, void* workspace,
+           size_t workspace_bytes, void* stream) {
     if (T < 0 || n_seq < 0 || max_pages < 0 || page_size <= 0 || kv.num_slots < 0 || !std::isfinite(sm_scale))
         return MLA_EINVAL;
     if (kv.row_bytes != MLA_ROW_BYTES && kv.row_bytes != MLA_ROW_BYTES_NOPE) return MLA_EINVAL;
@@ -980,23 +988,21 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
         static_cast<int64_t>(max_pages) * page_size > INT_MAX - 4096)      // positions, rounded up, are an int
         return MLA_EUNSUPPORTED;
     if (q_bf16 == nullptr || out_bf16 == nullptr || lse == nullptr || q_start == nullptr || kv_len == nullptr ||
-        (max_pages > 0 && (block_table == nullptr || kv.data == nullptr)))
+        (max_pages > 0 && (block_table == nullptr || kv.data == nullptr)) ||
+        (form == kTree && mask_words > 0 && mask == nullptr))
         return MLA_EINVAL;
     if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16) || !aligned(kv.data, 16) || !aligned(lse, 4) ||
-        !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
+        !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4) || !aligned(mask, 4))
         return MLA_EINVAL;
     int* err = mla_host::device_error_word();
     const int sms = mla_host::sm_count();
     if (err == nullptr || sms <= 0) return MLA_ECUDA;
-    const Sizes z = sizes_of(T, H, n_seq, static_cast<int64_t>(max_pages) * page_size, sms);
+    // (a tile's tokens have 32 bits: with one head the 64 rows of the kernel for many would be 64 tokens)
+    const int64_t positions = form == kTree && H == 1 ? 0 : static_cast<int64_t>(max_pages) * page_size;
+    const Sizes z = sizes_of(T, H, n_seq, positions, sms);
     if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < mla_chunk_attention_workspace_bytes(T, H, n_seq))
         return MLA_ENOWORKSPACE;
-    const bool rope = d_qk == kLatent + kRope;
-    const void* kernel = rope ? reinterpret_cast<const void*>(mla_chunk_small_kernel<true>)
-                              : reinterpret_cast<const void*>(mla_chunk_small_kernel<false>);
-    if (!mla_host::max_dynamic_smem(kernel, kSmemTotal)) return MLA_ECUDA;
-
-    ChunkArgs a;
+    ChunkArgs a = {};
     a.q = static_cast<const __nv_bfloat16*>(q_bf16);
     a.cache = static_cast<const uint8_t*>(kv.data);
     a.out = static_cast<__nv_bfloat16*>(out_bf16);
@@ -1013,6 +1019,8 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
     a.H = H;
     a.d_qk = d_qk;
     a.causal = causal != 0;
+    a.mask = mask;
+    a.mask_words = mask_words;
     a.sm_scale_log2 = sm_scale * kLog2e;
     a.err = err;
     a.tile_rows = z.tile_rows;
@@ -1034,12 +1042,54 @@ extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, m
         w += z.prefix;
     }
     if (!launch(chunk_plan_kernel, 1, kPlanThreads, 0, stream, a)) return MLA_ECUDA;
-    const bool ok = z.large ? mla_host::launch_chunk_large(a, z.max_pieces, rope, stream)
-                    : rope  ? launch(mla_chunk_small_kernel<true>, z.max_pieces, kThreads, kSmemTotal, stream, a)
-                            : launch(mla_chunk_small_kernel<false>, z.max_pieces, kThreads, kSmemTotal, stream, a);
-    if (!ok) return MLA_ECUDA;
-    const int64_t rows = static_cast<int64_t>(T) * H, held = static_cast<int64_t>(sms) * 16;
-    if (rows <= held) return launch(mla_chunk_merge_kernel<4>, rows, 32 * kMergeWarps, 0, stream, a) ? MLA_OK : MLA_ECUDA;
-    const int64_t ctas = (rows + kMergeWarps - 1) / kMergeWarps;
-    return launch(mla_chunk_merge_kernel<1>, ctas < held ? ctas : held, 32 * kMergeWarps, 0, stream, a) ? MLA_OK : MLA_ECUDA;
+    const bool ok = z.large ? mla_host::launch_chunk_large(a, form, z.max_pieces, stream)
+                            : mla_host::launch_chunk_small(a, form, z.max_pieces, stream);
+    return ok && mla_host::launch_chunk_merge(a, form, stream) ? MLA_OK : MLA_ECUDA;
 }
+
+}  // namespace
+
+extern "C" int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
+                                   const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages,
+                                   int page_size, int causal, float sm_scale, void* out_bf16, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    return attend(kDense, q_bf16, T, H, d_qk, kv, q_start, kv_len, block_table, n_seq, max_pages, page_size, causal, nullptr,
+                  0, sm_scale, out_bf16, lse, workspace, workspace_bytes, stream);
+}
+
+// The tree's form of the same call: positions of the context are every token's, those of the drafted tokens go by the
+// mask, which is read per position where it is one of theirs (form_slot).
+extern "C" int mla_tree_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
+                                  const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages,
+                                  int page_size, const uint32_t* mask, int mask_words, float sm_scale, void* out_bf16,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (mask_words < 0) return MLA_EINVAL;
+    return attend(kTree, q_bf16, T, H, d_qk, kv, q_start, kv_len, block_table, n_seq, max_pages, page_size, 0, mask,
+                  mask_words, sm_scale, out_bf16, lse, workspace, workspace_bytes, stream);
+}
+
+namespace mla_host {
+
+bool launch_chunk_small(const ChunkArgs& a, Form form, int64_t pieces, void* stream) {
+    const bool rope = a.d_qk == kLatent + kRope;
+    void (*kernel)(const ChunkArgs) = nullptr;
+    if (form == kDense) kernel = rope ? mla_chunk_small_kernel<true, kDense> : mla_chunk_small_kernel<false, kDense>;
+    if (form == kTree) kernel = rope ? mla_chunk_small_kernel<true, kTree> : mla_chunk_small_kernel<false, kTree>;
+    if (form == kBlocks) kernel = rope ? mla_chunk_small_kernel<true, kBlocks> : mla_chunk_small_kernel<false, kBlocks>;
+    const int smem = kSmemTotal + (form == kDense ? 0 : kSmemTokens);
+    if (!max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
+    return launch(kernel, pieces, kThreads, smem, stream, a);
+}
+
+bool launch_chunk_merge(const ChunkArgs& a, Form form, void* stream) {
+    const int sms = sm_count();
+    const int64_t rows = static_cast<int64_t>(a.T) * a.H, held = static_cast<int64_t>(sms) * 16;
+    const int64_t ctas = (rows + kMergeWarps - 1) / kMergeWarps;
+    if (rows <= held)
+        return launch(form == kBlocks ? mla_chunk_merge_kernel<4, kBlocks> : mla_chunk_merge_kernel<4, kDense>, rows,
+                      32 * kMergeWarps, 0, stream, a);
+    return launch(form == kBlocks ? mla_chunk_merge_kernel<1, kBlocks> : mla_chunk_merge_kernel<1, kDense>,
+                  ctas < held ? ctas : held, 32 * kMergeWarps, 0, stream, a);
+}
+
+}  // namespace mla_host

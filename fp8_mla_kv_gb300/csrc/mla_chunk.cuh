@@ -1,5 +1,5 @@
-// What the kernels of mla_chunk_attention share: their arguments, the plan of the
-// work and how a CTA finds its piece in it.
+// What the kernels of mla_chunk_attention, mla_tree_attention and mla_block_attention
+// share: their arguments, the plan of the work and how a CTA finds its piece in it.
 #pragma once
 
 #include "mla_device.cuh"
@@ -11,6 +11,19 @@ using namespace mla;
 constexpr int kSmallRows = 16;         // query rows per tile of the kernel for few rows
 constexpr int kLargeRows = 64;         // of the kernel for many rows
 constexpr int kLargeBlock = 128;       // positions per block there
+
+// What a token attends: the positions up to its own, or all of them (a limit for each query row); the context before
+// the chunk and those of the chunk's tokens that its mask names; or the positions up to its own of the blocks
+// that are listed for it. The last two have a mask of the tile's tokens for each position.
+enum Form { kDense, kTree, kBlocks };
+
+// kBlocks: a block that tokens of a group list.
+struct __align__(16) BlockEntry {
+    int32_t slot0;                     // of its first position
+    int32_t ahead;                     // that position, less the position of the group's first token
+    uint32_t tokens;                   // tokens of the group that list it
+    int32_t pad;
+};
 
 struct ChunkArgs {
     const __nv_bfloat16* q;
@@ -39,6 +52,14 @@ struct ChunkArgs {
     int32_t* split;                    // [n_seq] pieces per tile
     float* part_o;                     // [parts, tile_rows, 512] normalised partials
     float* part_lse;                   // [parts, tile_rows]
+    // kTree
+    const uint32_t* mask;              // [T, mask_words]: bit j of row t: token t attends its chunk's token j
+    int mask_words;
+    // kBlocks: groups of consecutive tokens, each with the blocks that any of its tokens lists, ascending
+    const BlockEntry* entries;         // [groups, entry_cap]
+    const int2* groups;                // [groups]: number of entries; tokens that are in a sequence
+    int entry_cap, group_tokens, group_tiles;      // group_tiles: tiles per group
+    int nk;                            // pieces per tile
 };
 
 // A sequence's new tokens and context, as far as they are valid.
@@ -73,7 +94,7 @@ __device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Seq& q) {
 }
 
 struct Piece {
-    int seq;                           // -1: no piece
+    int seq;                           // -1: no piece; kBlocks: the group
     Seq s;
     int row0, rows;                    // first query row of the tile; query rows of the sequence
     int64_t grow0;                     // the sequence's first row in q, out and lse
@@ -124,6 +145,48 @@ __device__ __forceinline__ int row_limit(const ChunkArgs& a, const Piece& p, int
     return token_limit(a, p.s, row / a.H);
 }
 
+// kBlocks: positions are counted through the group's entries, one block after the other. The pieces of a
+// tile are equal parts of them.
+__device__ __forceinline__ Piece block_piece(const ChunkArgs& a, int b) {
+    Piece p;
+    const int tile = b / a.nk, k = b - tile * a.nk;
+    p.seq = tile / a.group_tiles;
+    const int first = p.seq * a.group_tokens;
+    p.s.start = first;
+    p.s.n = min(a.group_tokens, a.T - first);
+    p.s.len = __ldg(&a.groups[p.seq].x) * a.page_size;
+    p.rows = p.s.n * a.H;
+    p.row0 = (tile - p.seq * a.group_tiles) * a.tile_rows;
+    p.grow0 = static_cast<int64_t>(first) * a.H;
+    const int per = ((p.s.len + a.nk - 1) / a.nk + a.align - 1) & ~(a.align - 1);
+    p.k0 = static_cast<int>(min(static_cast<int64_t>(p.s.len), static_cast<int64_t>(k) * per));
+    p.k1 = static_cast<int>(min(static_cast<int64_t>(p.s.len), static_cast<int64_t>(p.k0) + per));
+    p.part = a.nk > 1 ? tile * a.nk + k : -1;
+    // (a tile past the group's rows is none: the last group may have fewer)
+    if (p.row0 >= p.rows || __ldg(&a.groups[p.seq].y) == 0) p.seq = -1;
+    return p;
+}
+
+template <int kForm>
+__device__ __forceinline__ Piece piece_of(const ChunkArgs& a, int b, int lane) {
+    return kForm == kBlocks ? block_piece(a, b) : find_piece(a, b, lane);
+}
+
+// A tile's tokens are numbered from 0: the one of query row `row`, as a bit.
+__device__ __forceinline__ uint32_t token_bit(const ChunkArgs& a, const Piece& p, int row) {
+    return 1u << (row / a.H - p.row0 / a.H);
+}
+// All tokens of a tile (at most 32; rows: of the tile).
+__device__ __forceinline__ uint32_t tile_tokens(const ChunkArgs& a, const Piece& p, int rows) {
+    const int n = (p.row0 + rows - 1) / a.H - p.row0 / a.H + 1;
+    return 0xffffffffu >> (32 - n);
+}
+// Whether the query row belongs to a token that has an output.
+template <int kForm>
+__device__ __forceinline__ bool row_lives(const ChunkArgs& a, const Piece& p, int row) {
+    return kForm != kBlocks || ((static_cast<uint32_t>(__ldg(&a.groups[p.seq].y)) >> (row / a.H)) & 1u) != 0u;
+}
+
 // Slot of a position, or -1 when it is absent: no page there, the reserved slot, or a
 // slot past the cache (which is flagged).
 __device__ __forceinline__ int64_t chunk_slot(const ChunkArgs& a, const int32_t* bt, int pos) {
@@ -139,9 +202,69 @@ __device__ __forceinline__ int64_t chunk_slot(const ChunkArgs& a, const int32_t*
     return slot;
 }
 
+// The same for any form, with the tokens of the tile that attend the position (`rows` query rows in the tile).
+template <int kForm>
+__device__ __forceinline__ int64_t form_slot(const ChunkArgs& a, const Piece& p, const int32_t* bt, int pos, int rows,
+                                             uint32_t& tokens) {
+    if (kForm == kBlocks) {
+        const int e = pos / a.page_size, off = pos - e * a.page_size;
+        const int4 v = __ldg(reinterpret_cast<const int4*>(a.entries + static_cast<int64_t>(p.seq) * a.entry_cap + e));
+        const int64_t slot = static_cast<int64_t>(v.x) + off;
+        const int ahead = v.y + off;                 // token k of the group attends it from k = ahead on
+        tokens = ahead <= 0 ? v.z : ahead > 31 ? 0u : static_cast<uint32_t>(v.z) & (0xffffffffu << ahead);
+        if (slot == 0) return -1;
+        if (slot >= a.num_slots) {
+            atomicOr(a.err, MLA_ERR_DECODE_INDEX_RANGE);
+            return -1;
+        }
+        return slot;
+    }
+    tokens = 0xffffffffu;
+    const int j = pos - (p.s.len - p.s.n);
+    if (kForm == kTree && j >= 0) {
+        tokens = 0u;
+        const int t0 = p.row0 / a.H, n = (p.row0 + rows - 1) / a.H - t0 + 1;
+        if (j >> 5 < a.mask_words) {
+            const uint32_t* m = a.mask + (static_cast<int64_t>(p.s.start) + t0) * a.mask_words + (j >> 5);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) tokens |= ((__ldg(m + static_cast<int64_t>(i) * a.mask_words) >> (j & 31)) & 1u) << i;
+        }
+    }
+    return chunk_slot(a, bt, pos);
+}
+
+template <typename K, typename... A>
+bool launch(K kernel, int64_t grid, int threads, size_t smem, void* stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Two CTAs of the kernel for few rows fit an SM, one of the kernel for many. A piece
+// shorter than the minimum saves less than its partial and its share of the merge cost.
+constexpr int kCtasPerSm = 2;
+constexpr int kMinPiece = 128;
+constexpr int kLargeMinPiece = 256;
+
 }  // namespace mla_chunk
 
 namespace mla_host {
-// Launches the kernel for many query rows (grid bound `pieces`), false on a CUDA error.
-bool launch_chunk_large(const mla_chunk::ChunkArgs& a, int64_t pieces, bool rope, void* stream);
+// The kernel for few query rows, the kernel for many (grid bound `pieces`), and the merge of split tiles'
+// rows; false on a CUDA error.
+bool launch_chunk_small(const mla_chunk::ChunkArgs& a, mla_chunk::Form form, int64_t pieces, void* stream);
+bool launch_chunk_large(const mla_chunk::ChunkArgs& a, mla_chunk::Form form, int64_t pieces, void* stream);
+bool launch_chunk_merge(const mla_chunk::ChunkArgs& a, mla_chunk::Form form, void* stream);
 }

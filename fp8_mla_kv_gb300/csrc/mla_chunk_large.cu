@@ -98,17 +98,19 @@ struct __align__(16) RowData {               // per query row
     float neg_m[kRows];                      // exp2 offset (log2 units), negated
     float alpha[kRows];                      // what O^T and l are multiplied by when it moves; at the end 1 / l
     float shift[kRows];                      // undoes q's power of two
-    int lim[kRows];                          // positions it attends, counted from the piece's first
-    int unseen[kRows];                       // attends something, but nothing so far
+    int lim[kRows];                          // positions it attends, counted from the piece's first; else its token
+    int unseen[kRows];                       // attends something (else: may), but nothing so far
     float wmax[4][kRows];                    // by lane quarter: maxima; at the end sums of p
     float smax[kMetaWarps][4];               // largest scales, where a sigma moves
     int any_unseen[2], pad[2];
 };
+using Tokens = uint32_t[kN];                 // per position: the tile's tokens that attend it
 constexpr int kOffBars = kOffRow + static_cast<int>(sizeof(RowData));
 constexpr int kNumBars = 32;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
-constexpr int kSmemTotal = kOffMisc + 16;
-static_assert(kSmemTotal <= 232448, "shared memory");
+constexpr int kOffTokens = kOffMisc + 16;
+template <int kForm> constexpr int kSmemTotal = kOffTokens + (kForm == kDense ? 0 : kMeta * static_cast<int>(sizeof(Tokens)));
+static_assert(kSmemTotal<kBlocks> <= 232448, "shared memory");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColA = 4 * kRows, kColS = kColA + 128; // O^T tiles, four A slots of 32, two S slots of 64
@@ -310,12 +312,13 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-template <bool kRopeOn>
+template <bool kRopeOn, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
 mla_chunk_large_kernel(const ChunkArgs args) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Meta* meta = reinterpret_cast<Meta*>(smem + kOffMeta);
     RowData& rd = *reinterpret_cast<RowData*>(smem + kOffRow);
+    Tokens* tokens_s = reinterpret_cast<Tokens*>(smem + kOffTokens);     // [kMeta]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
     uint64_t* afull = bars;            // [4] A slot written (8 converting warps)
     uint64_t* afree = bars + 4;        // [4] its QK is done (commit)
@@ -335,7 +338,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
-    const Piece pc = find_piece(args, static_cast<int>(blockIdx.x), lane);
+    const Piece pc = piece_of<kForm>(args, static_cast<int>(blockIdx.x), lane);
     if (pc.seq < 0) return;
     if ((smem_u32(smem) & 1023u) != 0u) {      // the operand layout's phase would be off: no result
         if (threadIdx.x == 0) atomicOr(args.err, MLA_ERR_PIPELINE_TIMEOUT);
@@ -344,6 +347,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     const int n_keys = pc.k1 - pc.k0;
     const int nblk = (n_keys + kN - 1) / kN;
     const int n_rows = min(kRows, pc.rows - pc.row0);
+    const uint32_t all = kForm == kDense ? 0u : tile_tokens(args, pc, n_rows);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kASlots; ++i) {
@@ -375,9 +379,15 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (threadIdx.x < kRows) {
-        const int r = threadIdx.x, lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
-        rd.lim[r] = lim;
-        rd.unseen[r] = lim > 0;
+        const int r = threadIdx.x;
+        if (kForm == kDense) {
+            const int lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
+            rd.lim[r] = lim;
+            rd.unseen[r] = lim > 0;
+        } else {
+            rd.lim[r] = r < n_rows ? static_cast<int>(token_bit(args, pc, pc.row0 + r)) : 0;
+            rd.unseen[r] = r < n_rows;
+        }
         rd.neg_m[r] = 0.0f;
     }
     // ---- q of the tile's rows as operand tiles: a warp per row, lane l the 16-byte units
@@ -474,6 +484,10 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             // A wait that ran out only skips work up to the vote, which all four warps take.
             ok = warp_wait(&mfull[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
             int state = mt.state[key];
+            const uint32_t tokens = kForm == kDense ? 0u : tokens_s[b % kMeta][key];
+            auto attends = [&](int c) {                // (of a position that is there)
+                return kForm == kDense ? kN * b + key < rd.lim[c0 + c] : (tokens & static_cast<uint32_t>(rd.lim[c0 + c])) != 0u;
+            };
             uint64_t s[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) s[j] = 0ull;
@@ -514,11 +528,12 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 d[c + 2] = lo_of(s[c / 2 + 1]);
                 d[c + 3] = hi_of(s[c / 2 + 1]);
             }
-            if (__builtin_expect(__any_sync(0xffffffffu, state != 1) || kN * (b + 1) > lim_min, 0)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, state != 1 || (kForm != kDense && (tokens & all) != all)) ||
+                                     (kForm == kDense && kN * (b + 1) > lim_min), kForm == kBlocks)) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) {
                     if (state == 2) d[c] = __int_as_float(0x7FC00000);
-                    if (state == 0 || kN * b + key >= rd.lim[c0 + c]) d[c] = -INFINITY;
+                    if (state == 0 || !attends(c)) d[c] = -INFINITY;
                 }
             }
             float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -549,7 +564,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                         state = 2;
 #pragma unroll
                         for (int c = 0; c < kCols; ++c)
-                            if (kN * b + key < rd.lim[c0 + c]) d[c] = __int_as_float(0x7FC00000);
+                            if (attends(c)) d[c] = __int_as_float(0x7FC00000);
                     }
 #pragma unroll 1
                     for (int t = 0; t < 4; ++t) {
@@ -675,7 +690,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 const float kNaN = __int_as_float(0x7FC00000);
                 rd.alpha[c] = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : kNaN);
                 const float lse = sum > 0.0f ? (log2f(sum) - rd.neg_m[c]) * kLn2 : (sum == 0.0f ? -INFINITY : kNaN);
-                if (c < n_rows) {
+                if (c < n_rows && row_lives<kForm>(args, pc, pc.row0 + c)) {
                     if (pc.part < 0) args.lse[pc.grow0 + pc.row0 + c] = lse;
                     else args.part_lse[static_cast<int64_t>(pc.part) * kRows + c] = lse;
                 }
@@ -697,7 +712,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                     __nv_bfloat16* to = args.out + (pc.grow0 + pc.row0 + c0) * kLatent + dim;
 #pragma unroll
                     for (int c = 0; c < kCols; ++c)
-                        if (c < left) to[c * kLatent] = __float2bfloat16_rn(__uint_as_float(o[c]) * (f * rd.alpha[c0 + c]));
+                        if (c < left && row_lives<kForm>(args, pc, pc.row0 + c0 + c)) to[c * kLatent] = __float2bfloat16_rn(__uint_as_float(o[c]) * (f * rd.alpha[c0 + c]));
                 } else {
                     float* to = args.part_o + (static_cast<int64_t>(pc.part) * kRows + c0) * kLatent + dim;
 #pragma unroll
@@ -866,18 +881,21 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
         float sigma[4] = {0.0f, 0.0f, 0.0f, 0.0f}, inv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         int slot[kPer], slot1[kPer];                   // of blocks b and b + 1
+        uint32_t tokens[kPer], tokens1[kPer];          // that attend them
         uint4 u[kPer];                                 // their scales
         auto look_up = [&](int b) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int j = kN * b + 32 * (kPer * mw + i) + lane;
-                slot1[i] = j < n_keys ? static_cast<int>(chunk_slot(args, bt, pc.k0 + j)) : -1;
+                if (kForm == kDense) slot1[i] = j < n_keys ? static_cast<int>(chunk_slot(args, bt, pc.k0 + j)) : -1;
+                else slot1[i] = j < n_keys ? static_cast<int>(form_slot<kForm>(args, pc, bt, pc.k0 + j, n_rows, tokens1[i])) : -1;
             }
         };
         auto fetch = [&]() {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 slot[i] = slot1[i];
+                if (kForm != kDense) tokens[i] = tokens1[i];
                 u[i] = ld_row(args.cache, slot[i], row_bytes, kScaleOff);
                 if (slot[i] >= 0) {
                     const uint8_t* row = args.cache + static_cast<uint64_t>(static_cast<uint32_t>(slot[i])) * row_bytes;
@@ -968,6 +986,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             for (int i = 0; i < kPer; ++i) {
                 const int j = 32 * (kPer * mw + i) + lane;
                 mt.slot[j] = slot[i];
+                if (kForm != kDense) tokens_s[b % kMeta][j] = slot[i] < 0 ? 0u : tokens[i];
                 mt.state[j] = static_cast<uint8_t>(state[i]);
             }
             warp_arrive(&mfull[b % kMeta]);
@@ -993,23 +1012,15 @@ mla_chunk_large_kernel(const ChunkArgs args) {
 
 namespace mla_host {
 
-bool launch_chunk_large(const mla_chunk::ChunkArgs& a, int64_t pieces, bool rope, void* stream) {
-    const void* kernel = rope ? reinterpret_cast<const void*>(mla_chunk_large_kernel<true>)
-                              : reinterpret_cast<const void*>(mla_chunk_large_kernel<false>);
-    if (!max_dynamic_smem(kernel, kSmemTotal)) return false;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pieces));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemTotal;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return (rope ? cudaLaunchKernelEx(&cfg, mla_chunk_large_kernel<true>, a)
-                 : cudaLaunchKernelEx(&cfg, mla_chunk_large_kernel<false>, a)) == cudaSuccess &&
-           cudaGetLastError() == cudaSuccess;
+bool launch_chunk_large(const mla_chunk::ChunkArgs& a, mla_chunk::Form form, int64_t pieces, void* stream) {
+    const bool rope = a.d_qk == kLatent + kRope;
+    void (*kernel)(const ChunkArgs) = nullptr;
+    if (form == kDense) kernel = rope ? mla_chunk_large_kernel<true, kDense> : mla_chunk_large_kernel<false, kDense>;
+    if (form == kTree) kernel = rope ? mla_chunk_large_kernel<true, kTree> : mla_chunk_large_kernel<false, kTree>;
+    if (form == kBlocks) kernel = rope ? mla_chunk_large_kernel<true, kBlocks> : mla_chunk_large_kernel<false, kBlocks>;
+    const int smem = form == kDense ? kSmemTotal<kDense> : kSmemTotal<kBlocks>;
+    if (!max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
+    return launch(kernel, pieces, kThreads, smem, stream, a);
 }
 
 }  // namespace mla_host

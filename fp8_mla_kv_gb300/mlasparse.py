@@ -36,7 +36,9 @@ MLA_ERR_POOL_EMPTY = 0x80
 SYMBOLS = ("mla_kv_write", "mla_sparse_decode", "mla_sparse_decode_workspace_bytes",
            "mla_sparse_decode_paged", "mla_sparse_prefill", "mla_sparse_prefill_paged",
            "mla_gather_upconvert", "mla_rope", "mla_rope_kv_write", "mla_chunk_attention",
-           "mla_chunk_attention_workspace_bytes", "mla_page_copy", "mla_page_free", "mla_page_fork",
+           "mla_chunk_attention_workspace_bytes", "mla_block_keys", "mla_block_scores", "mla_block_select",
+           "mla_block_attention", "mla_block_attention_workspace_bytes", "mla_tree_mask", "mla_tree_attention",
+           "mla_tree_commit", "mla_page_copy", "mla_page_free", "mla_page_fork",
            "mla_page_compact", "mla_page_workspace_bytes", "mla_get_error", "mla_strerror")
 
 
@@ -104,6 +106,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.mla_chunk_attention.restype = i32
             lib.mla_chunk_attention.argtypes = [vp, i32, i32, i32, KVCache, vp, vp, vp, i32, i32, i32, i32, c.c_float,
                                                 vp, vp, vp, c.c_size_t, vp]
+            lib.mla_block_keys.restype = i32
+            lib.mla_block_keys.argtypes = [KVCache, i32, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp]
+            lib.mla_block_scores.restype = i32
+            lib.mla_block_scores.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp, vp, i32, i32, i32, c.c_float, vp, vp]
+            lib.mla_block_select.restype = i32
+            lib.mla_block_select.argtypes = [vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+            lib.mla_block_attention_workspace_bytes.restype = c.c_size_t
+            lib.mla_block_attention_workspace_bytes.argtypes = [i32, i32, i32]
+            lib.mla_block_attention.restype = i32
+            lib.mla_block_attention.argtypes = [vp, i32, i32, i32, KVCache, vp, i32, vp, vp, vp, i32, i32, i32, c.c_float,
+                                                vp, vp, vp, c.c_size_t, vp]
+            lib.mla_tree_mask.restype = i32
+            lib.mla_tree_mask.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, vp]
+            lib.mla_tree_attention.restype = i32
+            lib.mla_tree_attention.argtypes = [vp, i32, i32, i32, KVCache, vp, vp, vp, i32, i32, i32, vp, i32, c.c_float,
+                                               vp, vp, vp, c.c_size_t, vp]
+            lib.mla_tree_commit.restype = i32
+            lib.mla_tree_commit.argtypes = [KVCache, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp]
             lib.mla_page_copy.restype = i32
             lib.mla_page_copy.argtypes = [KVCache, KVCache, i32, vp, vp, i64, vp]
             lib.mla_page_free.restype = i32
@@ -458,6 +478,189 @@ def _ints(*ts) -> None:
     for t in ts:
         if t is not None:
             assert t.dtype == torch.int32 and t.is_contiguous()
+
+
+def _batch(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor | None) -> int:
+    """Checks a ragged batch's lengths and table; returns its number of sequences."""
+    _ints(q_start, kv_len, block_table)
+    n_seq = int(kv_len.numel())
+    assert q_start.numel() == n_seq + 1
+    assert block_table is None or (block_table.dim() == 2 and block_table.shape[0] == n_seq)
+    return n_seq
+
+
+def mla_block_keys(cache: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
+                   page_size: int, keys: torch.Tensor, n_tokens: int, stream=None) -> torch.Tensor:
+    """Mean keys of the pages that the new tokens completed, into keys bf16 [num_pages, 576 or 512]; n_tokens: the tokens
+    that q_start counts. With q_start counting all of kv_len, the keys of every complete page."""
+    _same_device(cache, q_start, kv_len, block_table, keys)
+    n_seq = _batch(q_start, kv_len, block_table)
+    assert keys.dtype == torch.bfloat16 and keys.is_contiguous() and keys.dim() == 2
+    rc = load().mla_block_keys(kv_cache(cache), int(keys.shape[1]), q_start.data_ptr(), kv_len.data_ptr(),
+                               block_table.data_ptr(), n_seq, int(block_table.shape[1]), int(page_size), int(n_tokens),
+                               keys.data_ptr(), int(keys.shape[0]), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_block_keys")
+    return keys
+
+
+def mla_block_scores(q: torch.Tensor, keys: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                     block_table: torch.Tensor, page_size: int, sm_scale: float, scores: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """scores fp32 [T, max_pages]: per token, summed over heads, the softmax of q . key over the complete blocks before its
+    own. Other columns are left alone (without `scores`: -inf)."""
+    _same_device(q, keys, q_start, kv_len, block_table, scores)
+    T, H, d_qk = (int(s) for s in q.shape)
+    n_seq = _batch(q_start, kv_len, block_table)
+    assert q.dtype == torch.bfloat16 and q.is_contiguous()
+    assert keys.dtype == torch.bfloat16 and keys.is_contiguous() and keys.dim() == 2 and keys.shape[1] == d_qk
+    if scores is None:
+        with _on(stream):
+            scores = torch.full((T, block_table.shape[1]), float("-inf"), dtype=torch.float32, device=q.device)
+    assert scores.dtype == torch.float32 and scores.is_contiguous() and scores.shape == (T, block_table.shape[1])
+    rc = load().mla_block_scores(q.data_ptr(), T, H, d_qk, keys.data_ptr(), int(keys.shape[0]), q_start.data_ptr(),
+                                 kv_len.data_ptr(), block_table.data_ptr(), n_seq, int(block_table.shape[1]),
+                                 int(page_size), float(sm_scale), scores.data_ptr(), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_block_scores")
+    return scores
+
+
+def mla_block_select(scores: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, page_size: int, width: int,
+                     sink: int = 1, local: int = 1, blocks: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """blocks int32 [T, width]: the first `sink` blocks, the last `local` up to the token's own, and the best others by
+    scores [T, max_pages]; ascending, then -1 (without `blocks`, -1 for tokens outside every sequence)."""
+    _same_device(scores, q_start, kv_len, blocks)
+    n_seq = _batch(q_start, kv_len, None)
+    assert scores.dtype == torch.float32 and scores.is_contiguous() and scores.dim() == 2
+    T = int(scores.shape[0])
+    if blocks is None:
+        with _on(stream):
+            blocks = torch.full((T, int(width)), -1, dtype=torch.int32, device=scores.device)
+    _ints(blocks)
+    assert blocks.shape == (T, int(width))
+    rc = load().mla_block_select(scores.data_ptr(), T, int(scores.shape[1]), q_start.data_ptr(), kv_len.data_ptr(), n_seq,
+                                 int(page_size), int(sink), int(local), int(width), blocks.data_ptr(), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_block_select")
+    return blocks
+
+
+def mla_block_attention_workspace_bytes(T: int, H: int, width: int) -> int:
+    return int(load().mla_block_attention_workspace_bytes(int(T), int(H), int(width)))
+
+
+def alloc_block_workspace(T: int, H: int, width: int, device=None) -> torch.Tensor:
+    return torch.empty(max(16, mla_block_attention_workspace_bytes(T, H, width)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def mla_block_attention(q: torch.Tensor, cache: torch.Tensor, blocks: torch.Tensor, q_start: torch.Tensor,
+                        kv_len: torch.Tensor, block_table: torch.Tensor, page_size: int, sm_scale: float,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Attention of each token over the positions up to its own of its blocks (int32 [T, width], -1: none): q bf16
+    [T, H, d_qk]. Returns (out bf16 [T, H, 512], lse fp32 [T, H]); without `out` and `lse`, tokens outside every sequence
+    get 0 and -inf."""
+    _same_device(q, cache, blocks, q_start, kv_len, block_table, out, lse, workspace)
+    T, H, d_qk = (int(s) for s in q.shape)
+    n_seq = _batch(q_start, kv_len, block_table)
+    assert q.dtype == torch.bfloat16 and q.is_contiguous()
+    _ints(blocks)
+    assert blocks.dim() == 2 and blocks.shape[0] == T
+    width = int(blocks.shape[1])
+    out, lse = _outputs(q, out, lse, stream)
+    if workspace is None:
+        with _on(stream):
+            workspace = alloc_block_workspace(T, H, width, q.device)
+    rc = load().mla_block_attention(q.data_ptr(), T, H, d_qk, kv_cache(cache), blocks.data_ptr(), width,
+                                    q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), n_seq,
+                                    int(block_table.shape[1]), int(page_size), float(sm_scale), out.data_ptr(),
+                                    lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_block_attention")
+    return out, lse
+
+
+def _outputs(q: torch.Tensor, out: torch.Tensor | None, lse: torch.Tensor | None, stream):
+    """out bf16 [T, H, 512] and lse fp32 [T, H] as given, or made: 0 and -inf."""
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if out is None or lse is None:
+        with _on(stream):
+            if out is None:
+                out = torch.zeros((T, H, 512), dtype=torch.bfloat16, device=q.device)
+            if lse is None:
+                lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q.device)
+    assert out.dtype == torch.bfloat16 and out.is_contiguous() and out.numel() == T * H * 512
+    assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == T * H
+    return out, lse
+
+
+def mla_tree_mask(parent: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, words: int | None = None,
+                  mask: torch.Tensor | None = None, positions: torch.Tensor | None = None, stream=None):
+    """For drafted tokens with parents int32 [T] (indices within their sequence; negative: none): (mask int32 [T, words],
+    bits for the token and its ancestors; positions int32 [T], for the rotary write). `words`: 32 tokens of a sequence
+    each, where no mask is given (2 unless said)."""
+    _same_device(parent, q_start, kv_len, mask, positions)
+    n_seq = _batch(q_start, kv_len, None)
+    T = int(parent.numel())
+    if mask is None or positions is None:
+        with _on(stream):
+            if mask is None:
+                mask = torch.zeros((T, 2 if words is None else int(words)), dtype=torch.int32, device=parent.device)
+            if positions is None:
+                positions = torch.zeros(T, dtype=torch.int32, device=parent.device)
+    _ints(parent, mask, positions)
+    assert mask.dim() == 2 and mask.shape[0] == T and positions.numel() == T
+    rc = load().mla_tree_mask(parent.data_ptr(), T, q_start.data_ptr(), kv_len.data_ptr(), n_seq, mask.data_ptr(),
+                              int(mask.shape[1]), positions.data_ptr(), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_tree_mask")
+    return mask, positions
+
+
+def mla_tree_attention(q: torch.Tensor, cache: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                       block_table: torch.Tensor, page_size: int, sm_scale: float, mask: torch.Tensor,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """mla_chunk_attention with a mask among the new tokens (int32 [T, words], as mla_tree_mask makes it). The workspace is
+    alloc_chunk_workspace's."""
+    _same_device(q, cache, q_start, kv_len, block_table, mask, out, lse, workspace)
+    T, H, d_qk = (int(s) for s in q.shape)
+    n_seq = _batch(q_start, kv_len, block_table)
+    assert q.dtype == torch.bfloat16 and q.is_contiguous()
+    _ints(mask)
+    assert mask.dim() == 2 and mask.shape[0] == T
+    out, lse = _outputs(q, out, lse, stream)
+    if workspace is None:
+        with _on(stream):
+            workspace = alloc_chunk_workspace(T, H, n_seq, q.device)
+    rc = load().mla_tree_attention(q.data_ptr(), T, H, d_qk, kv_cache(cache), q_start.data_ptr(), kv_len.data_ptr(),
+                                   block_table.data_ptr(), n_seq, int(block_table.shape[1]), int(page_size),
+                                   mask.data_ptr(), int(mask.shape[1]), float(sm_scale), out.data_ptr(), lse.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_tree_attention")
+    return out, lse
+
+
+def mla_tree_commit(cache: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
+                    page_size: int, path: torch.Tensor, path_len: torch.Tensor, kv_len_out: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Rows of the accepted tokens path[s, :path_len[s]] (int32 [n_seq, max_path], ascending indices within the sequence)
+    to the front of the drafted ones; kv_len_out (may be kv_len) receives the new lengths."""
+    _same_device(cache, q_start, kv_len, block_table, path, path_len, kv_len_out)
+    n_seq = _batch(q_start, kv_len, block_table)
+    _ints(path, path_len, kv_len_out)
+    assert path.dim() == 2 and path.shape[0] == n_seq and path_len.numel() == n_seq
+    assert kv_len_out is None or kv_len_out.numel() == n_seq
+    rc = load().mla_tree_commit(kv_cache(cache), q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), n_seq,
+                                int(block_table.shape[1]), int(page_size), path.data_ptr(), path_len.data_ptr(),
+                                int(path.shape[1]), kv_len_out.data_ptr() if kv_len_out is not None else None,
+                                _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_tree_commit")
 
 
 def mla_page_workspace_bytes(num_pages: int, n_forks: int = 0) -> int:

@@ -62,8 +62,8 @@ extern "C" {
 #define MLA_ERR_DECODE_INDEX_RANGE 0x2  /* mla_sparse_decode: index >= num_slots, entry absent */
 #define MLA_ERR_PIPELINE_TIMEOUT   0x4  /* a kernel's bounded wait on its own copies ran out */
 #define MLA_ERR_GATHER_INDEX_RANGE 0x8  /* mla_gather_upconvert: slot >= num_slots, zero row */
-#define MLA_ERR_CHUNK_RANGE        0x10 /* mla_chunk_attention: q_start not nondecreasing within [0, T], or kv_len past the table */
-#define MLA_ERR_PAGE_RANGE         0x20 /* mla_page_*: a page, row or length out of range, dropped */
+#define MLA_ERR_CHUNK_RANGE        0x10 /* mla_chunk_attention, mla_block_*, mla_tree_*: q_start not nondecreasing within [0, T], kv_len past the table, or a tree out of order */
+#define MLA_ERR_PAGE_RANGE         0x20 /* mla_page_*, mla_block_keys, mla_block_scores, mla_tree_commit: a page, row or length out of range, dropped */
 #define MLA_ERR_PAGE_COUNT         0x40 /* mla_page_free: a page whose count was 0 already */
 #define MLA_ERR_POOL_EMPTY         0x80 /* mla_page_fork: no free page left, the entry stays -1 */
 
@@ -407,6 +407,124 @@ int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache
                         const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages, int page_size,
                         int causal, float sm_scale, void* out_bf16, float* lse, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/*
+ * Block-sparse attention over the paged cache. A block is a page; block b of a sequence is its positions b * page_size ..
+ * (b + 1) * page_size - 1, in page block_table[s, b]. Ragged batches as in mla_chunk_attention: sequence s has the
+ * tokens q_start[s] .. q_start[s+1]-1 and kv_len[s] positions, its tokens' last, so its token i stands at position
+ * kv_len[s] - n + i (one past the table counts as the table's last; flagged MLA_ERR_CHUNK_RANGE), and its own
+ * block is the one that holds that position. A q_start that is not nondecreasing within [0, T] is flagged
+ * MLA_ERR_CHUNK_RANGE, and which tokens count as being in a sequence is then unspecified. Tokens outside
+ * every sequence keep what their outputs hold. Lengths are read on the device, so a captured call serves any. As calls in turn:
+ *   mla_rope_kv_write, mla_block_keys, mla_block_scores, mla_block_select, mla_block_attention.
+ * All are launched with programmatic stream serialization. max_pages * page_size is below 2^31 - 4096
+ * (otherwise MLA_EUNSUPPORTED); q_start, kv_len and block_table as in mla_chunk_attention.
+ *
+ * mla_block_keys - the mean key of each page that the new tokens completed:
+ *   keys[p] = (sum over the rows of page p of [latent (code x scale), rope]) / rows, fp32 sums, rounded to BF16 once.
+ * Sequence s completes its blocks floor((kv_len - n) / page_size) .. floor(kv_len / page_size) - 1: with n = kv_len all that are
+ * complete (after pages have moved, say). The reserved slot 0 is no row: page 0 has page_size - 1. Blocks without
+ * a page are skipped; a page >= num_keys or one that ends past the cache is flagged MLA_ERR_PAGE_RANGE (the first has no
+ * key, the second that of its rows in the cache). A row that is not finite makes its key so, in the values concerned.
+ *   kv         the cache (row_bytes 656, or 528 with d_qk 512);  d_qk  576 or 512
+ *   T          the tokens that q_start counts (its last value at most)
+ *   keys_bf16  bf16 [num_keys, d_qk], device, 16-byte aligned; page p's key at row p, other rows are left alone
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED or MLA_ECUDA.
+ */
+int mla_block_keys(mla_kv_cache_t kv, int d_qk, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                   int n_seq, int max_pages, int page_size, int T, void* keys_bf16, int num_keys, void* stream);
+
+/*
+ * mla_block_scores - how much token t wants each complete block before its own:
+ *   scores[t, b] = sum over h < H of softmax over b of ( sm_scale * q[t, h] . keys[block_table[s, b]] ),
+ * b < floor(position / page_size). Products are exact and summed in fp32, as are the exponentials; no
+ * score is written for other blocks. A block without a page, or whose page is >= num_keys (flagged
+ * MLA_ERR_PAGE_RANGE), gets -inf and no part in the softmax. A key or query row that is not finite makes the
+ * scores unspecified for exactly the tokens that meet it.
+ *   q_bf16     bf16 [T, H, d_qk] row-major, device, 16-byte aligned; H 1..128; T * H below 2^29
+ *   keys_bf16  bf16 [num_keys, d_qk] row-major, device, 16-byte aligned
+ *   scores     fp32 [T, max_pages], device
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED or MLA_ECUDA.
+ */
+int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, const void* keys_bf16, int num_keys,
+                     const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages,
+                     int page_size, float sm_scale, float* scores, void* stream);
+
+/*
+ * mla_block_select - the blocks that each token attends: the first `sink` blocks and the last `local` up to its own
+ * (its own among them), and of those between the ones with the highest scores, `width` in all. Of equal scores the
+ * lower block is taken; a block between whose score is -inf or NaN is not. Row t of `blocks` receives them in
+ * ascending order, then -1. A token at a negative position gets -1 throughout.
+ *   scores   fp32 [T, columns], device: a column for each block of the table
+ *   sink >= 0, local >= 1, sink + local <= width (otherwise MLA_EINVAL)
+ *   blocks   int32 [T, width], device
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED or MLA_ECUDA.
+ */
+int mla_block_select(const float* scores, int T, int columns, const int32_t* q_start, const int32_t* kv_len, int n_seq,
+                     int page_size, int sink, int local, int width, int32_t* blocks, void* stream);
+
+/*
+ * mla_block_attention - attention of each token over the positions up to its own of the blocks listed for it.
+ * out and lse as in mla_chunk_attention over those positions (absent positions, empty rows, rows that are not finite,
+ * precision: as there). A negative entry lists nothing; a block listed twice counts once; the order does not matter; a block
+ * past the token's own has no position for it. A block >= max_pages is absent and flagged
+ * MLA_ERR_DECODE_INDEX_RANGE, as is a page past the cache.
+ *   blocks       int32 [T, width], device, as mla_block_select writes them
+ *   workspace    device scratch of mla_block_attention_workspace_bytes(T, H, width) bytes, 16-byte aligned; as there
+ *   others       as mla_chunk_attention. min(width, max_pages) * page_size * (tokens in 64 query rows) is below 2^31 - 4096
+ *                (otherwise MLA_EUNSUPPORTED)
+ * The sizes decide which of two kernels runs, and how lists are cut; results agree to rounding.
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED, MLA_ENOWORKSPACE or MLA_ECUDA.
+ */
+size_t mla_block_attention_workspace_bytes(int T, int H, int width);
+int mla_block_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* blocks, int width,
+                        const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int n_seq,
+                        int max_pages, int page_size, float sm_scale, void* out_bf16, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Drafted trees. The n tokens of a sequence are drafted ones whose rows are the last n of its kv_len positions,
+ * in an order in which parents come first. As calls in turn: mla_tree_mask (the positions that their rotary parts
+ * are turned by), mla_rope_kv_write, mla_tree_attention, and once a path is accepted mla_tree_commit. Lengths are read
+ * on the device; launched with programmatic stream serialization.
+ *
+ * mla_tree_mask - for token i of a sequence, parent[q_start[s] + i] is the index within the sequence of the
+ * token before it (negative: it follows the context). Row t of `mask` receives a bit for the token itself and each of
+ * its ancestors (bit j % 32 of word j / 32: token j), positions[t] (may be NULL) kv_len - n + its depth: the number of its
+ * ancestors. A parent that does not come before its child counts as none, and a token j >= 32 * mask_words
+ * has no bit; both are flagged MLA_ERR_CHUNK_RANGE. (With mask_words 0 only positions are made.)
+ *   parent, positions  int32 [T], device;  mask  uint32 [T, mask_words], device
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+int mla_tree_mask(const int32_t* parent, int T, const int32_t* q_start, const int32_t* kv_len, int n_seq, uint32_t* mask,
+                  int mask_words, int32_t* positions, void* stream);
+
+/*
+ * mla_tree_attention - mla_chunk_attention with a mask among the new tokens: a token attends every position below
+ * kv_len - n and, of the others, position kv_len - n + j if bit j of its row of `mask` is set (any mask: also
+ * one with later tokens, or empty; a token j >= 32 * mask_words is attended by none). All else as mla_chunk_attention,
+ * its workspace (mla_chunk_attention_workspace_bytes) included.
+ *   mask      uint32 [T, mask_words], device, 4-byte aligned
+ */
+int mla_tree_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t kv, const int32_t* q_start,
+                       const int32_t* kv_len, const int32_t* block_table, int n_seq, int max_pages, int page_size,
+                       const uint32_t* mask, int mask_words, float sm_scale, void* out_bf16, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * mla_tree_commit - moves the rows of the accepted tokens path[s, 0 .. path_len[s]-1] (indices within the sequence,
+ * ascending) to positions kv_len - n, kv_len - n + 1, ..; kv_len_out[s] (may be NULL, or kv_len itself)
+ * becomes kv_len - n + path_len. A path is cut before an entry that is not above the one before it or not
+ * one of the tokens, and to its max_path entries; a sequence with fewer positions than tokens, or more than the
+ * table, keeps its rows and length; both are flagged MLA_ERR_CHUNK_RANGE. A row whose position, old or new, has no
+ * page, is the reserved slot or lies past the cache is not moved and flagged MLA_ERR_PAGE_RANGE.
+ * Precondition: no two sequences share the pages of their drafted tokens.
+ *   path      int32 [n_seq, max_path], device;  path_len, kv_len_out  int32 [n_seq], device
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED or MLA_ECUDA.
+ */
+int mla_tree_commit(mla_kv_cache_t kv, const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int n_seq,
+                    int max_pages, int page_size, const int32_t* path, const int32_t* path_len, int max_path,
+                    int32_t* kv_len_out, void* stream);
 
 /*
  * Pages of a cache. Page p is the slots p * page_size .. (p + 1) * page_size - 1; pages
