@@ -1,6 +1,19 @@
 // mla_block_scores: how much each token's heads want each complete block before the token's own,
 //   score[t, b] = sum over heads h of softmax over b of (sm_scale q[t, h] . K_b),
 // K_b the mean keys of mla_block_keys.
+//
+// A product of two matrices with a softmax over its rows and a sum over its rows' heads, on tcgen05: a tile is 128
+// (token, head) rows of one sequence, its columns are the sequence's blocks, 256 of them in fp32 in tensor memory, where
+// they stay until the rows' sums are known: nothing is multiplied twice or goes through memory. Up to
+// eight CTAs (a cluster) take a tile's columns in parts and exchange the rows' maxima and sums through
+// their shared memory; beyond 2,048 blocks a CTA has several rounds of 256 and multiplies twice.
+// A warp's 32 rows are whole tokens where a token has at most 32 heads (lanes left over stay empty), so that the sum
+// over heads is one warp's; two or four warps share a token with more.
+//
+// Roles: warps 0-3 softmax (TMEM lanes 32 w ..), 4-7 copy (16 bytes a thread and time, cp.async, since keys
+// lie wherever the block table says), 8 issues the products. q and keys come in tiles of 128 rows x 64 dims
+// (128 bytes a row, 128-byte swizzle) through a ring; for each 64 dims one of q and up to two of keys.
+// TIME_SCORES
 #include <climits>
 #include <cmath>
 
@@ -11,7 +24,28 @@ namespace {
 using namespace mla;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSoftWarps = 4, kLoadWarps = 4, kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kRows = 128;                                 // M
+constexpr int kCols = 256;                                 // columns a round: tensor memory of a CTA
+constexpr int kTileKeys = 128;                             // keys per ring tile
+constexpr int kTileBytes = 128 * 128;
+constexpr int kSlots = 5;                                  // two CTAs an SM
+// Tiles whose copies are on their way unannounced. A tile of q is free once its up to two tiles of keys are multiplied, so when
+// its slot is asked for again (kSlots tiles later) those two have to have been announced.
+constexpr int kAhead = kSlots - 3;
+constexpr int kMaxCluster = 8;
+
+constexpr int kOffRing = 0;
+constexpr int kOffTurn = kSlots * kTileBytes;              // per softmax warp 32 columns x 33
+constexpr int kOffJoin = kOffTurn + kSoftWarps * 32 * 33 * 4;      // per softmax warp 32 columns: parts of a token's sum
+constexpr int kOffMax = kOffJoin + kSoftWarps * 32 * 4;    // per row: maximum and sum, read by the cluster
+constexpr int kOffSeen = kOffMax + kRows * 8;              // per token: blocks that it sees
+constexpr int kOffBars = kOffSeen + kRows * 4;
+constexpr int kNumBars = 2 * kSlots + 3;
+constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
+constexpr int kSmem = kOffMisc + 16;
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct ScoreArgs {
     Batch b;
@@ -19,79 +53,440 @@ struct ScoreArgs {
     const __nv_bfloat16* keys;
     float* scores;
     int H, d_qk, num_keys;
+    int tile_tokens;                                       // tokens a tile
+    int least;                                             // columns that a CTA takes at least
+    int cluster;
     float scale_log2;
 };
 
-// A CTA takes a token, a warp every eighth block: products first for the heads' maxima and sums, then again for the scores.
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16: fp32 D, BF16 A and B, both K-major, M = 128, N.
+__device__ __forceinline__ uint32_t idesc(uint32_t n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((kRows >> 4) << 24);
+}
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)) : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+// 32 lanes x 32 bits, 32 columns: thread t gets lane t, columns c .. c + 31.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    tc_wait_ld(r);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+           "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+           "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16 bytes to shared memory, zeros where there is nothing to copy.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 peer_float2(uint32_t saddr, int rank) {
+    uint32_t at;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+// One thread of the warp; ptxas knows that it is one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// A bounded wait that also ends as soon as another role has given up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag != 0) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
 block_scores_kernel(const ScoreArgs a) {
-    extern __shared__ __align__(16) __nv_bfloat16 sq[];    // [H][d_qk]
-    __shared__ float m_s[kWarps][128], l_s[kWarps][128], off_s[128];
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float* const turn = reinterpret_cast<float*>(smem + kOffTurn);
+    float* const join = reinterpret_cast<float*>(smem + kOffJoin);
+    float2* const max_s = reinterpret_cast<float2*>(smem + kOffMax);
+    int* const seen_s = reinterpret_cast<int*>(smem + kOffSeen);
+    uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kOffBars);        // [kSlots] a tile copied
+    uint64_t* const empty = full + kSlots;                                      // [kSlots] its products are done
+    uint64_t* const dfull = empty + kSlots;                                     // a round's products are done
+    uint64_t* const dfree = dfull + 1;                                          // and have been read
+    uint64_t* const fin = dfree + 1;                                            // all products are done
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = blockIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    if (t == 0) check_lengths(a.b);
-    const int s = sequence_at(a.b, t, lane);
-    if (s < 0) return;
-    const Sequence q = sequence_of(a.b, s);
-    const int pos = position_of(a.b, q, t - q.start);
-    const int n = pos < 0 ? 0 : pos / a.b.page_size;
-    for (int i = threadIdx.x; i < a.H * a.d_qk; i += kThreads)
-        sq[i] = a.q[static_cast<int64_t>(t) * a.H * a.d_qk + i];
-    for (int i = threadIdx.x; i < kWarps * 128; i += kThreads) {
-        m_s[i / 128][i % 128] = -INFINITY;
-        l_s[i / 128][i % 128] = 0.0f;
+    if (blockIdx.x == 0) check_lengths(a.b);
+    const int rank = a.cluster > 1 ? static_cast<int>(blockIdx.x) % a.cluster : 0;
+    const int2 u = find_unit<kThreads>(a.b.n_seq, static_cast<int>(blockIdx.x) / a.cluster, [&](int s) {
+        return (sequence_of(a.b, s).n + a.tile_tokens - 1) / a.tile_tokens;
+    });
+    if (u.x < 0) return;                                   // (all CTAs of a cluster have the same tile)
+    const Sequence q = sequence_of(a.b, u.x);
+    const int first = u.y * a.tile_tokens, n_tokens = min(a.tile_tokens, q.n - first);
+    const int last = position_of(a.b, q, first + n_tokens - 1);
+    const int blocks = last < 0 ? 0 : last / a.b.page_size;            // the tile's columns
+    if (blocks == 0) return;
+    // This CTA's: [c0, c0 + cols)
+    const int share = ((blocks + a.cluster - 1) / a.cluster + 15) & ~15;
+    const int per = max(a.least, share), c0 = static_cast<int>(min(static_cast<int64_t>(blocks), static_cast<int64_t>(rank) * per));
+    const int cols = min(per, blocks - c0);
+    const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
+    const int n_dims = a.d_qk / 64;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&full[i], kLoadWarps);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(dfull, 1);
+        mbar_init(dfree, kSoftWarps);
+        mbar_init(fin, 1);
+        *abort_flag = (smem_u32(smem) & 1023u) != 0u;      // (the operands' layout would be off: no result)
+        fence_mbar_init();
     }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tmem_slot)), "r"(kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
     __syncthreads();
-    const int32_t* bt = a.b.block_table + static_cast<int64_t>(s) * a.b.max_pages;
-    float* row = a.scores + static_cast<int64_t>(t) * a.b.max_pages;
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int blk = warp; blk < n; blk += kWarps) {
-            const int phys = __ldg(bt + blk);
-            if (phys < 0 || phys >= a.num_keys) {
-                if (lane == 0 && pass == 1) {
-                    row[blk] = -INFINITY;
-                    if (phys >= 0) atomicOr(a.b.err, MLA_ERR_PAGE_RANGE);
-                }
-                continue;
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = *abort_flag == 0;
+
+    // Row r of the tile: lane r % 32 of warp r / 32. Tokens of at most 32 heads stand side by side in a warp.
+    const int heads_warps = a.H <= 32 ? 1 : a.H <= 64 ? 2 : 4;         // warps of a token
+    const int per_warp = a.H <= 32 ? 32 / a.H : 1;                     // tokens of a warp
+    auto row_of = [&](int r, int& token, int& head) {                  // false: an empty lane
+        const int w = r >> 5, l = r & 31;
+        if (heads_warps == 1) {
+            token = w * per_warp + l / a.H;
+            head = l % a.H;
+            return l < per_warp * a.H && token < n_tokens;
+        }
+        token = w / heads_warps;
+        head = (w % heads_warps) * 32 + l;
+        return head < a.H && token < n_tokens;
+    };
+
+    if (warp >= kSoftWarps && warp < kMmaWarp) {
+        // ---- copies: thread = 16-byte unit x, rows y + 16 i of each tile ----
+        const int id = threadIdx.x - 32 * kSoftWarps, x = id & 7, y = id >> 3;
+        int32_t q_row[8];                                  // rows of q, -1: none
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int token, head;
+            q_row[i] = row_of(y + 16 * i, token, head) ? (q.start + first + token) * a.H + head : -1;
+        }
+        const int32_t* bt = a.b.block_table + static_cast<int64_t>(u.x) * a.b.max_pages + c0;
+        const uint32_t ring = smem_u32(smem) + kOffRing + 128 * y + ((x ^ (y & 7)) << 4);      // (16 i leaves y & 7)
+        int issued = 0, told = 0;                          // tiles whose copies are on their way; that have been announced
+        auto announce = [&]() {                            // the oldest one has landed
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[told % kSlots]);
+            ++told;
+        };
+        auto tile = [&](const __nv_bfloat16* base, const int32_t (&row)[8], int dim, int rows) {
+            const int slot = issued % kSlots;
+            if (issued >= kSlots) ok = ok && warp_wait(&empty[slot], static_cast<uint32_t>((issued / kSlots - 1) & 1), abort_flag);
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (y + 16 * i < rows)
+                        copy16(ring + slot * kTileBytes + 2048 * i, base + static_cast<int64_t>(max(row[i], 0)) * a.d_qk + dim + 8 * x,
+                               row[i] >= 0);
             }
-            float k[18];
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++issued;
+            if (issued - told > kAhead) {
+                copies_wait<kAhead>();
+                announce();
+            }
+        };
+        for (int pass = 0; pass < passes; ++pass) {
+            for (int r = 0; r < rounds && ok; ++r) {
+                const int n = min(kCols, cols - r * kCols);
+                int32_t key[2][8];
+                uint32_t odd = 0u;
 #pragma unroll
-            for (int i = 0; i < 18; ++i)
-                k[i] = 32 * i + lane < a.d_qk ? __bfloat162float(a.keys[static_cast<int64_t>(phys) * a.d_qk + 32 * i + lane]) : 0.0f;
-            float sum = 0.0f;
-            for (int h = 0; h < a.H; ++h) {
-                float x = 0.0f;
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 18; ++i)
-                    if (32 * i + lane < a.d_qk) x = fmaf(k[i], __bfloat162float(sq[h * a.d_qk + 32 * i + lane]), x);
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = kTileKeys * t + y + 16 * i;
+                        const int32_t page = c < n ? __ldg(bt + r * kCols + c) : -1;
+                        if (page >= a.num_keys) odd = 1u;
+                        key[t][i] = page < a.num_keys ? page : -1;
+                    }
+                if (odd != 0u) atomicOr(a.b.err, MLA_ERR_PAGE_RANGE);
+#pragma unroll 1
+                for (int k = 0; k < n_dims; ++k) {
+                    tile(a.q, q_row, 64 * k, kRows);
+                    tile(a.keys, key[0], 64 * k, min(kTileKeys, (n + 15) & ~15));
+                    if (n > kTileKeys) tile(a.keys, key[1], 64 * k, (n - kTileKeys + 15) & ~15);
+                }
+            }
+            copies_wait<0>();
+            while (told < issued) announce();
+            if (pass == 0 && a.cluster > 1) cluster_sync();
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- products, one elected thread ----
+        for (int pass = 0; pass < passes; ++pass) {
+            if (elect_one()) {
+                for (int r = 0; r < rounds && ok; ++r) {
+                    const int n = min(kCols, cols - r * kCols), tiles = n > kTileKeys ? 2 : 1;
+                    const int round = pass * rounds + r;
+                    if (round > 0) ok = wait_or_abort(dfree, static_cast<uint32_t>((round - 1) & 1), abort_flag);
+                    // ring tiles before this round's: those of whole rounds, all of which have two tiles of keys
+                    int at = (pass * ((rounds - 1) * 3 + (cols - (rounds - 1) * kCols > kTileKeys ? 3 : 2)) + r * 3) * n_dims;
+                    tc_after();
+                    for (int k = 0; k < n_dims && ok; ++k) {
+                        const int qs = at % kSlots;
+                        ok = wait_or_abort(&full[qs], static_cast<uint32_t>((at / kSlots) & 1), abort_flag);
+                        ++at;
+                        const uint64_t dq = sw128_desc(smem_u32(smem) + kOffRing + qs * kTileBytes);
+                        for (int t = 0; t < tiles && ok; ++t) {
+                            const int ks = at % kSlots;
+                            ok = wait_or_abort(&full[ks], static_cast<uint32_t>((at / kSlots) & 1), abort_flag);
+                            ++at;
+                            if (!ok) break;
+                            tc_after();
+                            const uint64_t dk = sw128_desc(smem_u32(smem) + kOffRing + ks * kTileBytes);
+                            const uint32_t id = idesc((min(kTileKeys, n - kTileKeys * t) + 15) & ~15);
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                x *= a.scale_log2;
-                if (pass == 0) {
-                    if (lane == 0) {
-                        const float m = m_s[warp][h], now = fmaxf(m, x);
-                        l_s[warp][h] = l_s[warp][h] * exp2f(m - now) + exp2f(x - now);
-                        m_s[warp][h] = now;
+                            for (int s = 0; s < 4; ++s)
+                                umma(tmem + kTileKeys * t, dq + static_cast<uint64_t>(2 * s), dk + static_cast<uint64_t>(2 * s), id,
+                                     k > 0 || s > 0);
+                            umma_commit(&empty[ks]);
+                        }
+                        if (ok) umma_commit(&empty[qs]);
+                    }
+                    if (ok) umma_commit(dfull);
+                }
+                if (pass + 1 == passes) {                  // before tensor memory is freed
+                    umma_commit(fin);
+                    (void)mbar_wait_bounded(fin, 0);
+                }
+            }
+            __syncwarp();
+            if (pass == 0 && a.cluster > 1) cluster_sync();
+        }
+    } else {
+        // ---- softmax: thread = row ----
+        const int row = threadIdx.x;
+        int token, head;
+        const bool lives = row_of(row, token, head);
+        const int pos = lives ? position_of(a.b, q, first + token) : -1;
+        const int seen = (pos < 0 ? 0 : pos / a.b.page_size) - c0;         // columns of this CTA that the row sees
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const int32_t* bt = a.b.block_table + static_cast<int64_t>(u.x) * a.b.max_pages + c0;
+        if (lives && head == 0) seen_s[token] = seen + c0;                 // (read by its own warp alone)
+        float m = -INFINITY, l = 0.0f;
+        // Which of a round's columns have a key: lane j gets the bits of columns 32 j ..
+        auto keyed_columns = [&](int r) {
+            int32_t page[kCols / 32];
+#pragma unroll
+            for (int j = 0; j < kCols / 32; ++j) {
+                const int c = r * kCols + 32 * j + lane;
+                page[j] = c < cols ? __ldg(bt + c) : -1;
+            }
+            uint32_t mine = 0u;
+#pragma unroll
+            for (int j = 0; j < kCols / 32; ++j) {
+                const uint32_t word = __ballot_sync(0xffffffffu, page[j] >= 0 && page[j] < a.num_keys);
+                if (lane == j) mine = word;
+            }
+            return mine;
+        };
+        uint32_t keyed = 0u;
+        // 32 scores of the row in log2 units, -inf where it sees no block.
+        auto load = [&](int r, int j, float (&x)[32]) {
+            uint32_t v[32];
+            tmem_ld32(lanes + 32 * j, v);
+            const int left = seen - (r * kCols + 32 * j);
+            const uint32_t word = __shfl_sync(0xffffffffu, keyed, j);
+            const uint32_t sees = left >= 32 ? word : left <= 0 ? 0u : word & ((1u << left) - 1u);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * a.scale_log2;
+            if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] = ((sees >> c) & 1u) != 0u ? x[c] : -INFINITY;
+            }
+        };
+        for (int r = 0; r < rounds; ++r) {
+            keyed = keyed_columns(r);
+            ok = warp_wait(dfull, static_cast<uint32_t>(r & 1), abort_flag);
+            ok = !bar_sync_or(1, 32 * kSoftWarps, !ok);        // one answer for the four warps
+            if (!ok) break;
+            tc_after();
+            const int chunks = (min(kCols, cols - r * kCols) + 31) / 32;
+            float top = m;
+            for (int j = 0; j < chunks; ++j) {
+                float x[32];
+                load(r, j, x);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) top = fmaxf(top, x[c]);
+            }
+            const float off = top == -INFINITY ? 0.0f : top;
+            l *= ex2_approx(m - off);                      // (nothing so far: l is 0)
+            m = top;
+            for (int j = 0; j < chunks; ++j) {
+                float x[32];
+                load(r, j, x);
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    x[c] = ex2_approx(x[c] - off);
+                    sum[c & 3] += x[c];
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (rounds == 1) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(x[c]);
+                    tmem_st32(lanes + 32 * j, v);
+                }
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dfree);
+        }
+        float all_m = m, all_l = l;
+        if (a.cluster > 1) {
+            max_s[row] = make_float2(m, l);
+            cluster_sync();
+            for (int k = 0; k < a.cluster; ++k) all_m = fmaxf(all_m, peer_float2(smem_u32(&max_s[row]), k).x);
+            all_l = 0.0f;
+            for (int k = 0; k < a.cluster; ++k) {
+                const float2 v = peer_float2(smem_u32(&max_s[row]), k);
+                all_l += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - all_m);       // (v.y is 0 there, or NaN)
+            }
+        }
+        // p = exp2(x - off) x f; with one round exp2(x - m) is in tensor memory
+        const float off = all_m == -INFINITY ? 0.0f : all_m;
+        const float f = (rounds == 1 ? (m == -INFINITY ? 0.0f : ex2_approx(m - off)) : 1.0f) / (all_l == 0.0f ? 1.0f : all_l);
+        float* const mine = turn + warp * 32 * 33;
+        for (int r = 0; r < rounds && ok; ++r) {
+            if (rounds > 1) {
+                keyed = keyed_columns(r);
+                ok = warp_wait(dfull, static_cast<uint32_t>((rounds + r) & 1), abort_flag);
+                ok = !bar_sync_or(1, 32 * kSoftWarps, !ok);
+                if (!ok) break;
+                tc_after();
+            }
+            const int chunks = (min(kCols, cols - r * kCols) + 31) / 32;
+            for (int j = 0; j < chunks; ++j) {
+                if (rounds == 1) {
+                    uint32_t v[32];
+                    tmem_ld32(lanes + 32 * j, v);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) mine[33 * c + lane] = lives ? __uint_as_float(v[c]) * f : 0.0f;
+                } else {
+                    float x[32];
+                    load(r, j, x);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) mine[33 * c + lane] = lives ? ex2_approx(x[c] - off) * f : 0.0f;
+                }
+                __syncwarp();
+                // lane = column: the sums over each token's heads
+                const int c = c0 + r * kCols + 32 * j + lane;
+                const bool has = ((__shfl_sync(0xffffffffu, keyed, j) >> lane) & 1u) != 0u;
+                if (heads_warps == 1) {
+                    for (int k = 0; k < per_warp; ++k) {
+                        const int tok = warp * per_warp + k;
+                        if (tok >= n_tokens) break;
+                        float sum = 0.0f;
+#pragma unroll 4
+                        for (int h = 0; h < a.H; ++h) sum += mine[33 * lane + k * a.H + h];
+                        if (c < min(seen_s[tok], c0 + cols))
+                            a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
                     }
                 } else {
-                    sum += exp2f(x - off_s[h]);
+                    float sum = 0.0f;
+#pragma unroll 8
+                    for (int h = 0; h < 32; ++h) sum += mine[33 * lane + h];
+                    join[32 * warp + lane] = sum;
+                    bar_sync_or(1, 32 * kSoftWarps, false);
+                    const int tok = warp / heads_warps;
+                    if (warp % heads_warps == 0 && tok < n_tokens) {
+                        for (int w = 1; w < heads_warps; ++w) sum += join[32 * (warp + w) + lane];
+                        if (c < min(seen_s[tok], c0 + cols))
+                            a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
+                    }
+                    bar_sync_or(1, 32 * kSoftWarps, false);
                 }
+                __syncwarp();
             }
-            if (pass == 1 && lane == 0) row[blk] = sum;
-        }
-        __syncthreads();
-        if (pass == 0) {
-            for (int h = threadIdx.x; h < a.H; h += kThreads) {
-                float m = -INFINITY, l = 0.0f;
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_s[w][h]);
-                for (int w = 0; w < kWarps; ++w) l += m_s[w][h] == -INFINITY ? 0.0f : l_s[w][h] * exp2f(m_s[w][h] - m);
-                off_s[h] = m + log2f(l);
+            if (rounds > 1) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dfree);
             }
-            __syncthreads();
         }
     }
+    tc_before();
+    __syncthreads();
+    if (*abort_flag != 0 && threadIdx.x == 0) atomicOr(a.b.err, MLA_ERR_PIPELINE_TIMEOUT);
+    if (warp == kMmaWarp) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kCols) : "memory");
+    }
+    if (a.cluster > 1) cluster_sync();                     // (the others have read this CTA's maxima)
 }
 
 bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -111,10 +506,34 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
         off(keys_bf16, 16) || off(scores, 4))
         return MLA_EINVAL;
     b.err = mla_host::device_error_word();
-    if (b.err == nullptr) return MLA_ECUDA;
-    const ScoreArgs a = {b, static_cast<const __nv_bfloat16*>(q_bf16), static_cast<const __nv_bfloat16*>(keys_bf16), scores,
-                         H, d_qk, num_keys, sm_scale * kLog2e};
-    constexpr int kMostSmem = 128 * (kLatent + kRope) * 2;
-    if (!mla_host::max_dynamic_smem(reinterpret_cast<const void*>(block_scores_kernel), kMostSmem)) return MLA_ECUDA;
-    return mla_host::launch_pdl(block_scores_kernel, T, kThreads, H * d_qk * 2, stream, a) ? MLA_OK : MLA_ECUDA;
+    const int sms = mla_host::sm_count();
+    if (b.err == nullptr || sms <= 0 || !mla_host::max_dynamic_smem(reinterpret_cast<const void*>(block_scores_kernel), kSmem))
+        return MLA_ECUDA;
+    ScoreArgs a = {b, static_cast<const __nv_bfloat16*>(q_bf16), static_cast<const __nv_bfloat16*>(keys_bf16), scores,
+                   H, d_qk, num_keys, 1, kCols, 1, sm_scale * kLog2e};
+    a.tile_tokens = H <= 32 ? 4 * (32 / H) : H <= 64 ? 2 : 1;
+    const int64_t tiles = static_cast<int64_t>(T) / a.tile_tokens + (n_seq < T ? n_seq : T);
+    // CTAs per tile: as many as hold all of the table's blocks at once, and where that leaves SMs without work, as many
+    // as have kLeast columns each.
+    constexpr int kLeast = 64;
+    while (a.cluster < kMaxCluster && a.cluster * kCols < max_pages) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && tiles * a.cluster < sms && a.cluster * kLeast < max_pages) a.cluster *= 2;
+    if (tiles * a.cluster < 2 * sms) a.least = kLeast;
+    if (tiles * a.cluster > INT_MAX) a.cluster = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, block_scores_kernel, a) == cudaSuccess && cudaGetLastError() == cudaSuccess ? MLA_OK
+                                                                                                              : MLA_ECUDA;
 }
