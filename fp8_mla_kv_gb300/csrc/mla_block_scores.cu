@@ -10,12 +10,16 @@
 // A warp's 32 rows are whole tokens where a token has at most 32 heads (lanes left over stay empty), so that the sum
 // over heads is one warp's; two or four warps share a token with more.
 //
-// Roles: warps 0-3 softmax (TMEM lanes 32 w ..), 4-7 copy (16 bytes a thread and time, cp.async, since keys
-// lie wherever the block table says), 8 issues the products. q and keys come in tiles of 128 rows x 64 dims
-// (128 bytes a row, 128-byte swizzle) through a ring; for each 64 dims one of q and up to two of keys.
+// Roles: warps 0-3 softmax (TMEM lanes 32 w ..), 4-7 copy keys, 8 q, 9 issues the products. q comes by TMA in boxes of
+// 32 rows x 64 dims, one for each softmax warp; keys, which lie wherever the block table says, by 16 bytes a thread and
+// time (cp.async): TMA's gather of four rows took 41,000 cycles for what boxes take 15,000. Both in 128-byte-swizzled
+// tiles of 128 rows through a ring each, for each 64 dims one of q and up to two of keys.
 // TIME_SCORES
 #include <climits>
 #include <cmath>
+#include <mutex>
+
+#include <cuda.h>
 
 #include "mla_seq.cuh"
 
@@ -24,32 +28,31 @@ namespace {
 using namespace mla;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSoftWarps = 4, kLoadWarps = 4, kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kSoftWarps = 4, kLoadWarps = 4, kLoadWarp = kSoftWarps, kQWarp = kLoadWarp + kLoadWarps, kMmaWarp = kQWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kRows = 128;                                 // M
 constexpr int kCols = 256;                                 // columns a round: tensor memory of a CTA
 constexpr int kTileKeys = 128;                             // keys per ring tile
 constexpr int kTileBytes = 128 * 128;
-constexpr int kSlots = 5;                                  // two CTAs an SM
-// Tiles whose copies are on their way unannounced. A tile of q is free once its up to two tiles of keys are multiplied, so when
-// its slot is asked for again (kSlots tiles later) those two have to have been announced.
-constexpr int kAhead = kSlots - 3;
+constexpr int kSlots = 3, kQSlots = 2;                      // two CTAs an SM
 constexpr int kMaxCluster = 8;
 
 constexpr int kOffRing = 0;
-constexpr int kOffTurn = kSlots * kTileBytes;              // per softmax warp 32 columns x 33
-constexpr int kOffJoin = kOffTurn + kSoftWarps * 32 * 33 * 4;      // per softmax warp 32 columns: parts of a token's sum
+constexpr int kOffQ = kSlots * kTileBytes;
+constexpr int kOffTurn = kOffQ + kQSlots * kTileBytes;     // per softmax warp 32 columns x 36 (16-byte reads of a column meet no bank twice)
+constexpr int kTurn = 36;
+constexpr int kOffJoin = kOffTurn + kSoftWarps * 32 * kTurn * 4;      // per softmax warp 32 columns: parts of a token's sum
 constexpr int kOffMax = kOffJoin + kSoftWarps * 32 * 4;    // per row: maximum and sum, read by the cluster
 constexpr int kOffSeen = kOffMax + kRows * 8;              // per token: blocks that it sees
-constexpr int kOffBars = kOffSeen + kRows * 4;
-constexpr int kNumBars = 2 * kSlots + 3;
+constexpr int kOffOff = kOffSeen + kRows * 4;              // per 32 columns and row: the maximum that its exponentials go by
+constexpr int kOffBars = kOffOff + (kCols / 32) * kRows * 4;
+constexpr int kNumBars = 2 * kSlots + 2 * kQSlots + 3;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
 constexpr int kSmem = kOffMisc + 16;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct ScoreArgs {
     Batch b;
-    const __nv_bfloat16* q;
     const __nv_bfloat16* keys;
     float* scores;
     int H, d_qk, num_keys;
@@ -109,12 +112,20 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+// Dims x .. x + 63 of rows y .. y + 31.
+__device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
 // 16 bytes to shared memory, zeros where there is nothing to copy.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-template <int kLeft>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
+// Arrives at the barrier when all of this thread's copies so far have landed. (The order to the products, which read
+// through another proxy, is made by the thread that waits: a fence here would wait for the copies behind, too.)
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -150,15 +161,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 __global__ void __launch_bounds__(kThreads, 2)
-block_scores_kernel(const ScoreArgs a) {
+block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     float* const turn = reinterpret_cast<float*>(smem + kOffTurn);
     float* const join = reinterpret_cast<float*>(smem + kOffJoin);
     float2* const max_s = reinterpret_cast<float2*>(smem + kOffMax);
     int* const seen_s = reinterpret_cast<int*>(smem + kOffSeen);
+    float* const off_s = reinterpret_cast<float*>(smem + kOffOff);              // [kCols / 32][kRows]
     uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kOffBars);        // [kSlots] a tile copied
     uint64_t* const empty = full + kSlots;                                      // [kSlots] its products are done
-    uint64_t* const dfull = empty + kSlots;                                     // a round's products are done
+    uint64_t* const qfull = empty + kSlots;                                     // [kQSlots] the same for q
+    uint64_t* const qempty = qfull + kQSlots;
+    uint64_t* const dfull = qempty + kQSlots;                                   // a round's products are done
     uint64_t* const dfree = dfull + 1;                                          // and have been read
     uint64_t* const fin = dfree + 1;                                            // all products are done
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -182,13 +196,19 @@ block_scores_kernel(const ScoreArgs a) {
     const int share = ((blocks + a.cluster - 1) / a.cluster + 15) & ~15;
     const int per = max(a.least, share), c0 = static_cast<int>(min(static_cast<int64_t>(blocks), static_cast<int64_t>(rank) * per));
     const int cols = min(per, blocks - c0);
+    if (cols == 0) return;                                 // (its peers know: they neither wait for it nor read its maxima)
+    const int peers = (blocks + per - 1) / per;            // CTAs of the cluster with columns
     const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
     const int n_dims = a.d_qk / 64;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&full[i], kLoadWarps);
+            mbar_init(&full[i], 32 * kLoadWarps);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kQSlots; ++i) {
+            mbar_init(&qfull[i], 1);
+            mbar_init(&qempty[i], 1);
         }
         mbar_init(dfull, 1);
         mbar_init(dfree, kSoftWarps);
@@ -222,88 +242,96 @@ block_scores_kernel(const ScoreArgs a) {
         return head < a.H && token < n_tokens;
     };
 
-    if (warp >= kSoftWarps && warp < kMmaWarp) {
-        // ---- copies: thread = 16-byte unit x, rows y + 16 i of each tile ----
-        const int id = threadIdx.x - 32 * kSoftWarps, x = id & 7, y = id >> 3;
-        int32_t q_row[8];                                  // rows of q, -1: none
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            int token, head;
-            q_row[i] = row_of(y + 16 * i, token, head) ? (q.start + first + token) * a.H + head : -1;
-        }
+    if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
+        // ---- keys: thread = 16-byte unit x of 64 dims, rows y + 16 i of each tile ----
+        const int id = threadIdx.x - 32 * kLoadWarp, x = id & 7, y = id >> 3;
         const int32_t* bt = a.b.block_table + static_cast<int64_t>(u.x) * a.b.max_pages + c0;
         const uint32_t ring = smem_u32(smem) + kOffRing + 128 * y + ((x ^ (y & 7)) << 4);      // (16 i leaves y & 7)
-        int issued = 0, told = 0;                          // tiles whose copies are on their way; that have been announced
-        auto announce = [&]() {                            // the oldest one has landed
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[told % kSlots]);
-            ++told;
-        };
-        auto tile = [&](const __nv_bfloat16* base, const int32_t (&row)[8], int dim, int rows) {
-            const int slot = issued % kSlots;
-            if (issued >= kSlots) ok = ok && warp_wait(&empty[slot], static_cast<uint32_t>((issued / kSlots - 1) & 1), abort_flag);
-            if (ok) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (y + 16 * i < rows)
-                        copy16(ring + slot * kTileBytes + 2048 * i, base + static_cast<int64_t>(max(row[i], 0)) * a.d_qk + dim + 8 * x,
-                               row[i] >= 0);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ++issued;
-            if (issued - told > kAhead) {
-                copies_wait<kAhead>();
-                announce();
-            }
-        };
+        int issued = 0;                                    // tiles
         for (int pass = 0; pass < passes; ++pass) {
             for (int r = 0; r < rounds && ok; ++r) {
                 const int n = min(kCols, cols - r * kCols);
-                int32_t key[2][8];
-                uint32_t odd = 0u;
+                const __nv_bfloat16* src[2][8];
+                uint32_t there = 0u;
+                bool odd = false;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int c = kTileKeys * t + y + 16 * i;
                         const int32_t page = c < n ? __ldg(bt + r * kCols + c) : -1;
-                        if (page >= a.num_keys) odd = 1u;
-                        key[t][i] = page < a.num_keys ? page : -1;
+                        odd = odd || page >= a.num_keys;
+                        const bool has = page >= 0 && page < a.num_keys;
+                        there |= (has ? 1u : 0u) << (8 * t + i);
+                        src[t][i] = a.keys + static_cast<int64_t>(has ? page : 0) * a.d_qk + 8 * x;
                     }
-                if (odd != 0u) atomicOr(a.b.err, MLA_ERR_PAGE_RANGE);
+                if (odd) atomicOr(a.b.err, MLA_ERR_PAGE_RANGE);
 #pragma unroll 1
-                for (int k = 0; k < n_dims; ++k) {
-                    tile(a.q, q_row, 64 * k, kRows);
-                    tile(a.keys, key[0], 64 * k, min(kTileKeys, (n + 15) & ~15));
-                    if (n > kTileKeys) tile(a.keys, key[1], 64 * k, (n - kTileKeys + 15) & ~15);
+                for (int k = 0; k < n_dims && ok; ++k) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int rows = (n - kTileKeys * t + 15) & ~15;       // as many as the product takes
+                        if (rows <= 0) break;
+                        const int slot = issued % kSlots;
+                        if (issued >= kSlots) ok = ok && warp_wait(&empty[slot], static_cast<uint32_t>((issued / kSlots - 1) & 1), abort_flag);
+                        if (ok) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (y + 16 * i < rows)
+                                    copy16(ring + slot * kTileBytes + 2048 * i, src[t][i] + 64 * k, ((there >> (8 * t + i)) & 1u) != 0u);
+                            copies_arrive(&full[slot]);
+                        }
+                        ++issued;
+                    }
                 }
             }
-            copies_wait<0>();
-            while (told < issued) announce();
             if (pass == 0 && a.cluster > 1) cluster_sync();
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");   // (a call that failed may have some on their way)
+    } else if (warp == kQWarp) {
+        // ---- q: lane l < 4 the box of softmax warp l ----
+        int q_row = 0;
+        if (lane < kSoftWarps)
+            q_row = heads_warps == 1 ? (q.start + first + lane * per_warp) * a.H
+                                     : (q.start + first + lane / heads_warps) * a.H + 32 * (lane % heads_warps);
+        q_row = min(q_row, a.b.T * a.H - 1);               // (a box of none of the tile's tokens)
+        int issued = 0;
+        for (int pass = 0; pass < passes; ++pass) {
+            for (int i = 0; i < rounds * n_dims && ok; ++i, ++issued) {
+                const int slot = issued % kQSlots;
+                if (issued >= kQSlots) ok = warp_wait(&qempty[slot], static_cast<uint32_t>((issued / kQSlots - 1) & 1), abort_flag);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&qfull[slot], kTileBytes);
+                __syncwarp();
+                if (lane < kSoftWarps)
+                    copy_box(smem + kOffQ + slot * kTileBytes + lane * (kTileBytes / kSoftWarps), &q_map, 64 * (i % n_dims), q_row,
+                             &qfull[slot]);
+            }
+            if (pass == 0 && a.cluster > 1) cluster_sync();
+        }
+        // Copies in flight land before the CTA ends.
+        if (!ok)
+            for (int i = max(0, issued - kQSlots); i < issued; ++i)
+                (void)mbar_wait_bounded(&qfull[i % kQSlots], static_cast<uint32_t>((i / kQSlots) & 1));
     } else if (warp == kMmaWarp) {
         // ---- products, one elected thread ----
+        int at = 0, q_at = 0;                              // tiles so far (the elected thread is the same each time)
         for (int pass = 0; pass < passes; ++pass) {
             if (elect_one()) {
                 for (int r = 0; r < rounds && ok; ++r) {
                     const int n = min(kCols, cols - r * kCols), tiles = n > kTileKeys ? 2 : 1;
                     const int round = pass * rounds + r;
                     if (round > 0) ok = wait_or_abort(dfree, static_cast<uint32_t>((round - 1) & 1), abort_flag);
-                    // ring tiles before this round's: those of whole rounds, all of which have two tiles of keys
-                    int at = (pass * ((rounds - 1) * 3 + (cols - (rounds - 1) * kCols > kTileKeys ? 3 : 2)) + r * 3) * n_dims;
                     tc_after();
-                    for (int k = 0; k < n_dims && ok; ++k) {
-                        const int qs = at % kSlots;
-                        ok = wait_or_abort(&full[qs], static_cast<uint32_t>((at / kSlots) & 1), abort_flag);
-                        ++at;
-                        const uint64_t dq = sw128_desc(smem_u32(smem) + kOffRing + qs * kTileBytes);
-                        for (int t = 0; t < tiles && ok; ++t) {
+                    for (int k = 0; k < n_dims && ok; ++k, ++q_at) {
+                        const int qs = q_at % kQSlots;
+                        ok = wait_or_abort(&qfull[qs], static_cast<uint32_t>((q_at / kQSlots) & 1), abort_flag);
+                        const uint64_t dq = sw128_desc(smem_u32(smem) + kOffQ + qs * kTileBytes);
+                        for (int t = 0; t < tiles && ok; ++t, ++at) {
                             const int ks = at % kSlots;
                             ok = wait_or_abort(&full[ks], static_cast<uint32_t>((at / kSlots) & 1), abort_flag);
-                            ++at;
                             if (!ok) break;
+                            fence_proxy_async_smem();
                             tc_after();
                             const uint64_t dk = sw128_desc(smem_u32(smem) + kOffRing + ks * kTileBytes);
                             const uint32_t id = idesc((min(kTileKeys, n - kTileKeys * t) + 15) & ~15);
@@ -313,7 +341,7 @@ block_scores_kernel(const ScoreArgs a) {
                                      k > 0 || s > 0);
                             umma_commit(&empty[ks]);
                         }
-                        if (ok) umma_commit(&empty[qs]);
+                        if (ok) umma_commit(&qempty[qs]);
                     }
                     if (ok) umma_commit(dfull);
                 }
@@ -374,31 +402,28 @@ block_scores_kernel(const ScoreArgs a) {
             if (!ok) break;
             tc_after();
             const int chunks = (min(kCols, cols - r * kCols) + 31) / 32;
-            float top = m;
             for (int j = 0; j < chunks; ++j) {
                 float x[32];
                 load(r, j, x);
+                float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; ++c) top = fmaxf(top, x[c]);
-            }
-            const float off = top == -INFINITY ? 0.0f : top;
-            l *= ex2_approx(m - off);                      // (nothing so far: l is 0)
-            m = top;
-            for (int j = 0; j < chunks; ++j) {
-                float x[32];
-                load(r, j, x);
+                for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const float off = now == -INFINITY ? 0.0f : now;
+                l *= ex2_approx(m - off);                  // (nothing so far: l is 0)
+                m = now;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t v[32];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    x[c] = ex2_approx(x[c] - off);
-                    sum[c & 3] += x[c];
+                    const float p = ex2_approx(x[c] - off);
+                    sum[c & 3] += p;
+                    v[c] = __float_as_uint(p);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 if (rounds == 1) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(x[c]);
                     tmem_st32(lanes + 32 * j, v);
+                    off_s[j * kRows + row] = m;
                 }
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -410,17 +435,17 @@ block_scores_kernel(const ScoreArgs a) {
         if (a.cluster > 1) {
             max_s[row] = make_float2(m, l);
             cluster_sync();
-            for (int k = 0; k < a.cluster; ++k) all_m = fmaxf(all_m, peer_float2(smem_u32(&max_s[row]), k).x);
+            for (int k = 0; k < peers; ++k) all_m = fmaxf(all_m, peer_float2(smem_u32(&max_s[row]), k).x);
             all_l = 0.0f;
-            for (int k = 0; k < a.cluster; ++k) {
+            for (int k = 0; k < peers; ++k) {
                 const float2 v = peer_float2(smem_u32(&max_s[row]), k);
                 all_l += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - all_m);       // (v.y is 0 there, or NaN)
             }
         }
-        // p = exp2(x - off) x f; with one round exp2(x - m) is in tensor memory
+        // p = exp2(x - off) x f; with one round exp2(x - a maximum so far) is in tensor memory
         const float off = all_m == -INFINITY ? 0.0f : all_m;
-        const float f = (rounds == 1 ? (m == -INFINITY ? 0.0f : ex2_approx(m - off)) : 1.0f) / (all_l == 0.0f ? 1.0f : all_l);
-        float* const mine = turn + warp * 32 * 33;
+        const float f = 1.0f / (all_l == 0.0f ? 1.0f : all_l);
+        float* const mine = turn + warp * 32 * kTurn;
         for (int r = 0; r < rounds && ok; ++r) {
             if (rounds > 1) {
                 keyed = keyed_columns(r);
@@ -434,13 +459,14 @@ block_scores_kernel(const ScoreArgs a) {
                 if (rounds == 1) {
                     uint32_t v[32];
                     tmem_ld32(lanes + 32 * j, v);
+                    const float g = ex2_approx(off_s[j * kRows + row] - off) * f;      // (0 where nothing was seen so far)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) mine[33 * c + lane] = lives ? __uint_as_float(v[c]) * f : 0.0f;
+                    for (int c = 0; c < 32; ++c) mine[kTurn * c + lane] = lives ? __uint_as_float(v[c]) * g : 0.0f;
                 } else {
                     float x[32];
                     load(r, j, x);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) mine[33 * c + lane] = lives ? ex2_approx(x[c] - off) * f : 0.0f;
+                    for (int c = 0; c < 32; ++c) mine[kTurn * c + lane] = lives ? ex2_approx(x[c] - off) * f : 0.0f;
                 }
                 __syncwarp();
                 // lane = column: the sums over each token's heads
@@ -450,16 +476,28 @@ block_scores_kernel(const ScoreArgs a) {
                     for (int k = 0; k < per_warp; ++k) {
                         const int tok = warp * per_warp + k;
                         if (tok >= n_tokens) break;
-                        float sum = 0.0f;
+                        const float* col = mine + kTurn * lane + k * a.H;
+                        float4 part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (a.H % 4 == 0) {
 #pragma unroll 4
-                        for (int h = 0; h < a.H; ++h) sum += mine[33 * lane + k * a.H + h];
+                            for (int h = 0; h < a.H; h += 4) {
+                                const float4 v = *reinterpret_cast<const float4*>(col + h);
+                                part = make_float4(part.x + v.x, part.y + v.y, part.z + v.z, part.w + v.w);
+                            }
+                        } else {
+                            for (int h = 0; h < a.H; ++h) part.x += col[h];
+                        }
+                        const float sum = (part.x + part.y) + (part.z + part.w);
                         if (c < min(seen_s[tok], c0 + cols))
                             a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
                     }
                 } else {
                     float sum = 0.0f;
-#pragma unroll 8
-                    for (int h = 0; h < 32; ++h) sum += mine[33 * lane + h];
+#pragma unroll
+                    for (int h = 0; h < 32; h += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(mine + kTurn * lane + h);
+                        sum += (v.x + v.y) + (v.z + v.w);
+                    }
                     join[32 * warp + lane] = sum;
                     bar_sync_or(1, 32 * kSoftWarps, false);
                     const int tok = warp / heads_warps;
@@ -491,6 +529,36 @@ block_scores_kernel(const ScoreArgs a) {
 
 bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
+// TMA's maps are made by the driver, whose entry point is looked up once.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::once_flag once;
+    static EncodeTiled fn = nullptr;
+    std::call_once(once, []() {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(p);
+    });
+    return fn;
+}
+
+// BF16 [rows, dims], copied 64 dims x 32 rows at a time.
+bool make_map(CUtensorMap* map, const void* data, int64_t rows, int dims) {
+    const EncodeTiled fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(dims), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(dims) * 2};
+    const cuuint32_t box[2] = {64, 32}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(data), size, stride, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, const void* keys_bf16, int num_keys,
@@ -509,8 +577,7 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
     const int sms = mla_host::sm_count();
     if (b.err == nullptr || sms <= 0 || !mla_host::max_dynamic_smem(reinterpret_cast<const void*>(block_scores_kernel), kSmem))
         return MLA_ECUDA;
-    ScoreArgs a = {b, static_cast<const __nv_bfloat16*>(q_bf16), static_cast<const __nv_bfloat16*>(keys_bf16), scores,
-                   H, d_qk, num_keys, 1, kCols, 1, sm_scale * kLog2e};
+    ScoreArgs a = {b, static_cast<const __nv_bfloat16*>(keys_bf16), scores, H, d_qk, num_keys, 1, kCols, 1, sm_scale * kLog2e};
     a.tile_tokens = H <= 32 ? 4 * (32 / H) : H <= 64 ? 2 : 1;
     const int64_t tiles = static_cast<int64_t>(T) / a.tile_tokens + (n_seq < T ? n_seq : T);
     // CTAs per tile: as many as hold all of the table's blocks at once, and where that leaves SMs without work, as many
@@ -520,6 +587,8 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
     while (a.cluster < kMaxCluster && tiles * a.cluster < sms && a.cluster * kLeast < max_pages) a.cluster *= 2;
     if (tiles * a.cluster < 2 * sms) a.least = kLeast;
     if (tiles * a.cluster > INT_MAX) a.cluster = 1;
+    alignas(64) CUtensorMap q_map;
+    if (!make_map(&q_map, q_bf16, static_cast<int64_t>(T) * H, d_qk)) return MLA_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.cluster));
     cfg.blockDim = dim3(kThreads);
@@ -534,6 +603,6 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, block_scores_kernel, a) == cudaSuccess && cudaGetLastError() == cudaSuccess ? MLA_OK
+    return cudaLaunchKernelEx(&cfg, block_scores_kernel, q_map, a) == cudaSuccess && cudaGetLastError() == cudaSuccess ? MLA_OK
                                                                                                               : MLA_ECUDA;
 }
