@@ -10,11 +10,12 @@
 // A warp's 32 rows are whole tokens where a token has at most 32 heads (lanes left over stay empty), so that the sum
 // over heads is one warp's; two or four warps share a token with more.
 //
-// Roles: warps 0-3 softmax (TMEM lanes 32 w ..), 4-7 copy keys, 8 q, 9 issues the products. q comes by TMA in boxes of
-// 32 rows x 64 dims, one for each softmax warp; keys, which lie wherever the block table says, by 16 bytes a thread and
-// time (cp.async): TMA's gather of four rows took 41,000 cycles for what boxes take 15,000. Both in 128-byte-swizzled
-// tiles of 128 rows through a ring each, for each 64 dims one of q and up to two of keys.
+// Roles: warps 0-7 softmax (TMEM lanes 32 (w % 4) .., every other 16 columns), 8-11 copy keys, 12 q, 13 issues the
+// products. q comes by TMA in boxes of 32 rows x 64 dims, one for each lane quarter; keys, which lie wherever the block table
+// says, by 16 bytes a thread and time (cp.async): TMA's gather of four rows took 41,000 cycles for what boxes take 15,000.
+// Both in 128-byte-swizzled tiles of 128 rows through a ring each, for each 64 dims one of q and up to two of keys.
 // TIME_SCORES
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -28,7 +29,7 @@ namespace {
 using namespace mla;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSoftWarps = 4, kLoadWarps = 4, kLoadWarp = kSoftWarps, kQWarp = kLoadWarp + kLoadWarps, kMmaWarp = kQWarp + 1;
+constexpr int kSoftWarps = 8, kLoadWarps = 4, kLoadWarp = kSoftWarps, kQWarp = kLoadWarp + kLoadWarps, kMmaWarp = kQWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kRows = 128;                                 // M
 constexpr int kCols = 256;                                 // columns a round: tensor memory of a CTA
@@ -39,13 +40,14 @@ constexpr int kMaxCluster = 8;
 
 constexpr int kOffRing = 0;
 constexpr int kOffQ = kSlots * kTileBytes;
-constexpr int kOffTurn = kOffQ + kQSlots * kTileBytes;     // per softmax warp 32 columns x 36 (16-byte reads of a column meet no bank twice)
-constexpr int kTurn = 36;
-constexpr int kOffJoin = kOffTurn + kSoftWarps * 32 * kTurn * 4;      // per softmax warp 32 columns: parts of a token's sum
-constexpr int kOffMax = kOffJoin + kSoftWarps * 32 * 4;    // per row: maximum and sum, read by the cluster
-constexpr int kOffSeen = kOffMax + kRows * 8;              // per token: blocks that it sees
-constexpr int kOffOff = kOffSeen + kRows * 4;              // per 32 columns and row: the maximum that its exponentials go by
-constexpr int kOffBars = kOffOff + (kCols / 32) * kRows * 4;
+constexpr int kStep = 16;                                  // columns that a softmax warp takes at a time
+constexpr int kTurn = 36;                                  // (16-byte reads of a column then meet no bank twice)
+constexpr int kOffTurn = kOffQ + kQSlots * kTileBytes;     // per softmax warp kStep columns x 32 rows
+constexpr int kOffJoin = kOffTurn + kSoftWarps * kStep * kTurn * 4;    // per softmax warp and column: parts of a token's sum
+constexpr int kOffMax = kOffJoin + kSoftWarps * kStep * 4; // per half of the softmax warps and row: maximum and sum, read by the cluster
+constexpr int kOffSeen = kOffMax + 2 * kRows * 8;          // per token: blocks that it sees
+constexpr int kOffOff = kOffSeen + kRows * 4;              // per kStep columns and row: the maximum that its exponentials go by
+constexpr int kOffBars = kOffOff + (kCols / kStep) * kRows * 4;
 constexpr int kNumBars = 2 * kSlots + 2 * kQSlots + 3;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
 constexpr int kSmem = kOffMisc + 16;
@@ -81,34 +83,24 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+// 32 lanes x 32 bits, 16 columns: thread t gets lane t, columns c .. c + 15.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    // (the registers pass through, so that no use of them is scheduled before the wait)
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :: "memory");
 }
-// 32 lanes x 32 bits, 32 columns: thread t gets lane t, columns c .. c + 31.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-    tc_wait_ld(r);
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
         :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-           "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-           "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -165,9 +157,9 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     extern __shared__ __align__(1024) uint8_t smem[];
     float* const turn = reinterpret_cast<float*>(smem + kOffTurn);
     float* const join = reinterpret_cast<float*>(smem + kOffJoin);
-    float2* const max_s = reinterpret_cast<float2*>(smem + kOffMax);
+    float2* const max_s = reinterpret_cast<float2*>(smem + kOffMax);             // [2][kRows]
     int* const seen_s = reinterpret_cast<int*>(smem + kOffSeen);
-    float* const off_s = reinterpret_cast<float*>(smem + kOffOff);              // [kCols / 32][kRows]
+    float* const off_s = reinterpret_cast<float*>(smem + kOffOff);              // [kCols / kStep][kRows]
     uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kOffBars);        // [kSlots] a tile copied
     uint64_t* const empty = full + kSlots;                                      // [kSlots] its products are done
     uint64_t* const qfull = empty + kSlots;                                     // [kQSlots] the same for q
@@ -289,9 +281,9 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         }
         asm volatile("cp.async.wait_all;" ::: "memory");   // (a call that failed may have some on their way)
     } else if (warp == kQWarp) {
-        // ---- q: lane l < 4 the box of softmax warp l ----
+        // ---- q: lane l < 4 the box of lane quarter l ----
         int q_row = 0;
-        if (lane < kSoftWarps)
+        if (lane < 4)
             q_row = heads_warps == 1 ? (q.start + first + lane * per_warp) * a.H
                                      : (q.start + first + lane / heads_warps) * a.H + 32 * (lane % heads_warps);
         q_row = min(q_row, a.b.T * a.H - 1);               // (a box of none of the tile's tokens)
@@ -303,8 +295,8 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&qfull[slot], kTileBytes);
                 __syncwarp();
-                if (lane < kSoftWarps)
-                    copy_box(smem + kOffQ + slot * kTileBytes + lane * (kTileBytes / kSoftWarps), &q_map, 64 * (i % n_dims), q_row,
+                if (lane < 4)
+                    copy_box(smem + kOffQ + slot * kTileBytes + lane * (kTileBytes / 4), &q_map, 64 * (i % n_dims), q_row,
                              &qfull[slot]);
             }
             if (pass == 0 && a.cluster > 1) cluster_sync();
@@ -354,15 +346,16 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
             if (pass == 0 && a.cluster > 1) cluster_sync();
         }
     } else {
-        // ---- softmax: thread = row ----
-        const int row = threadIdx.x;
+        // ---- softmax: thread = row, of its quarter's columns every other kStep ----
+        const int quarter = warp & 3, half = warp >> 2;
+        const int row = 32 * quarter + lane;
         int token, head;
         const bool lives = row_of(row, token, head);
         const int pos = lives ? position_of(a.b, q, first + token) : -1;
         const int seen = (pos < 0 ? 0 : pos / a.b.page_size) - c0;         // columns of this CTA that the row sees
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         const int32_t* bt = a.b.block_table + static_cast<int64_t>(u.x) * a.b.max_pages + c0;
-        if (lives && head == 0) seen_s[token] = seen + c0;                 // (read by its own warp alone)
+        if (lives && head == 0) seen_s[token] = seen + c0;                 // (by both halves: the same)
         float m = -INFINITY, l = 0.0f;
         // Which of a round's columns have a key: lane j gets the bits of columns 32 j ..
         auto keyed_columns = [&](int r) {
@@ -381,48 +374,51 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
             return mine;
         };
         uint32_t keyed = 0u;
-        // 32 scores of the row in log2 units, -inf where it sees no block.
-        auto load = [&](int r, int j, float (&x)[32]) {
-            uint32_t v[32];
-            tmem_ld32(lanes + 32 * j, v);
-            const int left = seen - (r * kCols + 32 * j);
-            const uint32_t word = __shfl_sync(0xffffffffu, keyed, j);
-            const uint32_t sees = left >= 32 ? word : left <= 0 ? 0u : word & ((1u << left) - 1u);
+        // The bits of the kStep columns j.
+        auto keyed_step = [&](int j) { return (__shfl_sync(0xffffffffu, keyed, j >> 1) >> (kStep * (j & 1))) & 0xffffu; };
+        // Scores of the row in log2 units, -inf where it sees no block.
+        auto load = [&](int r, int j, float (&x)[kStep]) {
+            uint32_t v[kStep];
+            tmem_ld16(lanes + kStep * j, v);
+            const int left = seen - (r * kCols + kStep * j);
+            const uint32_t word = keyed_step(j);
+            const uint32_t sees = left >= kStep ? word : left <= 0 ? 0u : word & ((1u << left) - 1u);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * a.scale_log2;
-            if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) {
+            for (int c = 0; c < kStep; ++c) x[c] = __uint_as_float(v[c]) * a.scale_log2;
+            if (!__all_sync(0xffffffffu, sees == 0xffffu)) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = ((sees >> c) & 1u) != 0u ? x[c] : -INFINITY;
+                for (int c = 0; c < kStep; ++c) x[c] = ((sees >> c) & 1u) != 0u ? x[c] : -INFINITY;
             }
         };
         for (int r = 0; r < rounds; ++r) {
             keyed = keyed_columns(r);
             ok = warp_wait(dfull, static_cast<uint32_t>(r & 1), abort_flag);
-            ok = !bar_sync_or(1, 32 * kSoftWarps, !ok);        // one answer for the four warps
+            ok = !bar_sync_or(1, 32 * kSoftWarps, !ok);        // one answer for all of these warps
             if (!ok) break;
             tc_after();
-            const int chunks = (min(kCols, cols - r * kCols) + 31) / 32;
-            for (int j = 0; j < chunks; ++j) {
-                float x[32];
+            const int steps = (min(kCols, cols - r * kCols) + kStep - 1) / kStep;
+#pragma unroll 1
+            for (int j = half; j < steps; j += 2) {
+                float x[kStep];
                 load(r, j, x);
                 float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+                for (int c = 0; c < kStep; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
                 const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const float off = now == -INFINITY ? 0.0f : now;
                 l *= ex2_approx(m - off);                  // (nothing so far: l is 0)
                 m = now;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                uint32_t v[32];
+                uint32_t v[kStep];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < kStep; ++c) {
                     const float p = ex2_approx(x[c] - off);
                     sum[c & 3] += p;
                     v[c] = __float_as_uint(p);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 if (rounds == 1) {
-                    tmem_st32(lanes + 32 * j, v);
+                    tmem_st16(lanes + kStep * j, v);
                     off_s[j * kRows + row] = m;
                 }
             }
@@ -431,21 +427,24 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
             __syncwarp();
             if (lane == 0) mbar_arrive(dfree);
         }
-        float all_m = m, all_l = l;
-        if (a.cluster > 1) {
-            max_s[row] = make_float2(m, l);
-            cluster_sync();
-            for (int k = 0; k < peers; ++k) all_m = fmaxf(all_m, peer_float2(smem_u32(&max_s[row]), k).x);
-            all_l = 0.0f;
-            for (int k = 0; k < peers; ++k) {
-                const float2 v = peer_float2(smem_u32(&max_s[row]), k);
-                all_l += v.x == -INFINITY ? v.y : v.y * ex2_approx(v.x - all_m);       // (v.y is 0 there, or NaN)
-            }
+        // Maxima and sums of both halves, of all CTAs
+        max_s[half * kRows + row] = make_float2(m, l);
+        if (a.cluster > 1) cluster_sync();
+        else bar_sync_or(1, 32 * kSoftWarps, false);
+        float all_m = -INFINITY, all_l = 0.0f;
+        for (int k = 0; k < 2 * peers; ++k) {
+            const float2* at = &max_s[(k & 1) * kRows + row];
+            const float2 v = a.cluster > 1 ? peer_float2(smem_u32(at), k >> 1) : *at;
+            const float now = fmaxf(all_m, v.x), to = now == -INFINITY ? 0.0f : now;
+            all_l = all_l * ex2_approx(all_m - to) + v.y * ex2_approx(v.x - to);       // (0 x 0 where there is nothing)
+            all_m = now;
         }
         // p = exp2(x - off) x f; with one round exp2(x - a maximum so far) is in tensor memory
         const float off = all_m == -INFINITY ? 0.0f : all_m;
-        const float f = 1.0f / (all_l == 0.0f ? 1.0f : all_l);
-        float* const mine = turn + warp * 32 * kTurn;
+        const float f = lives ? 1.0f / (all_l == 0.0f ? 1.0f : all_l) : 0.0f;
+        float* const mine = turn + warp * kStep * kTurn;
+        // What the lane sums and stores: column lane % kStep, and of the warp's tokens every other one, or half of the rows of one.
+        const int col = lane & (kStep - 1), part = lane / kStep;
         for (int r = 0; r < rounds && ok; ++r) {
             if (rounds > 1) {
                 keyed = keyed_columns(r);
@@ -454,59 +453,60 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                 if (!ok) break;
                 tc_after();
             }
-            const int chunks = (min(kCols, cols - r * kCols) + 31) / 32;
-            for (int j = 0; j < chunks; ++j) {
+            const int steps = (min(kCols, cols - r * kCols) + kStep - 1) / kStep;
+#pragma unroll 1
+            for (int j = half; j < steps; j += 2) {
                 if (rounds == 1) {
-                    uint32_t v[32];
-                    tmem_ld32(lanes + 32 * j, v);
+                    uint32_t v[kStep];
+                    tmem_ld16(lanes + kStep * j, v);
                     const float g = ex2_approx(off_s[j * kRows + row] - off) * f;      // (0 where nothing was seen so far)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) mine[kTurn * c + lane] = lives ? __uint_as_float(v[c]) * g : 0.0f;
+                    for (int c = 0; c < kStep; ++c) mine[kTurn * c + lane] = lives ? __uint_as_float(v[c]) * g : 0.0f;
                 } else {
-                    float x[32];
+                    float x[kStep];
                     load(r, j, x);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) mine[kTurn * c + lane] = lives ? ex2_approx(x[c] - off) * f : 0.0f;
+                    for (int c = 0; c < kStep; ++c) mine[kTurn * c + lane] = lives ? ex2_approx(x[c] - off) * f : 0.0f;
                 }
                 __syncwarp();
-                // lane = column: the sums over each token's heads
-                const int c = c0 + r * kCols + 32 * j + lane;
-                const bool has = ((__shfl_sync(0xffffffffu, keyed, j) >> lane) & 1u) != 0u;
-                if (heads_warps == 1) {
-                    for (int k = 0; k < per_warp; ++k) {
-                        const int tok = warp * per_warp + k;
+                const int c = c0 + r * kCols + kStep * j + col, end = c0 + cols;
+                const bool has = ((keyed_step(j) >> col) & 1u) != 0u;
+                const float* const rows = mine + kTurn * col;
+                auto store = [&](int tok, float sum) {
+                    if (c < min(seen_s[tok], end))
+                        a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
+                };
+                auto sum16 = [&](const float* x) {
+                    const float4 v0 = *reinterpret_cast<const float4*>(x), v1 = *reinterpret_cast<const float4*>(x + 4);
+                    const float4 v2 = *reinterpret_cast<const float4*>(x + 8), v3 = *reinterpret_cast<const float4*>(x + 12);
+                    return (((v0.x + v0.y) + (v0.z + v0.w)) + ((v1.x + v1.y) + (v1.z + v1.w))) +
+                           (((v2.x + v2.y) + (v2.z + v2.w)) + ((v3.x + v3.y) + (v3.z + v3.w)));
+                };
+                if (a.H == 16) {
+                    const int tok = 2 * quarter + part;
+                    const float sum = sum16(rows + 16 * part);
+                    if (tok < n_tokens) store(tok, sum);
+                } else if (a.H < 32) {
+                    for (int k = part; k < per_warp; k += 2) {
+                        const int tok = quarter * per_warp + k;
                         if (tok >= n_tokens) break;
-                        const float* col = mine + kTurn * lane + k * a.H;
-                        float4 part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (a.H % 4 == 0) {
-#pragma unroll 4
-                            for (int h = 0; h < a.H; h += 4) {
-                                const float4 v = *reinterpret_cast<const float4*>(col + h);
-                                part = make_float4(part.x + v.x, part.y + v.y, part.z + v.z, part.w + v.w);
-                            }
-                        } else {
-                            for (int h = 0; h < a.H; ++h) part.x += col[h];
-                        }
-                        const float sum = (part.x + part.y) + (part.z + part.w);
-                        if (c < min(seen_s[tok], c0 + cols))
-                            a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
+                        float sum = 0.0f;
+                        for (int h = 0; h < a.H; ++h) sum += rows[k * a.H + h];
+                        store(tok, sum);
                     }
                 } else {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int h = 0; h < 32; h += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(mine + kTurn * lane + h);
-                        sum += (v.x + v.y) + (v.z + v.w);
+                    // a warp's part of one token's heads; lanes past the last head hold 0
+                    float sum = sum16(rows + 16 * part);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, kStep);
+                    const int tok = quarter / heads_warps;
+                    if (heads_warps > 1) {
+                        if (part == 0) join[kStep * warp + col] = sum;
+                        bar_sync_or(2 + half, 128, false);
+                        if (quarter % heads_warps == 0)
+                            for (int w = 1; w < heads_warps; ++w) sum += join[kStep * (warp + w) + col];
+                        bar_sync_or(2 + half, 128, false);
                     }
-                    join[32 * warp + lane] = sum;
-                    bar_sync_or(1, 32 * kSoftWarps, false);
-                    const int tok = warp / heads_warps;
-                    if (warp % heads_warps == 0 && tok < n_tokens) {
-                        for (int w = 1; w < heads_warps; ++w) sum += join[32 * (warp + w) + lane];
-                        if (c < min(seen_s[tok], c0 + cols))
-                            a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
-                    }
-                    bar_sync_or(1, 32 * kSoftWarps, false);
+                    if (quarter % heads_warps == 0 && part == 0 && tok < n_tokens) store(tok, sum);
                 }
                 __syncwarp();
             }
@@ -579,11 +579,12 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
         return MLA_ECUDA;
     ScoreArgs a = {b, static_cast<const __nv_bfloat16*>(keys_bf16), scores, H, d_qk, num_keys, 1, kCols, 1, sm_scale * kLog2e};
     a.tile_tokens = H <= 32 ? 4 * (32 / H) : H <= 64 ? 2 : 1;
-    const int64_t tiles = static_cast<int64_t>(T) / a.tile_tokens + (n_seq < T ? n_seq : T);
-    // CTAs per tile: as many as hold all of the table's blocks at once, and where that leaves SMs without work, as many
-    // as have kLeast columns each.
+    // (a tile has a token at least, and only a sequence's last one has fewer than tile_tokens)
+    const int64_t tiles = std::min<int64_t>(T, static_cast<int64_t>(T) / a.tile_tokens + n_seq);
+    // CTAs per tile: as many as hold three quarters of the table's blocks at once (tables are seldom full), and where
+    // that leaves SMs without work, as many as have kLeast columns each.
     constexpr int kLeast = 64;
-    while (a.cluster < kMaxCluster && a.cluster * kCols < max_pages) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && a.cluster * kCols < max_pages - max_pages / 4) a.cluster *= 2;
     while (a.cluster < kMaxCluster && tiles * a.cluster < sms && a.cluster * kLeast < max_pages) a.cluster *= 2;
     if (tiles * a.cluster < 2 * sms) a.least = kLeast;
     if (tiles * a.cluster > INT_MAX) a.cluster = 1;
