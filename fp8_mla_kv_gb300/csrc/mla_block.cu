@@ -115,18 +115,17 @@ block_keys_kernel(const Batch b, const uint8_t* __restrict__ cache, int64_t num_
 //
 // A score becomes a 32-bit key that orders like it (0: not to be chosen, the largest: chosen whatever its score). The
 // W-th largest key is found two bits at a time from the top, by counting how many keys have each next digit; the keys
-// above it are taken, and of those equal to it the first ones. A CTA of kWarps warps takes a token; kWarps x 256 keys
-// stay in registers, and where there are more, each pass reads the scores again (from L2).
+// above it are taken, and of those equal to it the first ones. A CTA takes a token, with its keys in registers;
+// where there are more than fit, each pass reads the scores again (from L2).
 // Bound by the chain of passes (16 at most, it ends when a digit's keys are exactly those wanted): TIME_SELECT.
-constexpr int kPer = 8;                                    // keys per thread at a time
-
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (!(x > -INFINITY)) return 0u;                       // -inf or NaN: not chosen
     const uint32_t u = x == 0.0f ? 0u : __float_as_uint(x);       // (-0 is 0)
     return (u >> 31) != 0u ? ~u : u | 0x80000000u;
 }
 
-template <int kWarps, bool kWide>
+// kWarps warps with kPer keys a thread hold a token's keys; kWide: more are read again for each pass.
+template <int kWarps, int kPer, bool kWide>
 __global__ void __launch_bounds__(32 * kWarps)
 block_select_kernel(const Batch b, const float* __restrict__ scores, int columns, int sink, int local, int width,
                     int32_t* __restrict__ blocks) {
@@ -145,40 +144,40 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
     int32_t* out = blocks + static_cast<int64_t>(t) * width;
     const int n = pos < 0 ? 0 : pos / b.page_size + 1;     // blocks up to the token's own
     const float* row = scores + static_cast<int64_t>(t) * columns;
-    auto key_of = [&](int i) -> uint32_t {
-        if (i >= n) return 0u;
-        if (i < sink || i > n - 1 - local) return 0xffffffffu;
-        return order_key(__ldg(row + i));
-    };
     uint32_t key[kPer];
     auto load = [&](int base) {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) key[k] = key_of(base + k * kThreads + threadIdx.x);
+        for (int k = 0; k < kPer; ++k) {
+            const int i = base + k * kThreads + threadIdx.x;
+            const bool always = i < sink || i > n - 1 - local;
+            key[k] = i >= n ? 0u : always ? 0xffffffffu : order_key(__ldg(row + i));
+        }
     };
     load(0);
     const int chunks = kWide ? (n + kChunk - 1) / kChunk : 1;
-    // The threshold's digits; `left`: how many keys that agree with it so far are still wanted.
+    // The threshold's digits; `left`: how many keys that agree with it so far are still wanted. Where there are no more
+    // keys than wanted, all are taken: the threshold is 0, and a key of 0 never is.
     uint32_t found = 0u;
     int left = width;
-    bool all = false;                                      // every key that agrees is taken
+    bool all = n <= width;                                 // every key from the threshold on is taken
 #pragma unroll 1
     for (int shift = 30; shift >= 0 && !all; shift -= 2) {
         const int turn = (shift >> 1) & 1;
-        int c3 = 0, c2 = 0, c1 = 0;
+        int c1 = 0, c2 = 0, c3 = 0;                        // keys whose next digit is 1, 2, 3
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             if (kWide) load(c * kChunk);
+            uint32_t packed = 0u;                          // ten bits each: at most 32 x kPer in a warp
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-                const uint32_t d = (key[k] ^ found) >> shift;      // agrees above: 0 .. 3, the digit
-                c3 += d == 3u;
-                c2 += d == 2u;
-                c1 += d == 1u;
+                const uint32_t d = ((key[k] ^ found) >> shift) - 1u;       // agrees above: -1 .. 2, the digit less 1
+                packed += d < 3u ? 1u << (10u * d) : 0u;
             }
+            packed = __reduce_add_sync(0xffffffffu, packed);
+            c1 += packed & 1023u;
+            c2 += (packed >> 10) & 1023u;
+            c3 += packed >> 20;
         }
-        c3 = __reduce_add_sync(0xffffffffu, c3);
-        c2 = __reduce_add_sync(0xffffffffu, c2);
-        c1 = __reduce_add_sync(0xffffffffu, c1);
         if (kWarps > 1) {
             if (lane == 0) {
                 counts[turn][warp][0] = c1;
@@ -186,50 +185,45 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
                 counts[turn][warp][2] = c3;
             }
             __syncthreads();
-            c1 = lane < kWarps ? counts[turn][lane][0] : 0;
-            c2 = lane < kWarps ? counts[turn][lane][1] : 0;
-            c3 = lane < kWarps ? counts[turn][lane][2] : 0;
-            c3 = __reduce_add_sync(0xffffffffu, c3);
-            c2 = __reduce_add_sync(0xffffffffu, c2);
-            c1 = __reduce_add_sync(0xffffffffu, c1);
+            c1 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][0] : 0);
+            c2 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][1] : 0);
+            c3 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][2] : 0);
         }
-        int here = c3;
         uint32_t digit = 3u;
+        int here = c3;
         if (left > here) { left -= here; here = c2; digit = 2u; }
         if (digit == 2u && left > here) { left -= here; here = c1; digit = 1u; }
         if (digit == 1u && left > here) { left -= here; digit = 0u; }
         found |= digit << shift;
         all = digit != 0u && left == here;                 // (the lower digits stay 0: any are taken)
     }
-    // Those above the threshold and the first `left` of those equal to it, in ascending order. (Fewer keys than wanted:
-    // the threshold is 0, and a key of 0 is never taken.)
-    auto above = [&](uint32_t x) { return all ? x >= found : x > found; };
+    // Those above the threshold and the first `left` of those equal to it, in ascending order.
+    auto above = [&](uint32_t x) { return x != 0u && (all ? x >= found : x > found); };
     auto equal = [&](uint32_t x) { return !all && found != 0u && x == found; };
     const uint32_t lower = (1u << lane) - 1u;
     int n_above = 0, n_equal = 0;                          // before this step's
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
         if (kWide) load(c * kChunk);
-        if (kWarps > 1) __syncthreads();                   // (the chunk before has been placed)
+        if (kWarps > 1) {
+            __syncthreads();                               // (the chunk before has been placed)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const unsigned a = __ballot_sync(0xffffffffu, above(key[k])), e = __ballot_sync(0xffffffffu, equal(key[k]));
-            if (lane == 0) place[k][warp] = __popc(a) | __popc(e) << 16;
-        }
-        if (kWarps > 1) __syncthreads();
-        else __syncwarp();
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int row = lane < kWarps ? place[k][lane] : 0;
-            int incl = row;
-#pragma unroll
-            for (int d = 1; d < kWarps; d <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += x;
+            for (int k = 0; k < kPer; ++k) {
+                const unsigned a = __ballot_sync(0xffffffffu, above(key[k])), e = __ballot_sync(0xffffffffu, equal(key[k]));
+                if (lane == 0) place[k][warp] = __popc(a) | __popc(e) << 16;
             }
-            const int total = __shfl_sync(0xffffffffu, incl, kWarps - 1), before = __shfl_sync(0xffffffffu, incl - row, warp);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
             const bool a = above(key[k]), e = equal(key[k]);
             const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
+            int total = __popc(am) | __popc(em) << 16, before = 0;
+            if (kWarps > 1) {
+                const int mine = lane < kWarps ? place[k][lane] : 0;
+                total = __reduce_add_sync(0xffffffffu, mine);
+                before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+            }
             const int e_rank = n_equal + (before >> 16) + __popc(em & lower);
             if (a || (e && e_rank < left))
                 out[n_above + (before & 0xffff) + __popc(am & lower) + min(e_rank, left)] = c * kChunk + k * kThreads + threadIdx.x;
@@ -277,12 +271,13 @@ extern "C" int mla_block_select(const float* scores, int T, int columns, const i
     b.max_pages = columns;
     b.err = mla_host::device_error_word();
     if (b.err == nullptr) return MLA_ECUDA;
-    void (*kernel)(const Batch, const float*, int, int, int, int, int32_t*) = block_select_kernel<32, true>;
+    void (*kernel)(const Batch, const float*, int, int, int, int, int32_t*) = block_select_kernel<32, 8, true>;
     int warps = 32;
-    if (columns <= 256) { kernel = block_select_kernel<1, false>; warps = 1; }
-    else if (columns <= 1024) { kernel = block_select_kernel<4, false>; warps = 4; }
-    else if (columns <= 2048) { kernel = block_select_kernel<8, false>; warps = 8; }
-    else if (columns <= 8192) { kernel = block_select_kernel<32, false>; warps = 32; }
+    if (columns <= 256) { kernel = block_select_kernel<1, 8, false>; warps = 1; }
+    else if (columns <= 512) { kernel = block_select_kernel<1, 16, false>; warps = 1; }
+    else if (columns <= 1024) { kernel = block_select_kernel<4, 8, false>; warps = 4; }
+    else if (columns <= 4096) { kernel = block_select_kernel<16, 8, false>; warps = 16; }
+    else if (columns <= 8192) { kernel = block_select_kernel<32, 8, false>; warps = 32; }
     return mla_host::launch_pdl(kernel, T, 32 * warps, 0, stream, b, scores, columns, sink, local, width, blocks) ? MLA_OK
                                                                                                                 : MLA_ECUDA;
 }
