@@ -55,6 +55,7 @@ using namespace mla_chunk;
 constexpr int kN = kLargeBlock;              // positions per block (M of the MMAs)
 constexpr int kRows = kLargeRows;            // query rows per tile (N of the MMAs)
 constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kQWarps = kSoftWarps + kConvWarps;        // they lay out q, too
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kMetaWarp = kMmaWarp + 1, kMetaWarps = 2;
 constexpr int kPvWarp = kMetaWarp + kMetaWarps;
@@ -330,6 +331,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     uint64_t* pvdone = bars + 21;      // PV of a block done (commit)
     uint64_t* mfull = bars + 22;       // [2] meta stage written (2 meta warps)
     uint64_t* mfree = bars + 24;       // [2] meta stage read (8 softmax, 8 converting warps)
+    uint64_t* qready = bars + 26;      // q written (16 warps)
     uint64_t* fin = bars + 27;         // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
@@ -348,6 +350,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
     const int nblk = (n_keys + kN - 1) / kN;
     const int n_rows = min(kRows, pc.rows - pc.row0);
     const uint32_t all = kForm == kDense ? 0u : tile_tokens(args, pc, n_rows);
+    const uint32_t live = kForm == kBlocks ? static_cast<uint32_t>(__ldg(&args.groups[pc.seq].y)) : 0xffffffffu;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kASlots; ++i) {
@@ -368,6 +371,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             mbar_init(&mfull[i], kMetaWarps);
             mbar_init(&mfree[i], kSoftWarps + kConvWarps);
         }
+        mbar_init(qready, kQWarps);
         mbar_init(&fin[0], 1);
         mbar_init(&fin[1], 1);
         *abort_flag = 0;
@@ -378,90 +382,96 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                      :: "r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (threadIdx.x < kRows) {
-        const int r = threadIdx.x;
-        if (kForm == kDense) {
-            const int lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
-            rd.lim[r] = lim;
-            rd.unseen[r] = lim > 0;
-        } else {
-            rd.lim[r] = r < n_rows ? static_cast<int>(token_bit(args, pc, pc.row0 + r)) : 0;
-            rd.unseen[r] = r < n_rows;
-        }
-        rd.neg_m[r] = 0.0f;
-    }
-    // ---- q of the tile's rows as operand tiles: a warp per row, lane l the 16-byte units
-    // l and l + 32 of the latent and, l < 8, unit l of RoPE; the next row's on their way ----
-    uint4 ahead[3];
-    auto load_q = [&](int r) {
-        ahead[0] = ahead[1] = ahead[2] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n_rows) {
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(args.q + (pc.grow0 + pc.row0 + r) * args.d_qk);
-            ahead[0] = ld_nc_v4(src + 16 * lane);
-            ahead[1] = ld_nc_v4(src + 512 + 16 * lane);
-            if (kRopeOn && lane < 8) ahead[2] = ld_nc_v4(src + 1024 + 16 * lane);
-        }
-    };
-    load_q(warp);
-#pragma unroll 1
-    for (int r = warp; r < kRows; r += kThreads / 32) {
-        const uint4 v[3] = {ahead[0], ahead[1], ahead[2]};
-        load_q(r + kThreads / 32);
-        // The row's largest value (as bits: |bf16| are ordered like integers) and the power of two that
-        // brings it into [2^7, 2^8); undone on the scores.
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
-        }
-        const int mx = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        const int k = mx >= 0x7f80 ? 0 : max((mx >> 7) - 134, -126);
-        const __nv_bfloat162 down = __float2bfloat162_rn(__int_as_float((127 - k) << 23));
-        if (lane == 0) rd.shift[r] = __int_as_float((127 + k) << 23);
-        // Each value as an E4M3 part and the rest as an E5M2 one. Operand place of the dims: 4-byte word
-        // m of the 32 bytes that a converting thread holds of a row (16 c .. of each half) goes to tensor-memory
-        // column 8 (m / 2) + 2 c + m % 2, so the 8 dims of a unit stay together.
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __half2 x = __float22half2_rn(__bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down)));
-                hi[j] = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-                const __half2 y(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[j]), __NV_E4M3));
-                lo[j] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, y), __NV_SATFINITE, __NV_E5M2);
-            }
-            const int u = lane + 32 * i, ut = u & 15;
-            const int at = 4 * (16 * (ut >> 3) + 8 * (ut & 1) + 2 * ((ut >> 1) & 3));      // bytes
-            uint8_t* q = smem + kOffQ + 2 * (u >> 4) * kQChunk + swz(kRows, r, at >> 4) + (at & 8);
-            *reinterpret_cast<uint2*>(q) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(q + kQChunk) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        }
-        if (kRopeOn && lane < 8) {
-            const uint32_t w[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down);
-                h[j] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            const int at = 16 * (2 * (lane >> 2)) + 4 * (lane & 3);
-            uint8_t* q = smem + kOffQ + 8 * kQChunk;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int pos = at + 16 * j;
-                *reinterpret_cast<uint2*>(q + swz(kRows, r, pos >> 3) + ((pos & 4) << 1)) = make_uint2(h[2 * j], h[2 * j + 1]);
-            }
-        }
-    }
-    fence_proxy_async_smem();
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = *tmem_slot;
+    // The other warps begin with their own work meanwhile: the table's chain of loads is as long as this.
+    if (warp < kQWarps) {
+        if (threadIdx.x < kRows) {
+            const int r = threadIdx.x;
+            if (kForm == kDense) {
+                const int lim = r < n_rows ? row_limit(args, pc, pc.row0 + r) - pc.k0 : 0;
+                rd.lim[r] = lim;
+                rd.unseen[r] = lim > 0;
+            } else {
+                rd.lim[r] = r < n_rows ? static_cast<int>(token_bit(args, pc, pc.row0 + r)) : 0;
+                rd.unseen[r] = r < n_rows;
+            }
+            rd.neg_m[r] = 0.0f;
+        }
+        // ---- q of the tile's rows as operand tiles: a warp of the first sixteen per row, lane l the 16-byte units
+        // l and l + 32 of the latent and, l < 8, unit l of RoPE; the next row's on their way ----
+        uint4 ahead[3];
+        auto load_q = [&](int r) {
+            ahead[0] = ahead[1] = ahead[2] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < n_rows) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(args.q + (pc.grow0 + pc.row0 + r) * args.d_qk);
+                ahead[0] = ld_nc_v4(src + 16 * lane);
+                ahead[1] = ld_nc_v4(src + 512 + 16 * lane);
+                if (kRopeOn && lane < 8) ahead[2] = ld_nc_v4(src + 1024 + 16 * lane);
+            }
+        };
+        load_q(warp);
+#pragma unroll 1
+        for (int r = warp; r < kRows; r += kQWarps) {
+            const uint4 v[3] = {ahead[0], ahead[1], ahead[2]};
+            load_q(r + kQWarps);
+            // The row's largest value (as bits: |bf16| are ordered like integers) and the power of two that
+            // brings it into [2^7, 2^8); undone on the scores.
+            uint32_t top = 0u;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
+            }
+            const int mx = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+            const int k = mx >= 0x7f80 ? 0 : max((mx >> 7) - 134, -126);
+            const __nv_bfloat162 down = __float2bfloat162_rn(__int_as_float((127 - k) << 23));
+            if (lane == 0) rd.shift[r] = __int_as_float((127 + k) << 23);
+            // Each value as an E4M3 part and the rest as an E5M2 one. Operand place of the dims: 4-byte word
+            // m of the 32 bytes that a converting thread holds of a row (16 c .. of each half) goes to tensor-memory
+            // column 8 (m / 2) + 2 c + m % 2, so the 8 dims of a unit stay together.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 x = __float22half2_rn(__bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down)));
+                    hi[j] = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                    const __half2 y(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[j]), __NV_E4M3));
+                    lo[j] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, y), __NV_SATFINITE, __NV_E5M2);
+                }
+                const int u = lane + 32 * i, ut = u & 15;
+                const int at = 4 * (16 * (ut >> 3) + 8 * (ut & 1) + 2 * ((ut >> 1) & 3));      // bytes
+                uint8_t* q = smem + kOffQ + 2 * (u >> 4) * kQChunk + swz(kRows, r, at >> 4) + (at & 8);
+                *reinterpret_cast<uint2*>(q) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(q + kQChunk) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            }
+            if (kRopeOn && lane < 8) {
+                const uint32_t w[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), down);
+                    h[j] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                const int at = 16 * (2 * (lane >> 2)) + 4 * (lane & 3);
+                uint8_t* q = smem + kOffQ + 8 * kQChunk;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int pos = at + 16 * j;
+                    *reinterpret_cast<uint2*>(q + swz(kRows, r, pos >> 3) + ((pos & 4) << 1)) = make_uint2(h[2 * j], h[2 * j + 1]);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        warp_arrive(qready);
+        bar_sync_or(3, 32 * kQWarps, false);           // what is kept per row
+    }
+
     constexpr int kGroups = kRopeOn ? 5 : 4;          // S partials per block: [RoPE,] tiles 0 .. 3
 
     if (warp < kSoftWarps) {
@@ -474,6 +484,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         // what is uniform over this half's query rows
         const int my_lim = rd.lim[c0 + lane];
         const int lim_min = __reduce_min_sync(0xffffffffu, my_lim);
+        const bool whole_tokens = kForm != kDense && args.H % 16 == 0;
         bool unseen = true;                            // some row has seen nothing yet: take maxima
         float l = 0.0f;                                // sum of p of query row c0 + lane, over the warp's positions
         float sig[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -530,10 +541,17 @@ mla_chunk_large_kernel(const ChunkArgs args) {
             }
             if (__builtin_expect(__any_sync(0xffffffffu, state != 1 || (kForm != kDense && (tokens & all) != all)) ||
                                      (kForm == kDense && kN * (b + 1) > lim_min), kForm == kBlocks)) {
+                if (kForm == kDense || !whole_tokens || __any_sync(0xffffffffu, state != 1)) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    if (state == 2) d[c] = __int_as_float(0x7FC00000);
-                    if (state == 0 || !attends(c)) d[c] = -INFINITY;
+                    for (int c = 0; c < kCols; ++c) {
+                        if (state == 2) d[c] = __int_as_float(0x7FC00000);
+                        if (state == 0 || !attends(c)) d[c] = -INFINITY;
+                    }
+                } else {
+                    // sixteen query rows are one token's: a choice for each such part
+                    const bool a0 = attends(0), a1 = attends(16);
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) d[c] = (c < 16 ? a0 : a1) ? d[c] : -INFINITY;
                 }
             }
             float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -690,13 +708,14 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 const float kNaN = __int_as_float(0x7FC00000);
                 rd.alpha[c] = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : kNaN);
                 const float lse = sum > 0.0f ? (log2f(sum) - rd.neg_m[c]) * kLn2 : (sum == 0.0f ? -INFINITY : kNaN);
-                if (c < n_rows && row_lives<kForm>(args, pc, pc.row0 + c)) {
+                if (c < n_rows && (kForm != kBlocks || (live & static_cast<uint32_t>(rd.lim[c])) != 0u)) {
                     if (pc.part < 0) args.lse[pc.grow0 + pc.row0 + c] = lse;
                     else args.part_lse[static_cast<int64_t>(pc.part) * kRows + c] = lse;
                 }
             }
             bar_sync_or(1 + half, 128, false);
             const int left = n_rows - c0;              // query rows of this half that there are
+            const bool some_dead = kForm == kBlocks && (live & all) != all;    // tokens that are in no sequence
 #pragma unroll 1
             for (int t = 0; t < 4; ++t) {
                 uint32_t o[kCols];
@@ -709,10 +728,18 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 const float f = t == 0 ? sig[0] : t == 1 ? sig[1] : t == 2 ? sig[2] : sig[3];
                 const int dim = kTile * t + key;           // here the lane is a dim
                 if (pc.part < 0) {
-                    __nv_bfloat16* to = args.out + (pc.grow0 + pc.row0 + c0) * kLatent + dim;
+                    // Two dims of a row a store: an even lane takes row c of a pair of rows, an odd one row c + 1. (A BF16
+                    // value a store took three times as long: TIME_EPI.)
+                    const int odd = lane & 1;
+                    __nv_bfloat16* to = args.out + (pc.grow0 + pc.row0 + c0 + odd) * kLatent + (dim - odd);
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c)
-                        if (c < left && row_lives<kForm>(args, pc, pc.row0 + c0 + c)) to[c * kLatent] = __float2bfloat16_rn(__uint_as_float(o[c]) * (f * rd.alpha[c0 + c]));
+                    for (int c = 0; c < kCols; c += 2) {
+                        const float x = __uint_as_float(o[c]) * (f * rd.alpha[c0 + c]);
+                        const float y = __uint_as_float(o[c + 1]) * (f * rd.alpha[c0 + c + 1]);
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+                        if (c + odd < left && (!some_dead || (live & static_cast<uint32_t>(rd.lim[c0 + c + odd])) != 0u))
+                            *reinterpret_cast<uint32_t*>(to + c * kLatent) = pack_bf16x2(odd ? got : x, odd ? y : got);
+                    }
                 } else {
                     float* to = args.part_o + (static_cast<int64_t>(pc.part) * kRows + c0) * kLatent + dim;
 #pragma unroll
@@ -815,10 +842,10 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         if (elect_one()) {
             const uint64_t dq = sw128_desc(smem_u32(smem) + kOffQ, 16, 1024);
             const int n_groups = nblk * kGroups;
-            bool ok = true;
+            bool ok = wait_or_abort(qready, 0u, abort_flag);
             int t = 4 - kGroups;                       // latent tile; -1: RoPE
 #pragma unroll 1
-            for (int g = 0; g < n_groups; ++g) {
+            for (int g = 0; g < n_groups && ok; ++g) {
                 const int slot = g & 1, as = g % kASlots;
                 ok = wait_or_abort(&afull[as], static_cast<uint32_t>((g / kASlots) & 1), abort_flag);
                 if (g >= 2) ok = ok && wait_or_abort(&sfree[slot], static_cast<uint32_t>(((g >> 1) - 1) & 1), abort_flag);
