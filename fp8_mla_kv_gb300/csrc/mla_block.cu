@@ -113,8 +113,7 @@ block_keys_kernel(const Batch b, const uint8_t* __restrict__ cache, int64_t num_
 
 // ---- selection ----
 //
-// A score becomes a 32-bit key that orders like it (0: not to be chosen, the largest: chosen whatever its score). The
-// W-th largest key is found two bits at a time from the top, by counting how many keys have each next digit; the keys
+// A score becomes a 32-bit key that orders like it (0: not to be chosen). The last one wanted is found two bits at a time from the top, by counting how many keys have each next digit; the keys
 // above it are taken, and of those equal to it the first ones. A CTA takes a token, with its keys in registers;
 // where there are more than fit, each pass reads the scores again (from L2).
 // Bound by the chain of passes (16 at most, it ends when a digit's keys are exactly those wanted): TIME_SELECT.
@@ -144,13 +143,14 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
     int32_t* out = blocks + static_cast<int64_t>(t) * width;
     const int n = pos < 0 ? 0 : pos / b.page_size + 1;     // blocks up to the token's own
     const float* row = scores + static_cast<int64_t>(t) * columns;
+    auto always = [&](int i) { return i < sink || i > n - 1 - local; };
     uint32_t key[kPer];
     auto load = [&](int base) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const int i = base + k * kThreads + threadIdx.x;
-            const bool always = i < sink || i > n - 1 - local;
-            key[k] = i >= n ? 0u : always ? 0xffffffffu : order_key(__ldg(row + i));
+            key[k] = 0u;
+            if (base + k * kThreads < n) key[k] = i >= n || always(i) ? 0u : order_key(__ldg(row + i));
         }
     };
     load(0);
@@ -158,11 +158,40 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
     // The threshold's digits; `left`: how many keys that agree with it so far are still wanted. Where there are no more
     // keys than wanted, all are taken: the threshold is 0, and a key of 0 never is.
     uint32_t found = 0u;
-    int left = width;
+    int left = width - sink - local;                       // (of n > width blocks so many are taken anyway)
     bool all = n <= width;                                 // every key from the threshold on is taken
+    // Bits in which no two of the scores differ need no pass: exponents are near each other, and rounded scores end in zeros.
+    uint32_t ones = 0u, zeros = 0u;                        // set in any, clear in any
+#pragma unroll 1
+    for (int c = 0; c < chunks && !all; ++c) {
+        if (kWide) load(c * kChunk);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (key[k] != 0u) {
+                ones |= key[k];
+                zeros |= ~key[k];
+            }
+    }
+    ones = __reduce_or_sync(0xffffffffu, ones);
+    zeros = __reduce_or_sync(0xffffffffu, zeros);
+    if (kWarps > 1) {
+        if (lane == 0) {
+            counts[1][warp][0] = ones;
+            counts[1][warp][1] = zeros;
+        }
+        __syncthreads();
+        ones = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][0] : 0u);
+        zeros = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][1] : 0u);
+    }
+    const uint32_t differ = ones & zeros;
+    int turn = 0;
 #pragma unroll 1
     for (int shift = 30; shift >= 0 && !all; shift -= 2) {
-        const int turn = (shift >> 1) & 1;
+        if (((differ >> shift) & 3u) == 0u) {
+            found |= ones & (3u << shift);
+            continue;
+        }
+        turn ^= 1;
         int c1 = 0, c2 = 0, c3 = 0;                        // keys whose next digit is 1, 2, 3
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
@@ -198,7 +227,7 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
         all = digit != 0u && left == here;                 // (the lower digits stay 0: any are taken)
     }
     // Those above the threshold and the first `left` of those equal to it, in ascending order.
-    auto above = [&](uint32_t x) { return x != 0u && (all ? x >= found : x > found); };
+    auto above = [&](uint32_t x, int i) { return (x != 0u && (all ? x >= found : x > found)) || (i < n && always(i)); };
     auto equal = [&](uint32_t x) { return !all && found != 0u && x == found; };
     const uint32_t lower = (1u << lane) - 1u;
     int n_above = 0, n_equal = 0;                          // before this step's
@@ -209,14 +238,16 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
             __syncthreads();                               // (the chunk before has been placed)
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-                const unsigned a = __ballot_sync(0xffffffffu, above(key[k])), e = __ballot_sync(0xffffffffu, equal(key[k]));
+                const unsigned a = __ballot_sync(0xffffffffu, above(key[k], c * kChunk + k * kThreads + threadIdx.x)), e = __ballot_sync(0xffffffffu, equal(key[k]));
                 if (lane == 0) place[k][warp] = __popc(a) | __popc(e) << 16;
             }
             __syncthreads();
         }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const bool a = above(key[k]), e = equal(key[k]);
+            if (c * kChunk + k * kThreads >= n) break;
+            const int i = c * kChunk + k * kThreads + threadIdx.x;
+            const bool a = above(key[k], i), e = equal(key[k]);
             const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
             int total = __popc(am) | __popc(em) << 16, before = 0;
             if (kWarps > 1) {
@@ -226,7 +257,7 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
             }
             const int e_rank = n_equal + (before >> 16) + __popc(em & lower);
             if (a || (e && e_rank < left))
-                out[n_above + (before & 0xffff) + __popc(am & lower) + min(e_rank, left)] = c * kChunk + k * kThreads + threadIdx.x;
+                out[n_above + (before & 0xffff) + __popc(am & lower) + min(e_rank, left)] = i;
             n_above += total & 0xffff;
             n_equal += total >> 16;
         }

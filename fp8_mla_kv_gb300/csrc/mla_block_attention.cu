@@ -27,7 +27,10 @@ constexpr int kThreads = 256;
 constexpr int kWords = 2048;                           // of the bit map: 65,536 blocks at a time
 constexpr int kPerThread = kWords / kThreads;
 
-// Blocks of the group's tokens, ascending by sequence and block. TIME_LISTS.
+// Blocks of the group's tokens, ascending by sequence and block. A thread keeps up to kKeep entries of the lists (and looks
+// the others up again each time). Bound by its chain of loads (sequences, lists, table): TIME_LISTS.
+constexpr int kKeep = 4;
+
 __global__ void __launch_bounds__(kThreads)
 block_lists_kernel(const Batch b, const int32_t* __restrict__ blocks, int width, int group_tokens, int64_t num_slots,
                    BlockEntry* __restrict__ entries, int entry_cap, int2* __restrict__ groups) {
@@ -38,8 +41,16 @@ block_lists_kernel(const Batch b, const int32_t* __restrict__ blocks, int width,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x == 0) check_lengths(b);
     const int first = blockIdx.x * group_tokens, n_tokens = min(group_tokens, b.T - first);
+    const int32_t* const lists = blocks + static_cast<int64_t>(first) * width;
+    const int total = n_tokens * width;
+    int block[kKeep], phys[kKeep], token[kKeep];
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        block[j] = i < total ? __ldg(lists + i) : -1;
+    }
+    if (blockIdx.x == 0) check_lengths(b);
     for (int k = warp; k < n_tokens; k += kThreads / 32) {
         const int s = sequence_at(b, first + k, lane);
         int pos = -1;
@@ -53,6 +64,29 @@ block_lists_kernel(const Batch b, const int32_t* __restrict__ blocks, int width,
         }
     }
     __syncthreads();
+    // Its page where token k attends something of the block (at or before its own, with a page), else -1.
+    auto page_of = [&](int at, int k) {
+        const int s = seq_s[k], pos = pos_s[k];
+        if (at < 0 || s < 0) return -1;
+        if (at >= b.max_pages) atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
+        if (pos < 0 || at > pos / b.page_size) return -1;
+        const int page = __ldg(b.block_table + static_cast<int64_t>(s) * b.max_pages + at);
+        if (page >= 0 && static_cast<int64_t>(page) * b.page_size >= num_slots) {
+            atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
+            return -1;
+        }
+        return page;
+    };
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        token[j] = 0;
+        phys[j] = -1;
+        if (i < total) {
+            token[j] = i / width;
+            phys[j] = page_of(block[j], token[j]);
+        }
+    }
     BlockEntry* out = entries + static_cast<int64_t>(blockIdx.x) * entry_cap;
     uint32_t live = 0u;
     int count = 0;                                     // entries so far
@@ -60,35 +94,32 @@ block_lists_kernel(const Batch b, const int32_t* __restrict__ blocks, int width,
         const int s = seq_s[k0];
         for (k1 = k0 + 1; k1 < n_tokens && seq_s[k1] == s;) ++k1;
         if (s < 0) continue;
-        live |= (k1 - k0 == 32 ? 0xffffffffu : (1u << (k1 - k0)) - 1u) << k0;
+        live |= (0xffffffffu >> (32 - (k1 - k0))) << k0;
+        if (pos_s[k1 - 1] < 0) continue;               // (their positions ascend)
         const int ahead0 = k0 - pos_s[k0];             // position p is that of the group's token p + ahead0
-        const int last = pos_s[k1 - 1] / b.page_size;  // (their positions ascend)
-        if (pos_s[k1 - 1] < 0) continue;
-        const int32_t* bt = b.block_table + static_cast<int64_t>(s) * b.max_pages;
+        const int last = pos_s[k1 - 1] / b.page_size;
         for (int w0 = 0;; w0 += 32 * kWords) {
             const int words = min(kWords, (last - w0) / 32 + 1);
-            __syncthreads();                           // (the step before has read them)
+            // f(block, page, token) for the listed ones of these tokens in these words
+            auto each = [&](auto f) {
+#pragma unroll
+                for (int j = 0; j < kKeep; ++j)
+                    if (phys[j] >= 0 && token[j] >= k0 && token[j] < k1 && block[j] >= w0 && block[j] - w0 < 32 * words)
+                        f(block[j], phys[j], token[j]);
+                for (int i = max(k0 * width, kKeep * kThreads) + threadIdx.x; i < k1 * width; i += kThreads) {
+                    const int at = __ldg(lists + i), k = i / width;
+                    if (at < w0 || at - w0 >= 32 * words) {
+                        if (at >= b.max_pages) atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
+                        continue;
+                    }
+                    const int page = page_of(at, k);
+                    if (page >= 0) f(at, page, k);
+                }
+            };
+            __syncthreads();                           // (the step before has read the words)
             for (int i = threadIdx.x; i < words; i += kThreads) bits[i] = 0u;
             __syncthreads();
-            // Listed, at or before the token's own block, and with a page.
-            auto listed = [&](int i, int& block, int& k, int& phys) {
-                k = k0 + i / width;
-                block = __ldg(blocks + (static_cast<int64_t>(first) + k0) * width + i);
-                if (block >= b.max_pages && w0 == 0) atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
-                if (block < w0 || block - w0 >= 32 * words || pos_s[k] < 0 || block > pos_s[k] / b.page_size) return false;
-                phys = __ldg(bt + block);
-                if (phys < 0) return false;
-                if (static_cast<int64_t>(phys) * b.page_size >= num_slots) {
-                    atomicOr(b.err, MLA_ERR_DECODE_INDEX_RANGE);
-                    return false;
-                }
-                return true;
-            };
-            const int total = (k1 - k0) * width;
-            for (int i = threadIdx.x; i < total; i += kThreads) {
-                int block, k, phys;
-                if (listed(i, block, k, phys)) atomicOr(&bits[(block - w0) >> 5], 1u << (block & 31));
-            }
+            each([&](int at, int, int) { atomicOr(&bits[(at - w0) >> 5], 1u << (at & 31)); });
             __syncthreads();
             // Prefix counts: kPerThread words a thread.
             int mine = 0;
@@ -116,26 +147,19 @@ block_lists_kernel(const Batch b, const int32_t* __restrict__ blocks, int width,
                 const int w = threadIdx.x * kPerThread + j;
                 if (w >= words) break;
                 before[w] = at;
-                for (uint32_t left = bits[w]; left != 0u; left &= left - 1u) {
-                    const int block = w0 + 32 * w + __ffs(left) - 1;
-                    BlockEntry e;
-                    e.slot0 = __ldg(bt + block) * b.page_size;
-                    e.ahead = block * b.page_size + ahead0;
-                    e.tokens = k1 - k0 == 1 ? 1u << k0 : 0u;
-                    e.pad = 0;
-                    *reinterpret_cast<int4*>(out + at++) = *reinterpret_cast<const int4*>(&e);
-                }
+                at += __popc(bits[w]);
             }
             __syncthreads();
-            if (k1 - k0 > 1)
-                for (int i = threadIdx.x; i < total; i += kThreads) {
-                    int block, k, phys;
-                    if (listed(i, block, k, phys)) {
-                        const int w = (block - w0) >> 5;
-                        const int rank = before[w] + __popc(bits[w] & ((1u << (block & 31)) - 1u));
-                        atomicOr(&out[rank].tokens, 1u << k);
-                    }
-                }
+            // A block's entry is written by all who list it, alike; then each adds its token's bit.
+            auto rank = [&](int x) { return before[(x - w0) >> 5] + __popc(bits[(x - w0) >> 5] & ((1u << (x & 31)) - 1u)); };
+            const uint32_t alone = k1 - k0 == 1 ? 1u << k0 : 0u;
+            each([&](int x, int page, int) {
+                *reinterpret_cast<int4*>(out + rank(x)) = make_int4(page * b.page_size, x * b.page_size + ahead0, static_cast<int>(alone), 0);
+            });
+            if (alone == 0u) {
+                __syncthreads();
+                each([&](int x, int, int k) { atomicOr(&out[rank(x)].tokens, 1u << k); });
+            }
             count += found;
             if (last - w0 < 32 * kWords) break;
         }
