@@ -167,7 +167,7 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
         if (kWide) load(c * kChunk);
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
-            if (key[k] != 0u) {
+            if (c * kChunk + k * kThreads < n && key[k] != 0u) {
                 ones |= key[k];
                 zeros |= ~key[k];
             }
@@ -199,6 +199,7 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
             uint32_t packed = 0u;                          // ten bits each: at most 32 x kPer in a warp
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
+                if (c * kChunk + k * kThreads >= n) break;
                 const uint32_t d = ((key[k] ^ found) >> shift) - 1u;       // agrees above: -1 .. 2, the digit less 1
                 packed += d < 3u ? 1u << (10u * d) : 0u;
             }
