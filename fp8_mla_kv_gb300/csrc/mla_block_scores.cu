@@ -35,15 +35,15 @@ constexpr int kRows = 128;                                 // M
 constexpr int kCols = 256;                                 // columns a round: tensor memory of a CTA
 constexpr int kTileKeys = 128;                             // keys per ring tile
 constexpr int kTileBytes = 128 * 128;
-constexpr int kSlots = 3, kQSlots = 2;                      // two CTAs an SM
+constexpr int kSlots = 3, kQSlots = 3;                      // two CTAs an SM
 constexpr int kMaxCluster = 8;
 
 constexpr int kOffRing = 0;
 constexpr int kOffQ = kSlots * kTileBytes;
 constexpr int kStep = 16;                                  // columns that a softmax warp takes at a time
-constexpr int kTurn = 36;                                  // (16-byte reads of a column then meet no bank twice)
-constexpr int kOffTurn = kOffQ + kQSlots * kTileBytes;     // per softmax warp kStep columns x 32 rows
-constexpr int kOffJoin = kOffTurn + kSoftWarps * kStep * kTurn * 4;    // per softmax warp and column: parts of a token's sum
+constexpr int kOffTurn = kOffQ + (kQSlots - 1) * kTileBytes;       // per softmax warp kStep columns x 32 rows: where q's last slot is
+static_assert(kSoftWarps * kStep * 32 * 4 <= kTileBytes, "the turned scores have the place of a tile");
+constexpr int kOffJoin = kOffQ + kQSlots * kTileBytes;     // per softmax warp and column: parts of a token's sum
 constexpr int kOffMax = kOffJoin + kSoftWarps * kStep * 4; // per half of the softmax warps and row: maximum and sum, read by the cluster
 constexpr int kOffSeen = kOffMax + 2 * kRows * 8;          // per token: blocks that it sees
 constexpr int kOffOff = kOffSeen + kRows * 4;              // per kStep columns and row: the maximum that its exponentials go by
@@ -103,6 +103,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
            "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+
+// Where a role is in a ring: the slot and how often it has come round (the parity of a wait).
+struct Turn {
+    int slot = 0;
+    uint32_t parity = 0u;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
 
 // Dims x .. x + 63 of rows y .. y + 31.
 __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -192,6 +204,8 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     const int peers = (blocks + per - 1) / per;            // CTAs of the cluster with columns
     const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
     const int n_dims = a.d_qk / 64;
+    // With one round the copies are over when the scores are turned; with more, q does without its last slot.
+    const int q_slots = rounds == 1 ? kQSlots : kQSlots - 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
@@ -239,7 +253,8 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         const int id = threadIdx.x - 32 * kLoadWarp, x = id & 7, y = id >> 3;
         const int32_t* bt = a.b.block_table + static_cast<int64_t>(u.x) * a.b.max_pages + c0;
         const uint32_t ring = smem_u32(smem) + kOffRing + 128 * y + ((x ^ (y & 7)) << 4);      // (16 i leaves y & 7)
-        int issued = 0;                                    // tiles
+        Turn at;
+        at.parity = 1u;                                    // (a slot's first wait is over at once)
         for (int pass = 0; pass < passes; ++pass) {
             for (int r = 0; r < rounds && ok; ++r) {
                 const int n = min(kCols, cols - r * kCols);
@@ -264,16 +279,15 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     for (int t = 0; t < 2; ++t) {
                         const int rows = (n - kTileKeys * t + 15) & ~15;       // as many as the product takes
                         if (rows <= 0) break;
-                        const int slot = issued % kSlots;
-                        if (issued >= kSlots) ok = ok && warp_wait(&empty[slot], static_cast<uint32_t>((issued / kSlots - 1) & 1), abort_flag);
+                        ok = ok && warp_wait(&empty[at.slot], at.parity, abort_flag);
                         if (ok) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 if (y + 16 * i < rows)
-                                    copy16(ring + slot * kTileBytes + 2048 * i, src[t][i] + 64 * k, ((there >> (8 * t + i)) & 1u) != 0u);
-                            copies_arrive(&full[slot]);
+                                    copy16(ring + at.slot * kTileBytes + 2048 * i, src[t][i] + 64 * k, ((there >> (8 * t + i)) & 1u) != 0u);
+                            copies_arrive(&full[at.slot]);
                         }
-                        ++issued;
+                        at.next(kSlots);
                     }
                 }
             }
@@ -287,27 +301,30 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
             q_row = heads_warps == 1 ? (q.start + first + lane * per_warp) * a.H
                                      : (q.start + first + lane / heads_warps) * a.H + 32 * (lane % heads_warps);
         q_row = min(q_row, a.b.T * a.H - 1);               // (a box of none of the tile's tokens)
+        Turn at;
+        at.parity = 1u;
         int issued = 0;
         for (int pass = 0; pass < passes; ++pass) {
-            for (int i = 0; i < rounds * n_dims && ok; ++i, ++issued) {
-                const int slot = issued % kQSlots;
-                if (issued >= kQSlots) ok = warp_wait(&qempty[slot], static_cast<uint32_t>((issued / kQSlots - 1) & 1), abort_flag);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&qfull[slot], kTileBytes);
-                __syncwarp();
-                if (lane < 4)
-                    copy_box(smem + kOffQ + slot * kTileBytes + lane * (kTileBytes / 4), &q_map, 64 * (i % n_dims), q_row,
-                             &qfull[slot]);
-            }
+            for (int r = 0; r < rounds && ok; ++r)
+                for (int k = 0; k < n_dims && ok; ++k, ++issued) {
+                    ok = warp_wait(&qempty[at.slot], at.parity, abort_flag);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&qfull[at.slot], kTileBytes);
+                    __syncwarp();
+                    if (lane < 4)
+                        copy_box(smem + kOffQ + at.slot * kTileBytes + lane * (kTileBytes / 4), &q_map, 64 * k, q_row, &qfull[at.slot]);
+                    at.next(q_slots);
+                }
             if (pass == 0 && a.cluster > 1) cluster_sync();
         }
         // Copies in flight land before the CTA ends.
         if (!ok)
-            for (int i = max(0, issued - kQSlots); i < issued; ++i)
-                (void)mbar_wait_bounded(&qfull[i % kQSlots], static_cast<uint32_t>((i / kQSlots) & 1));
+            for (int i = max(0, issued - q_slots); i < issued; ++i)
+                (void)mbar_wait_bounded(&qfull[i % q_slots], static_cast<uint32_t>((i / q_slots) & 1));
     } else if (warp == kMmaWarp) {
         // ---- products, one elected thread ----
-        int at = 0, q_at = 0;                              // tiles so far (the elected thread is the same each time)
+        Turn at, q_at;                                     // (the elected thread is the same each time)
+        const uint32_t d_ring = smem_u32(smem) + kOffRing, d_q = smem_u32(smem) + kOffQ;
         for (int pass = 0; pass < passes; ++pass) {
             if (elect_one()) {
                 for (int r = 0; r < rounds && ok; ++r) {
@@ -315,25 +332,25 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     const int round = pass * rounds + r;
                     if (round > 0) ok = wait_or_abort(dfree, static_cast<uint32_t>((round - 1) & 1), abort_flag);
                     tc_after();
-                    for (int k = 0; k < n_dims && ok; ++k, ++q_at) {
-                        const int qs = q_at % kQSlots;
-                        ok = wait_or_abort(&qfull[qs], static_cast<uint32_t>((q_at / kQSlots) & 1), abort_flag);
-                        const uint64_t dq = sw128_desc(smem_u32(smem) + kOffQ + qs * kTileBytes);
-                        for (int t = 0; t < tiles && ok; ++t, ++at) {
-                            const int ks = at % kSlots;
-                            ok = wait_or_abort(&full[ks], static_cast<uint32_t>((at / kSlots) & 1), abort_flag);
+                    const uint32_t id0 = idesc((min(kTileKeys, n) + 15) & ~15), id1 = idesc((n - kTileKeys + 15) & ~15);
+                    for (int k = 0; k < n_dims && ok; ++k) {
+                        ok = wait_or_abort(&qfull[q_at.slot], q_at.parity, abort_flag);
+                        const uint64_t dq = sw128_desc(d_q + q_at.slot * kTileBytes);
+                        for (int t = 0; t < tiles && ok; ++t) {
+                            ok = wait_or_abort(&full[at.slot], at.parity, abort_flag);
                             if (!ok) break;
                             fence_proxy_async_smem();
                             tc_after();
-                            const uint64_t dk = sw128_desc(smem_u32(smem) + kOffRing + ks * kTileBytes);
-                            const uint32_t id = idesc((min(kTileKeys, n - kTileKeys * t) + 15) & ~15);
+                            const uint64_t dk = sw128_desc(d_ring + at.slot * kTileBytes);
 #pragma unroll
                             for (int s = 0; s < 4; ++s)
-                                umma(tmem + kTileKeys * t, dq + static_cast<uint64_t>(2 * s), dk + static_cast<uint64_t>(2 * s), id,
-                                     k > 0 || s > 0);
-                            umma_commit(&empty[ks]);
+                                umma(tmem + kTileKeys * t, dq + static_cast<uint64_t>(2 * s), dk + static_cast<uint64_t>(2 * s),
+                                     t == 0 ? id0 : id1, k > 0 || s > 0);
+                            umma_commit(&empty[at.slot]);
+                            at.next(kSlots);
                         }
-                        if (ok) umma_commit(&qempty[qs]);
+                        if (ok) umma_commit(&qempty[q_at.slot]);
+                        q_at.next(q_slots);
                     }
                     if (ok) umma_commit(dfull);
                 }
@@ -442,7 +459,10 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         // p = exp2(x - off) x f; with one round exp2(x - a maximum so far) is in tensor memory
         const float off = all_m == -INFINITY ? 0.0f : all_m;
         const float f = lives ? 1.0f / (all_l == 0.0f ? 1.0f : all_l) : 0.0f;
-        float* const mine = turn + warp * kStep * kTurn;
+        // Row r of column c at 16-byte unit r / 4 ^ c % 8 of the column: neither a column's rows nor eight columns' units
+        // meet a bank twice.
+        float* const mine = turn + warp * kStep * 32;
+        auto place = [&](int c, int r) -> float* { return mine + 32 * c + ((((r >> 2) ^ (c & 7)) << 2) | (r & 3)); };
         // What the lane sums and stores: column lane % kStep, and of the warp's tokens every other one, or half of the rows of one.
         const int col = lane & (kStep - 1), part = lane / kStep;
         for (int r = 0; r < rounds && ok; ++r) {
@@ -461,42 +481,41 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     tmem_ld16(lanes + kStep * j, v);
                     const float g = ex2_approx(off_s[j * kRows + row] - off) * f;      // (0 where nothing was seen so far)
 #pragma unroll
-                    for (int c = 0; c < kStep; ++c) mine[kTurn * c + lane] = lives ? __uint_as_float(v[c]) * g : 0.0f;
+                    for (int c = 0; c < kStep; ++c) *place(c, lane) = lives ? __uint_as_float(v[c]) * g : 0.0f;
                 } else {
                     float x[kStep];
                     load(r, j, x);
 #pragma unroll
-                    for (int c = 0; c < kStep; ++c) mine[kTurn * c + lane] = lives ? ex2_approx(x[c] - off) * f : 0.0f;
+                    for (int c = 0; c < kStep; ++c) *place(c, lane) = lives ? ex2_approx(x[c] - off) * f : 0.0f;
                 }
                 __syncwarp();
                 const int c = c0 + r * kCols + kStep * j + col, end = c0 + cols;
                 const bool has = ((keyed_step(j) >> col) & 1u) != 0u;
-                const float* const rows = mine + kTurn * col;
                 auto store = [&](int tok, float sum) {
                     if (c < min(seen_s[tok], end))
                         a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
                 };
-                auto sum16 = [&](const float* x) {
-                    const float4 v0 = *reinterpret_cast<const float4*>(x), v1 = *reinterpret_cast<const float4*>(x + 4);
-                    const float4 v2 = *reinterpret_cast<const float4*>(x + 8), v3 = *reinterpret_cast<const float4*>(x + 12);
+                auto sum16 = [&](int r) {
+                    const float4 v0 = *reinterpret_cast<const float4*>(place(col, r)), v1 = *reinterpret_cast<const float4*>(place(col, r + 4));
+                    const float4 v2 = *reinterpret_cast<const float4*>(place(col, r + 8)), v3 = *reinterpret_cast<const float4*>(place(col, r + 12));
                     return (((v0.x + v0.y) + (v0.z + v0.w)) + ((v1.x + v1.y) + (v1.z + v1.w))) +
                            (((v2.x + v2.y) + (v2.z + v2.w)) + ((v3.x + v3.y) + (v3.z + v3.w)));
                 };
                 if (a.H == 16) {
                     const int tok = 2 * quarter + part;
-                    const float sum = sum16(rows + 16 * part);
+                    const float sum = sum16(16 * part);
                     if (tok < n_tokens) store(tok, sum);
                 } else if (a.H < 32) {
                     for (int k = part; k < per_warp; k += 2) {
                         const int tok = quarter * per_warp + k;
                         if (tok >= n_tokens) break;
                         float sum = 0.0f;
-                        for (int h = 0; h < a.H; ++h) sum += rows[k * a.H + h];
+                        for (int h = 0; h < a.H; ++h) sum += *place(col, k * a.H + h);
                         store(tok, sum);
                     }
                 } else {
                     // a warp's part of one token's heads; lanes past the last head hold 0
-                    float sum = sum16(rows + 16 * part);
+                    float sum = sum16(16 * part);
                     sum += __shfl_xor_sync(0xffffffffu, sum, kStep);
                     const int tok = quarter / heads_warps;
                     if (heads_warps > 1) {
