@@ -228,20 +228,16 @@ __device__ __forceinline__ uint32_t swz(int rows, int r, int u) {
 
 // A bounded wait that also ends as soon as another role has given up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    // (the clock's upper bits are enough, in a register)
     if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
     const int t0 = static_cast<int>(clock64() >> 16);
 #pragma unroll 1
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (static_cast<int>(clock64() >> 16) - t0 > static_cast<int>(kWaitCycles >> 16)) {
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag != 0 || static_cast<int>(clock64() >> 16) - t0 > static_cast<int>(kWaitCycles >> 16)) {
             *abort_flag = 1;
             return false;
         }
     }
+    return true;
 }
 // The same by a whole warp, with one answer for it.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -289,6 +285,9 @@ __device__ __forceinline__ uint32_t zero_tiles(const uint8_t* row, uint32_t tile
     }
     return tiles;
 }
+
+// What an absent position is read as.
+__device__ __align__(16) uint8_t zero_row[kRowBytes];
 
 // A row's 16 bytes, zeros where the row is absent (slot < 0): a predicate, not a branch.
 __device__ __forceinline__ uint4 ld_row(const uint8_t* cache, int slot, uint32_t row_bytes, uint32_t off) {
@@ -757,21 +756,24 @@ mla_chunk_large_kernel(const ChunkArgs args) {
         const int r0 = 32 * quarter + 16 * hh + (lane >> 2);
         const uint32_t a_base = tmem + (static_cast<uint32_t>(32 * quarter + 16 * hh) << 16) + kColA;
         const uint32_t row_bytes = static_cast<uint32_t>(args.row_bytes);
-        int slot[2];
+        const uint8_t* row[2];                         // zeros where a position is absent
         uint4 v[4][2][2];                              // a block's codes; v[3] holds RoPE's values first
         bool ok = true;
         int g = 0;
         auto rows_of = [&](int b) {
             ok = ok && warp_wait(&mfull[b % kMeta], static_cast<uint32_t>((b / kMeta) & 1), abort_flag);
             if (!ok) return;
-            slot[0] = meta[b % kMeta].slot[r0];
-            slot[1] = meta[b % kMeta].slot[r0 + 8];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int slot = meta[b % kMeta].slot[r0 + 8 * e];
+                row[e] = (slot < 0 ? zero_row : args.cache + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * row_bytes) + 16 * c;
+            }
         };
         auto load = [&](uint4 (&x)[2][2], uint32_t off) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                x[e][0] = ld_row(args.cache, slot[e], row_bytes, off + 16 * c);
-                x[e][1] = ld_row(args.cache, slot[e], row_bytes, off + 16 * c + 64);
+                x[e][0] = ld_nc_v4(row[e] + off);
+                x[e][1] = ld_nc_v4(row[e] + off + 64);
             }
         };
         auto put = [&](const uint4 (&x)[2][2]) {       // the rows' bytes as they are: an A operand of QK
