@@ -65,6 +65,8 @@ _lib = None
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the shared library (raises OSError if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -159,10 +161,14 @@ def _require_cuda(*ts):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# The same for the current device, where CUDA is initialised.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -181,10 +187,11 @@ def _on(stream):
 def kv_cache(cache: torch.Tensor) -> KVCache:
     """View a uint8 [num_slots, 656] (or [num_slots, 528] NoPE-only) device tensor
     as the C cache descriptor."""
-    if (cache.dtype != torch.uint8 or cache.dim() != 2 or cache.shape[1] not in (ROW_BYTES, ROW_BYTES_NOPE)
+    shape = cache.shape
+    if (cache.dtype is not torch.uint8 or len(shape) != 2 or (shape[1] != ROW_BYTES and shape[1] != ROW_BYTES_NOPE)
             or not cache.is_contiguous()):
         raise ValueError("cache must be a contiguous uint8 tensor [num_slots, 656] or [num_slots, 528]")
-    return KVCache(cache.data_ptr(), cache.shape[0], int(cache.shape[1]))
+    return KVCache(cache.data_ptr(), shape[0], shape[1])
 
 
 def mla_kv_write(cache: torch.Tensor, slot_idx: torch.Tensor, latent: torch.Tensor,
@@ -349,7 +356,7 @@ def rope_spec(inv_freq, axis=None, interleaved: bool = False, scale: float = 1.0
 
 def _same_device(*ts) -> None:
     """Device tensors, all on the current device (whose stream and kernels the call uses)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    dev = _device() if torch.cuda.is_initialized() else -2
     for t in ts:
         if t is not None and t.get_device() != dev:
             _require_cuda(t)
@@ -475,17 +482,21 @@ def mla_chunk_attention(q: torch.Tensor, cache: torch.Tensor, q_start: torch.Ten
 
 
 def _ints(*ts) -> None:
+    i32 = torch.int32
     for t in ts:
         if t is not None:
-            assert t.dtype == torch.int32 and t.is_contiguous()
+            assert t.dtype is i32 and t.is_contiguous()
 
 
 def _batch(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor | None) -> int:
     """Checks a ragged batch's lengths and table; returns its number of sequences."""
-    _ints(q_start, kv_len, block_table)
-    n_seq = int(kv_len.numel())
-    assert q_start.numel() == n_seq + 1
-    assert block_table is None or (block_table.dim() == 2 and block_table.shape[0] == n_seq)
+    i32 = torch.int32
+    n_seq = kv_len.numel()
+    assert q_start.dtype is i32 and q_start.is_contiguous() and q_start.numel() == n_seq + 1
+    assert kv_len.dtype is i32 and kv_len.is_contiguous()
+    if block_table is not None:
+        assert block_table.dtype is i32 and block_table.is_contiguous()
+        assert block_table.dim() == 2 and block_table.shape[0] == n_seq
     return n_seq
 
 
@@ -495,10 +506,10 @@ def mla_block_keys(cache: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Ten
     that q_start counts. With q_start counting all of kv_len, the keys of every complete page."""
     _same_device(cache, q_start, kv_len, block_table, keys)
     n_seq = _batch(q_start, kv_len, block_table)
-    assert keys.dtype == torch.bfloat16 and keys.is_contiguous() and keys.dim() == 2
-    rc = load().mla_block_keys(kv_cache(cache), int(keys.shape[1]), q_start.data_ptr(), kv_len.data_ptr(),
-                               block_table.data_ptr(), n_seq, int(block_table.shape[1]), int(page_size), int(n_tokens),
-                               keys.data_ptr(), int(keys.shape[0]), _stream(stream))
+    assert keys.dtype is torch.bfloat16 and keys.is_contiguous() and keys.dim() == 2
+    rc = load().mla_block_keys(kv_cache(cache), keys.shape[1], q_start.data_ptr(), kv_len.data_ptr(),
+                               block_table.data_ptr(), n_seq, block_table.shape[1], int(page_size), int(n_tokens),
+                               keys.data_ptr(), keys.shape[0], _stream(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_block_keys")
     return keys
@@ -510,16 +521,16 @@ def mla_block_scores(q: torch.Tensor, keys: torch.Tensor, q_start: torch.Tensor,
     """scores fp32 [T, max_pages]: per token, summed over heads, the softmax of q . key over the complete blocks before its
     own. Other columns are left alone (without `scores`: -inf)."""
     _same_device(q, keys, q_start, kv_len, block_table, scores)
-    T, H, d_qk = (int(s) for s in q.shape)
+    T, H, d_qk = q.shape
     n_seq = _batch(q_start, kv_len, block_table)
-    assert q.dtype == torch.bfloat16 and q.is_contiguous()
-    assert keys.dtype == torch.bfloat16 and keys.is_contiguous() and keys.dim() == 2 and keys.shape[1] == d_qk
+    assert q.dtype is torch.bfloat16 and q.is_contiguous()
+    assert keys.dtype is torch.bfloat16 and keys.is_contiguous() and keys.dim() == 2 and keys.shape[1] == d_qk
     if scores is None:
         with _on(stream):
             scores = torch.full((T, block_table.shape[1]), float("-inf"), dtype=torch.float32, device=q.device)
-    assert scores.dtype == torch.float32 and scores.is_contiguous() and scores.shape == (T, block_table.shape[1])
-    rc = load().mla_block_scores(q.data_ptr(), T, H, d_qk, keys.data_ptr(), int(keys.shape[0]), q_start.data_ptr(),
-                                 kv_len.data_ptr(), block_table.data_ptr(), n_seq, int(block_table.shape[1]),
+    assert scores.dtype is torch.float32 and scores.is_contiguous() and scores.shape == (T, block_table.shape[1])
+    rc = load().mla_block_scores(q.data_ptr(), T, H, d_qk, keys.data_ptr(), keys.shape[0], q_start.data_ptr(),
+                                 kv_len.data_ptr(), block_table.data_ptr(), n_seq, block_table.shape[1],
                                  int(page_size), float(sm_scale), scores.data_ptr(), _stream(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_block_scores")
@@ -532,14 +543,14 @@ def mla_block_select(scores: torch.Tensor, q_start: torch.Tensor, kv_len: torch.
     scores [T, max_pages]; ascending, then -1 (without `blocks`, -1 for tokens outside every sequence)."""
     _same_device(scores, q_start, kv_len, blocks)
     n_seq = _batch(q_start, kv_len, None)
-    assert scores.dtype == torch.float32 and scores.is_contiguous() and scores.dim() == 2
-    T = int(scores.shape[0])
+    assert scores.dtype is torch.float32 and scores.is_contiguous() and scores.dim() == 2
+    T = scores.shape[0]
     if blocks is None:
         with _on(stream):
             blocks = torch.full((T, int(width)), -1, dtype=torch.int32, device=scores.device)
     _ints(blocks)
     assert blocks.shape == (T, int(width))
-    rc = load().mla_block_select(scores.data_ptr(), T, int(scores.shape[1]), q_start.data_ptr(), kv_len.data_ptr(), n_seq,
+    rc = load().mla_block_select(scores.data_ptr(), T, scores.shape[1], q_start.data_ptr(), kv_len.data_ptr(), n_seq,
                                  int(page_size), int(sink), int(local), int(width), blocks.data_ptr(), _stream(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_block_select")
@@ -563,19 +574,19 @@ def mla_block_attention(q: torch.Tensor, cache: torch.Tensor, blocks: torch.Tens
     [T, H, d_qk]. Returns (out bf16 [T, H, 512], lse fp32 [T, H]); without `out` and `lse`, tokens outside every sequence
     get 0 and -inf."""
     _same_device(q, cache, blocks, q_start, kv_len, block_table, out, lse, workspace)
-    T, H, d_qk = (int(s) for s in q.shape)
+    T, H, d_qk = q.shape
     n_seq = _batch(q_start, kv_len, block_table)
-    assert q.dtype == torch.bfloat16 and q.is_contiguous()
+    assert q.dtype is torch.bfloat16 and q.is_contiguous()
     _ints(blocks)
     assert blocks.dim() == 2 and blocks.shape[0] == T
-    width = int(blocks.shape[1])
+    width = blocks.shape[1]
     out, lse = _outputs(q, out, lse, stream)
     if workspace is None:
         with _on(stream):
             workspace = alloc_block_workspace(T, H, width, q.device)
     rc = load().mla_block_attention(q.data_ptr(), T, H, d_qk, kv_cache(cache), blocks.data_ptr(), width,
                                     q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), n_seq,
-                                    int(block_table.shape[1]), int(page_size), float(sm_scale), out.data_ptr(),
+                                    block_table.shape[1], int(page_size), float(sm_scale), out.data_ptr(),
                                     lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     _stream(stream))
     if rc != MLA_OK:
@@ -585,15 +596,15 @@ def mla_block_attention(q: torch.Tensor, cache: torch.Tensor, blocks: torch.Tens
 
 def _outputs(q: torch.Tensor, out: torch.Tensor | None, lse: torch.Tensor | None, stream):
     """out bf16 [T, H, 512] and lse fp32 [T, H] as given, or made: 0 and -inf."""
-    T, H = int(q.shape[0]), int(q.shape[1])
+    T, H = q.shape[:2]
     if out is None or lse is None:
         with _on(stream):
             if out is None:
                 out = torch.zeros((T, H, 512), dtype=torch.bfloat16, device=q.device)
             if lse is None:
                 lse = torch.full((T, H), float("-inf"), dtype=torch.float32, device=q.device)
-    assert out.dtype == torch.bfloat16 and out.is_contiguous() and out.numel() == T * H * 512
-    assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == T * H
+    assert out.dtype is torch.bfloat16 and out.is_contiguous() and out.numel() == T * H * 512
+    assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == T * H
     return out, lse
 
 
@@ -604,7 +615,7 @@ def mla_tree_mask(parent: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Ten
     each, where no mask is given (2 unless said)."""
     _same_device(parent, q_start, kv_len, mask, positions)
     n_seq = _batch(q_start, kv_len, None)
-    T = int(parent.numel())
+    T = parent.numel()
     if mask is None or positions is None:
         with _on(stream):
             if mask is None:
@@ -614,7 +625,7 @@ def mla_tree_mask(parent: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Ten
     _ints(parent, mask, positions)
     assert mask.dim() == 2 and mask.shape[0] == T and positions.numel() == T
     rc = load().mla_tree_mask(parent.data_ptr(), T, q_start.data_ptr(), kv_len.data_ptr(), n_seq, mask.data_ptr(),
-                              int(mask.shape[1]), positions.data_ptr(), _stream(stream))
+                              mask.shape[1], positions.data_ptr(), _stream(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_tree_mask")
     return mask, positions
@@ -627,9 +638,9 @@ def mla_tree_attention(q: torch.Tensor, cache: torch.Tensor, q_start: torch.Tens
     """mla_chunk_attention with a mask among the new tokens (int32 [T, words], as mla_tree_mask makes it). The workspace is
     alloc_chunk_workspace's."""
     _same_device(q, cache, q_start, kv_len, block_table, mask, out, lse, workspace)
-    T, H, d_qk = (int(s) for s in q.shape)
+    T, H, d_qk = q.shape
     n_seq = _batch(q_start, kv_len, block_table)
-    assert q.dtype == torch.bfloat16 and q.is_contiguous()
+    assert q.dtype is torch.bfloat16 and q.is_contiguous()
     _ints(mask)
     assert mask.dim() == 2 and mask.shape[0] == T
     out, lse = _outputs(q, out, lse, stream)
@@ -637,8 +648,8 @@ def mla_tree_attention(q: torch.Tensor, cache: torch.Tensor, q_start: torch.Tens
         with _on(stream):
             workspace = alloc_chunk_workspace(T, H, n_seq, q.device)
     rc = load().mla_tree_attention(q.data_ptr(), T, H, d_qk, kv_cache(cache), q_start.data_ptr(), kv_len.data_ptr(),
-                                   block_table.data_ptr(), n_seq, int(block_table.shape[1]), int(page_size),
-                                   mask.data_ptr(), int(mask.shape[1]), float(sm_scale), out.data_ptr(), lse.data_ptr(),
+                                   block_table.data_ptr(), n_seq, block_table.shape[1], int(page_size),
+                                   mask.data_ptr(), mask.shape[1], float(sm_scale), out.data_ptr(), lse.data_ptr(),
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_tree_attention")
@@ -656,8 +667,8 @@ def mla_tree_commit(cache: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Te
     assert path.dim() == 2 and path.shape[0] == n_seq and path_len.numel() == n_seq
     assert kv_len_out is None or kv_len_out.numel() == n_seq
     rc = load().mla_tree_commit(kv_cache(cache), q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), n_seq,
-                                int(block_table.shape[1]), int(page_size), path.data_ptr(), path_len.data_ptr(),
-                                int(path.shape[1]), kv_len_out.data_ptr() if kv_len_out is not None else None,
+                                block_table.shape[1], int(page_size), path.data_ptr(), path_len.data_ptr(),
+                                path.shape[1], kv_len_out.data_ptr() if kv_len_out is not None else None,
                                 _stream(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_tree_commit")
