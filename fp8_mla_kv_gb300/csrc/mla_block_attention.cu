@@ -300,6 +300,15 @@ extern "C" int mla_block_attention(const void* q_bf16, int T, int H, int d_qk, m
     a.group_tokens = z.group_tokens;
     a.group_tiles = z.group_tiles;
     a.nk = z.nk;
+    a.lists = blocks;
+    a.width = width;
+    a.heads = groups;
+    // Few rows and a token a tile: each CTA reads its token's list itself.
+    const bool alone = !z.large && z.group_tokens == 1 && width <= kListMax;
+    if (alone)
+        return mla_host::launch_chunk_small(a, kListed, z.tiles * z.nk, stream) &&
+                       (z.nk == 1 || mla_host::launch_chunk_merge(a, kBlocks, stream))
+                   ? MLA_OK : MLA_ECUDA;
     if (!mla_host::launch_pdl(block_lists_kernel, z.groups, kThreads, 0, stream, b, blocks, width, z.group_tokens,
                               kv.num_slots, entries, a.entry_cap, groups))
         return MLA_ECUDA;

@@ -35,6 +35,7 @@
 #include <cmath>
 
 #include "mla_chunk.cuh"
+#include "mla_seq.cuh"
 
 namespace {
 
@@ -55,6 +56,8 @@ constexpr int kSmemP = 4 * 32 * 8;                   // P (f16): uint2 [n-tile][
 constexpr int kSmemQmax = 3 * kWarps * kHeads * 4;   // |q| maxima, block score maxima, l partials
 constexpr int kSmemMisc = 2 * kStages * 8 + kStages * 4 + 16 + 16;   // barriers, present masks, poisoned rows, issued
 constexpr int kSmemTokens = kStages * kNB * 4;       // where a position has a mask of tokens
+constexpr int kSmemLists = kListMax * 8;             // where the CTA reads its token's list: slot and position of each block
+static_assert(kListMax * 4 + 16 <= kSmemStages, "the list's place");
 constexpr int kSmemTotal = kSmemStages + kSmemRed + kSmemP + kSmemQmax + kSmemMisc;
 constexpr float kLn2 = 0.6931471805599453f;
 // The exp2 offset puts the largest score at kTop (log2 units) and moves only when one is
@@ -398,6 +401,77 @@ __device__ __forceinline__ unsigned mend_part(uint8_t* st, int stride, int warp,
     return __ballot_sync(0xffffffffu, odd != 0u);
 }
 
+// kListed: the list of the CTA's token as blocks with a page, a slot (-1: nothing) and first position each, in
+// shared memory (the whole CTA). Lists as mla_block_select writes them ascend, so nothing is there twice; in others each
+// entry is compared with those before it. Returns the entries up to the last that lists something, -1 for a token
+// that is in no sequence.
+__device__ __forceinline__ int read_list(const ChunkArgs& a, int token, int2* entries, int* list, int& pos) {
+    constexpr int kOwn = (kListMax + kThreads - 1) / kThreads;
+    const Batch b = {a.q_start, a.kv_len, a.block_table, a.n_seq, a.max_pages, a.page_size, a.T, a.err};
+    int* const count = list + kListMax;
+    int block[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        block[j] = i < a.width ? __ldg(a.lists + static_cast<int64_t>(token) * a.width + i) : -1;
+    }
+    if (blockIdx.x == 0) check_lengths(b);
+    const int s = sequence_at(b, token, threadIdx.x & 31);
+    pos = -1;
+    if (s >= 0) {
+        const Sequence q = sequence_of(b, s);
+        pos = position_of(b, q, token - q.start);
+    }
+    const int own = pos < 0 ? -1 : pos / a.page_size;
+    if (threadIdx.x == 0) *count = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (s >= 0 && block[j] >= a.max_pages) atomicOr(a.err, MLA_ERR_DECODE_INDEX_RANGE);
+        if (block[j] > own) block[j] = -1;
+        if (i < a.width) list[i] = block[j];
+    }
+    __syncthreads();
+    bool odd = false;                                  // not above the entry before it
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (i > 0 && i < a.width && block[j] >= 0) odd = odd || block[j] <= list[i - 1] || list[i - 1] < 0;
+    }
+    odd = __syncthreads_or(odd) != 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (i >= a.width) break;
+        int slot = -1;
+        if (block[j] >= 0) {
+            bool again = false;
+            if (odd)
+                for (int k = 0; k < i; ++k) again = again || list[k] == block[j];
+            const int page = again ? -1 : __ldg(a.block_table + static_cast<int64_t>(s) * a.max_pages + block[j]);
+            if (page >= 0 && static_cast<int64_t>(page) * a.page_size >= a.num_slots) atomicOr(a.err, MLA_ERR_DECODE_INDEX_RANGE);
+            else if (page >= 0) slot = page * a.page_size;
+            if (slot >= 0) atomicMax(count, i + 1);
+        }
+        entries[i] = make_int2(slot, slot < 0 ? 0 : block[j] * a.page_size);
+    }
+    __syncthreads();
+    return s < 0 ? -1 : *count;
+}
+
+// Slot of position `at` of the list, counted through its entries, where the token (at `pos`) attends it.
+__device__ __forceinline__ int64_t list_slot(const ChunkArgs& a, const int2* entries, int at, int pos) {
+    const int e = at / a.page_size, off = at - e * a.page_size;
+    const int2 v = entries[e];
+    const int64_t slot = static_cast<int64_t>(v.x) + off;
+    if (v.x < 0 || slot == 0 || v.y + off > pos) return -1;
+    if (slot >= a.num_slots) {
+        atomicOr(a.err, MLA_ERR_DECODE_INDEX_RANGE);
+        return -1;
+    }
+    return slot;
+}
+
 template <bool kRopeOn, int kForm>
 __global__ void __launch_bounds__(kThreads, 2)
 mla_chunk_small_kernel(const ChunkArgs args) {
@@ -424,8 +498,20 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     pdl_wait();
     pdl_launch_dependents();
 
-    const Piece pc = piece_of<kForm>(args, blockIdx.x, lane);
-    if (pc.seq < 0) return;
+    int2* const entries_s = reinterpret_cast<int2*>(tokens_s);        // kListed
+    int own_pos = 0;
+    Piece pc;
+    if (kForm == kListed) {
+        const int tile = blockIdx.x / args.nk, token = tile / args.group_tiles;
+        const int count = read_list(args, token, entries_s, reinterpret_cast<int*>(stages), own_pos);
+        if (threadIdx.x == 0 && blockIdx.x - tile * args.nk == 0 && tile - token * args.group_tiles == 0)
+            args.heads[token] = make_int2(count, count >= 0 ? 1 : 0);
+        if (count < 0) return;
+        pc = block_piece(args, blockIdx.x, count);
+    } else {
+        pc = piece_of<kForm>(args, blockIdx.x, lane);
+        if (pc.seq < 0) return;
+    }
     const int k0 = pc.k0, n_keys = pc.k1 - pc.k0;
     const int n_rows = min(kHeads, pc.rows - pc.row0);
     const int nblk = (n_keys + kNB - 1) / kNB;
@@ -446,11 +532,12 @@ mla_chunk_small_kernel(const ChunkArgs args) {
         // finds the slot of position 32 b + j one block ahead of its copy ----
         const int pw = warp - kWarps;
         const int32_t* bt = args.block_table + static_cast<int64_t>(pc.seq) * args.max_pages;
-        const uint32_t all = kForm == kDense ? 0u : tile_tokens(args, pc, n_rows);
+        const uint32_t all = has_masks(kForm) ? tile_tokens(args, pc, n_rows) : 0u;
         uint32_t tokens = 0u, next_tokens = 0u;          // that attend the position, and the next block's
         auto look_up = [&](int b, uint32_t& attending) -> int64_t {
             attending = 0u;
             if (b >= nblk || b * kNB + lane >= n_keys) return -1;
+            if (kForm == kListed) return list_slot(args, entries_s, k0 + b * kNB + lane, own_pos);
             return kForm == kDense ? chunk_slot(args, bt, k0 + b * kNB + lane)
                                    : form_slot<kForm>(args, pc, bt, k0 + b * kNB + lane, n_rows, attending);
         };
@@ -477,8 +564,8 @@ mla_chunk_small_kernel(const ChunkArgs args) {
             const int64_t first = __shfl_sync(0xffffffffu, slot, 0);
             // All 32 rows side by side in the cache, and nothing but rows as staged: one copy.
             const bool run = __all_sync(0xffffffffu, present && slot == first + lane) && args.row_bytes == kRowRead;
-            const unsigned whole = kForm == kDense ? mask : mask & __ballot_sync(0xffffffffu, (tokens & all) == all);
-            if (kForm != kDense) {
+            const unsigned whole = has_masks(kForm) ? mask & __ballot_sync(0xffffffffu, (tokens & all) == all) : mask;
+            if (has_masks(kForm)) {
                 tokens_s[s * kNB + lane] = present ? tokens : 0u;
                 __syncwarp();
             }
@@ -514,7 +601,9 @@ mla_chunk_small_kernel(const ChunkArgs args) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) qraw[r][k] = 0u;
         if (row < pc.rows) {
-            lim[r] = kForm == kDense ? row_limit(args, pc, row) - k0 : static_cast<int>(token_bit(args, pc, row));
+            lim[r] = kForm == kListed  ? n_keys
+                     : kForm == kDense ? row_limit(args, pc, row) - k0
+                                       : static_cast<int>(token_bit(args, pc, row));
             const __nv_bfloat16* qh = args.q + (pc.grow0 + row) * args.d_qk;
             const uint8_t* p = reinterpret_cast<const uint8_t*>(qh + 128 * warp + 32 * c);
 #pragma unroll
@@ -729,11 +818,11 @@ mla_chunk_small_kernel(const ChunkArgs args) {
             a.x += bq.x; a.y += bq.y; a.z += bq.z; a.w += bq.w;
         }
         float sv[4] = {a.x * rowf[0], a.y * rowf[0], a.z * rowf[1], a.w * rowf[1]};
-        if ((~present | poison) != 0u || (kForm == kDense && kNB * (b + 1) > lim_all)) {
+        if ((~present | poison) != 0u || (!has_masks(kForm) && kNB * (b + 1) > lim_all)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = 8 * warp + 2 * c + (i & 1);
-                const bool attended = kForm == kDense ? ((present >> j) & 1u) != 0u && kNB * b + j < lim[i >> 1]
+                const bool attended = !has_masks(kForm) ? ((present >> j) & 1u) != 0u && kNB * b + j < lim[i >> 1]
                                                       : (tokens_s[s * kNB + j] & static_cast<uint32_t>(lim[i >> 1])) != 0u;
                 if (((poison >> j) & 1u) != 0u) sv[i] = __int_as_float(0x7FC00000);
                 if (!attended) sv[i] = -INFINITY;
@@ -1076,7 +1165,8 @@ bool launch_chunk_small(const ChunkArgs& a, Form form, int64_t pieces, void* str
     if (form == kDense) kernel = rope ? mla_chunk_small_kernel<true, kDense> : mla_chunk_small_kernel<false, kDense>;
     if (form == kTree) kernel = rope ? mla_chunk_small_kernel<true, kTree> : mla_chunk_small_kernel<false, kTree>;
     if (form == kBlocks) kernel = rope ? mla_chunk_small_kernel<true, kBlocks> : mla_chunk_small_kernel<false, kBlocks>;
-    const int smem = kSmemTotal + (form == kDense ? 0 : kSmemTokens);
+    if (form == kListed) kernel = rope ? mla_chunk_small_kernel<true, kListed> : mla_chunk_small_kernel<false, kListed>;
+    const int smem = kSmemTotal + (form == kListed ? kSmemLists : has_masks(form) ? kSmemTokens : 0);
     if (!max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
     return launch(kernel, pieces, kThreads, smem, stream, a);
 }

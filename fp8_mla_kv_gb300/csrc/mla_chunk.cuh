@@ -14,8 +14,11 @@ constexpr int kLargeBlock = 128;       // positions per block there
 
 // What a token attends: the positions up to its own, or all of them (a limit for each query row); the context before
 // the chunk and those of the chunk's tokens that its mask names; or the positions up to its own of the blocks
-// that are listed for it. The last two have a mask of the tile's tokens for each position.
-enum Form { kDense, kTree, kBlocks };
+// that are listed for it, in groups of tokens or (kListed) a token a tile, whose list the CTA reads itself. kTree and kBlocks
+// have a mask of the tile's tokens for each position.
+enum Form { kDense, kTree, kBlocks, kListed };
+constexpr bool has_masks(int form) { return form == kTree || form == kBlocks; }
+constexpr int kListMax = 512;          // entries of a list that a CTA reads itself
 
 // kBlocks: a block that tokens of a group list.
 struct __align__(16) BlockEntry {
@@ -60,6 +63,10 @@ struct ChunkArgs {
     const int2* groups;                // [groups]: number of entries; tokens that are in a sequence
     int entry_cap, group_tokens, group_tiles;      // group_tiles: tiles per group
     int nk;                            // pieces per tile
+    // kListed
+    const int32_t* lists;              // [T, width]
+    int width;
+    int2* heads;                       // groups, to be written
 };
 
 // A sequence's new tokens and context, as far as they are valid.
@@ -145,16 +152,16 @@ __device__ __forceinline__ int row_limit(const ChunkArgs& a, const Piece& p, int
     return token_limit(a, p.s, row / a.H);
 }
 
-// kBlocks: positions are counted through the group's entries, one block after the other. The pieces of a
+// kBlocks, kListed: positions are counted through the group's entries (`count`), one block after the other. The pieces of a
 // tile are equal parts of them.
-__device__ __forceinline__ Piece block_piece(const ChunkArgs& a, int b) {
+__device__ __forceinline__ Piece block_piece(const ChunkArgs& a, int b, int count) {
     Piece p;
     const int tile = b / a.nk, k = b - tile * a.nk;
     p.seq = tile / a.group_tiles;
     const int first = p.seq * a.group_tokens;
     p.s.start = first;
     p.s.n = min(a.group_tokens, a.T - first);
-    p.s.len = __ldg(&a.groups[p.seq].x) * a.page_size;
+    p.s.len = count * a.page_size;
     p.rows = p.s.n * a.H;
     p.row0 = (tile - p.seq * a.group_tiles) * a.tile_rows;
     p.grow0 = static_cast<int64_t>(first) * a.H;
@@ -162,14 +169,17 @@ __device__ __forceinline__ Piece block_piece(const ChunkArgs& a, int b) {
     p.k0 = static_cast<int>(min(static_cast<int64_t>(p.s.len), static_cast<int64_t>(k) * per));
     p.k1 = static_cast<int>(min(static_cast<int64_t>(p.s.len), static_cast<int64_t>(p.k0) + per));
     p.part = a.nk > 1 ? tile * a.nk + k : -1;
-    // (a tile past the group's rows is none: the last group may have fewer)
-    if (p.row0 >= p.rows || __ldg(&a.groups[p.seq].y) == 0) p.seq = -1;
     return p;
 }
 
 template <int kForm>
 __device__ __forceinline__ Piece piece_of(const ChunkArgs& a, int b, int lane) {
-    return kForm == kBlocks ? block_piece(a, b) : find_piece(a, b, lane);
+    if (kForm != kBlocks) return find_piece(a, b, lane);
+    const int2 head = __ldg(&a.groups[b / a.nk / a.group_tiles]);
+    Piece p = block_piece(a, b, head.x);
+    // (a tile past the group's rows is none: the last group may have fewer)
+    if (p.row0 >= p.rows || head.y == 0) p.seq = -1;
+    return p;
 }
 
 // A tile's tokens are numbered from 0: the one of query row `row`, as a bit.
