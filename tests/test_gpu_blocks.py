@@ -53,6 +53,14 @@ def test_keys_of_many_sequences():
     check_keys(B.batch([(1 + i % 3, 1 + i) for i in range(600)], 1, 576, 16, 656, seed=1), 576)
 
 
+@pytest.mark.parametrize("d_qk,row", [(576, 656), (512, 528)])
+def test_keys_of_many_pages(d_qk, row):
+    """More than a GPU's worth: several pages a CTA."""
+    b = B.batch([(9, 20), (2900, 2900), (0, 40), (2500, 2600), (1, 7)], 1, d_qk, 1, row, seed=6)
+    b["table"][1, 17] = -1
+    check_keys(b, d_qk)
+
+
 def test_keys_page_0_holes_and_pages_out_of_range():
     b = B.batch([(200, 200), (100, 250)], 1, 576, 16, 656, seed=2)
     b["table"][0, 3] = 0                                # the reserved slot is no row
