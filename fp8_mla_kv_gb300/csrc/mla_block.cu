@@ -12,7 +12,10 @@ using namespace mla;
 //
 // A CTA takes a page that a sequence's new tokens completed, a warp every eighth row: lane l values 16 l .. 16 l + 15
 // of the latent (tile l / 8) and, l < 8, RoPE values 8 l .. 8 l + 7, kAhead rows' loads on their way; sums in fp32, the
-// warps' joined in shared memory. Bound by the bytes of the rows where there are many: TIME_KEYS.
+// warps' joined in shared memory. 256 sequences that complete four pages take 4.1 us in a graph, a launch and the
+// chain of its loads; 20,000 tokens of four prompts (283 pages) 6.0 us; 1,048,576 rows 176 us, 4.0 TB/s, 0.59 of the
+// measured copy rate: the loads of a page's rows wait for its place, and each warp sums what it loaded before it loads
+// on. (Eight pages a CTA: 168 us, but the prompts' case 6.7.)
 constexpr int kKeyThreads = 256;
 constexpr int kKeyWarps = kKeyThreads / 32;
 constexpr int kAhead = 4;
@@ -113,10 +116,13 @@ block_keys_kernel(const Batch b, const uint8_t* __restrict__ cache, int64_t num_
 
 // ---- selection ----
 //
-// A score becomes a 32-bit key that orders like it (0: not to be chosen). The last one wanted is found two bits at a time from the top, by counting how many keys have each next digit; the keys
-// above it are taken, and of those equal to it the first ones. A CTA takes a token, with its keys in registers;
+// A score becomes a 32-bit key that orders like it (0: not to be chosen). The last one wanted is found two bits at a time from
+// the top, by counting how many keys have each next digit; the keys above it are taken, and of those equal to it the first ones. A CTA takes a token, with its keys in registers;
 // where there are more than fit, each pass reads the scores again (from L2).
-// Bound by the chain of passes (16 at most, it ends when a digit's keys are exactly those wanted): TIME_SELECT.
+// What it costs is the chain of passes (16 at most; it ends when a digit's keys are exactly those wanted, and bits in
+// which no two scores differ take none): 64 tokens of up to 2,048 blocks 7.3 us in a graph, 4,096 tokens of up to 256
+// blocks 12.3 us (1,500 instructions a token; a digit at a time with a count for each value 34 us, without leaving out
+// what does not differ 14.1, four tokens a CTA 15.6).
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (!(x > -INFINITY)) return 0u;                       // -inf or NaN: not chosen
     const uint32_t u = x == 0.0f ? 0u : __float_as_uint(x);       // (-0 is 0)

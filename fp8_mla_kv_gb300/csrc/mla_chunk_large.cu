@@ -35,12 +35,14 @@
 // left their place; each warp 16 positions), 16 issues QK, 17 and 18 walk the block table ahead
 // of them (slots, scales, sigma, prefetches into L2), 19 issues PV.
 //
-// 4,096 new tokens of 16 heads behind 12,288 positions: 2,960 us, 690 TFLOP/s, 0.36 of the
+// 4,096 new tokens of 16 heads behind 12,288 positions: 2,860 us, 713 TFLOP/s, 0.39 of the
 // measured dense bf16 rate. What bounds it: L1 and shared memory are busy 72 % of the time (V is written
 // there once and read by PV, q and P by the MMAs, the rows come through it), the issue slots
 // 53 %, the tensor pipe 31 %; and a block is a chain of about a dozen hand-offs between the roles,
 // 120 cycles each, which keeps these from overlapping further. 24 sequences of two tokens of 128 heads
-// and up to 16,384 positions: 247 us, of which starting and ending a piece take about 12 us each of three.
+// and up to 16,384 positions: 240 us, of which starting and ending a piece take about 12 us each of three. With masks (trees,
+// blocks) 8 trees of 60 tokens of 128 heads over up to 16,384 positions take 1,465 us, 625 TFLOP/s; 16 trees of up to 31 tokens
+// of 16 heads, NoPE, 106 us and with plan and merge 112.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -728,7 +730,7 @@ mla_chunk_large_kernel(const ChunkArgs args) {
                 const int dim = kTile * t + key;           // here the lane is a dim
                 if (pc.part < 0) {
                     // Two dims of a row a store: an even lane takes row c of a pair of rows, an odd one row c + 1. (A BF16
-                    // value a store took three times as long: TIME_EPI.)
+                    // value a store: 15,300 cycles instead of 7,700.)
                     const int odd = lane & 1;
                     __nv_bfloat16* to = args.out + (pc.grow0 + pc.row0 + c0 + odd) * kLatent + (dim - odd);
 #pragma unroll
