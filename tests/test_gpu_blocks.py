@@ -134,6 +134,15 @@ def test_scores_heads(H):
     check_scores(b, some_keys(b, 576))
 
 
+@pytest.mark.parametrize("d_qk", [512, 576])
+def test_scores_of_a_single_row(d_qk):
+    b = B.batch([(1, 20)], 1, d_qk, 1, 656, seed=2)     # fewer query rows than a copy takes
+    check_scores(b, some_keys(b, d_qk))
+    keys = some_keys(b, d_qk)[:1]                       # one key, and blocks past it
+    b["table"][0, :19] = 0
+    check_scores(b, keys)
+
+
 @pytest.mark.parametrize("n", [1, 20])
 @pytest.mark.parametrize("blocks", [127, 128, 129, 255, 257, 511, 512, 513, 1025, 2100, 4097, 5000])
 def test_scores_of_many_blocks(blocks, n):
