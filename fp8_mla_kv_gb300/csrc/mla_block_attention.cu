@@ -11,10 +11,11 @@
 // 4,096 tokens of 16 heads with 32 blocks of 64 of up to 256 each: 787 us, 366 TFLOP/s of the listed pairs (a group of four has
 // 49 blocks, of which each token lists two thirds; of the pairs that are multiplied it is 564). What bounds it is what
 // bounds the kernel for many rows, and 20,000 + 8,000 of a tile's 229,000 cycles are its start and end. 64 single tokens:
-// 36.8 us, 2.2 TB/s, bound as the kernel for few rows (256 pieces of 16 blocks for 304 places, the merge).
+// 33.8 us, 2.4 TB/s, bound as the kernel for few rows (256 pieces of 16 blocks of 32 positions for 304 places).
 //
-// Where a tile is one token's of few rows, its CTAs read the list themselves (read_list). Otherwise a first launch makes the
-// groups' lists (block_lists_kernel; for the 64 tokens it took 2 us more): a CTA per group marks the listed blocks in a bit
+// Where a tile is one token's of few rows, its CTAs, a cluster, read the list themselves (read_list) and join their parts
+// through their shared memory (join_parts). Otherwise a first launch makes the groups' lists (block_lists_kernel; with
+// it and the merge the 64 tokens took 38.7 us): a CTA per group marks the listed blocks in a bit
 // map, so that a block counts once however often and in whatever order it is listed, and ranks them by prefix counts.
 // The pieces of the tiles are planned on the host: it knows how long lists are at most. A captured call serves any
 // lengths and lists.
@@ -191,11 +192,11 @@ struct Sizes {
 
 // nk: the pieces per tile that make the least of waves x (positions of a piece + its cost); without positions, as many
 // as are ever taken.
-Sizes sizes_of(int T, int H, int width, int64_t positions, bool large, int sms) {
+Sizes sizes_of(int T, int H, int width, int64_t positions, bool large, bool alone, int sms) {
     Sizes z;
     z.large = large;
     z.tile_rows = large ? kLargeRows : kSmallRows;
-    z.group_tokens = H < z.tile_rows ? z.tile_rows / H : 1;
+    z.group_tokens = H < z.tile_rows && !alone ? z.tile_rows / H : 1;
     if (z.group_tokens > 32) z.group_tokens = 32;      // a bit each
     z.group_tiles = (H + z.tile_rows - 1) / z.tile_rows;
     z.groups = (static_cast<int64_t>(T) + z.group_tokens - 1) / z.group_tokens;
@@ -235,7 +236,7 @@ extern "C" size_t mla_block_attention_workspace_bytes(int T, int H, int width) {
     // whatever the page size: the most pieces, of either kernel
     size_t most = 0;
     for (const bool large : {false, true}) {
-        const Sizes z = sizes_of(T, H, width, -1, large, sms);
+        const Sizes z = sizes_of(T, H, width, -1, large, false, sms);
         if (z.total() > most) most = z.total();
     }
     return most;
@@ -264,7 +265,14 @@ extern "C" int mla_block_attention(const void* q_bf16, int T, int H, int d_qk, m
     const int sms = mla_host::sm_count();
     b.err = mla_host::device_error_word();
     if (b.err == nullptr || sms <= 0) return MLA_ECUDA;
-    const Sizes z = sizes_of(T, H, width, positions, takes_large(T, H, n_seq, positions), sms);
+    // Few rows, and tokens that share a tile with none (16 heads and more) or with none of their own sequence (mostly
+    // single tokens): each CTA reads its token's list itself, and the pieces of a tile, a cluster, join it. (In groups: 64
+    // tokens of 16 heads 38.7 instead of 33.8 us, 8 of 5 heads 25.3 instead of 15.5, 64 of one head 86 instead of 29, but 200 of
+    // 8 heads 75 instead of 86.)
+    const bool large = takes_large(T, H, n_seq, positions);
+    const bool alone = !large && width <= kListMax && static_cast<int64_t>(width) * page_size <= INT_MAX - 4096 &&
+                       (H >= kSmallRows || T < 2 * static_cast<int64_t>(n_seq));
+    const Sizes z = sizes_of(T, H, width, positions, large, alone, sms);
     if (positions * z.group_tokens > INT_MAX - 4096 || z.tiles * z.nk > INT_MAX ||
         static_cast<int64_t>(z.group_tokens) * width > INT_MAX)
         return MLA_EUNSUPPORTED;
@@ -309,13 +317,10 @@ extern "C" int mla_block_attention(const void* q_bf16, int T, int H, int d_qk, m
     a.nk = z.nk;
     a.lists = blocks;
     a.width = width;
-    a.heads = groups;
-    // Few rows and a token a tile: each CTA reads its token's list itself.
-    const bool alone = !z.large && z.group_tokens == 1 && width <= kListMax;
-    if (alone)
-        return mla_host::launch_chunk_small(a, kListed, z.tiles * z.nk, stream) &&
-                       (z.nk == 1 || mla_host::launch_chunk_merge(a, kBlocks, stream))
-                   ? MLA_OK : MLA_ECUDA;
+    if (alone) {
+        a.nk = z.nk < kListPieces ? z.nk : kListPieces;
+        return mla_host::launch_chunk_small(a, kListed, z.tiles * a.nk, stream) ? MLA_OK : MLA_ECUDA;
+    }
     if (!mla_host::launch_pdl(block_lists_kernel, z.groups, kThreads, 0, stream, b, blocks, width, z.group_tokens,
                               kv.num_slots, entries, a.entry_cap, groups))
         return MLA_ECUDA;

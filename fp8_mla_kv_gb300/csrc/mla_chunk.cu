@@ -472,6 +472,67 @@ __device__ __forceinline__ int64_t list_slot(const ChunkArgs& a, const int2* ent
     return slot;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, int rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float peer_float(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_float4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// kListed: a tile's outputs from its pieces' parts in the shared memory of the cluster, in piece order, as
+// mla_chunk_merge_kernel joins them. A part is kHeads rows of kPartRow values; an lse of +inf says that its CTA failed.
+constexpr int kPartRow = kLatent + 4;                  // (rows 4 words apart modulo the banks)
+static_assert((kHeads * kPartRow + kHeads) * 4 <= kSmemStages, "a part has the place of the rows");
+
+__device__ __forceinline__ void join_parts(const ChunkArgs& a, const Piece& p, uint32_t part, uint32_t part_lse, int n_rows) {
+    const int rank = static_cast<int>(blockIdx.x) % a.nk;
+    for (int u = rank * kConsumerThreads + threadIdx.x; u < n_rows * (kLatent / 4); u += a.nk * kConsumerThreads) {
+        const int row = u / (kLatent / 4), dim = u % (kLatent / 4) * 4;
+        float ls[kListPieces];
+        float4 v[kListPieces];
+        float mx = -INFINITY;
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < kListPieces; ++k) {
+            ls[k] = -INFINITY;
+            if (k < a.nk) {
+                ls[k] = peer_float(peer_address(part_lse + 4 * row, k));
+                v[k] = peer_float4(peer_address(part + 4 * (row * kPartRow + dim), k));
+            }
+            mx = fmaxf(mx, ls[k]);
+            nan = nan || ls[k] != ls[k];
+        }
+        if (mx == INFINITY) return;
+        float sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kListPieces; ++k)
+            if (ls[k] != -INFINITY) {                  // (a piece with nothing attended has no part in it)
+                const float w = expf(ls[k] - mx);
+                sum += w;
+                acc = make_float4(fmaf(w, v[k].x, acc.x), fmaf(w, v[k].y, acc.y), fmaf(w, v[k].z, acc.z), fmaf(w, v[k].w, acc.w));
+            }
+        float lse = mx + logf(sum), inv = 1.0f / sum;
+        if (mx == -INFINITY) { lse = -INFINITY; inv = 0.0f; }
+        if (nan) lse = inv = __int_as_float(0x7FC00000);
+        *reinterpret_cast<uint2*>(a.out + (p.grow0 + p.row0 + row) * kLatent + dim) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (dim == 0) a.lse[p.grow0 + p.row0 + row] = lse;
+    }
+}
+
 template <bool kRopeOn, int kForm>
 __global__ void __launch_bounds__(kThreads, 2)
 mla_chunk_small_kernel(const ChunkArgs args) {
@@ -504,9 +565,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     if (kForm == kListed) {
         const int tile = blockIdx.x / args.nk, token = tile / args.group_tiles;
         const int count = read_list(args, token, entries_s, reinterpret_cast<int*>(stages), own_pos);
-        if (threadIdx.x == 0 && blockIdx.x - tile * args.nk == 0 && tile - token * args.group_tiles == 0)
-            args.heads[token] = make_int2(count, count >= 0 ? 1 : 0);
-        if (count < 0) return;
+        if (count < 0) return;                           // (all CTAs of the cluster)
         pc = block_piece(args, blockIdx.x, count);
     } else {
         pc = piece_of<kForm>(args, blockIdx.x, lane);
@@ -932,7 +991,8 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     }
 
     __syncthreads();     // all warps: producers done issuing, consumers done reading
-    if (failed || issued_s[0] + issued_s[1] < nblk) {
+    const bool lost = failed || issued_s[0] + issued_s[1] < nblk;
+    if (lost) {
         // A wait ran out: record it, let the copies already issued land (bounded)
         // and leave without touching the outputs.
         if (threadIdx.x == 0) {
@@ -945,7 +1005,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
                 }
             }
         }
-        return;
+        if (kForm != kListed || args.nk == 1) return;
     }
 
     // ---- epilogue: l over the four warps' positions, then O * sigma / l ----
@@ -966,6 +1026,33 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     // l = 0: nothing attended (out 0, lse -inf). l NaN: an attended row holds a value
     // that is not finite (out and lse NaN).
     const float kNaN = __int_as_float(0x7FC00000);
+    if (kForm == kListed && args.nk > 1) {
+        // The pieces' CTAs are a cluster: each leaves its part in its own shared memory, where the rows were, and joins
+        // every nk-th four dims of all of them.
+        float* const part = reinterpret_cast<float*>(stages);
+        float* const part_lse = part + kHeads * kPartRow;
+        if (lost) {
+            if (threadIdx.x < kHeads) part_lse[threadIdx.x] = INFINITY;      // no lse: the tile gets no outputs
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float mm = lt[r] > 0.0f ? sigma / lt[r] : (lt[r] == 0.0f ? 0.0f : kNaN);
+                if (warp == 0 && c == 0)
+                    part_lse[g + 8 * r] = lt[r] > 0.0f ? (m_ref[r] + log2f(lt[r])) * kLn2 : (lt[r] == 0.0f ? -INFINITY : kNaN);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int qd = 0; qd < 4; ++qd)
+                        *reinterpret_cast<float4*>(part + (g + 8 * r) * kPartRow + 128 * warp + 32 * c + 16 * e + 4 * qd) =
+                            make_float4(o[4 * qd + 0][2 * r + e] * mm, o[4 * qd + 1][2 * r + e] * mm,
+                                        o[4 * qd + 2][2 * r + e] * mm, o[4 * qd + 3][2 * r + e] * mm);
+            }
+        }
+        cluster_sync();
+        join_parts(args, pc, smem_u32(part), smem_u32(part_lse), n_rows);
+        cluster_sync();                                // the others have read this CTA's part
+        return;
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int row = pc.row0 + g + 8 * r;
@@ -1130,7 +1217,7 @@ int attend(Form form, const void* q_bf16, int T, int H, int d_qk, mla_kv_cache_t
         *p = reinterpret_cast<int32_t*>(w);
         w += z.prefix;
     }
-    if (!launch(chunk_plan_kernel, 1, kPlanThreads, 0, stream, a)) return MLA_ECUDA;
+    if (!launch(chunk_plan_kernel, 1, kPlanThreads, 0, stream, 1, a)) return MLA_ECUDA;
     const bool ok = z.large ? mla_host::launch_chunk_large(a, form, z.max_pieces, stream)
                             : mla_host::launch_chunk_small(a, form, z.max_pieces, stream);
     return ok && mla_host::launch_chunk_merge(a, form, stream) ? MLA_OK : MLA_ECUDA;
@@ -1168,7 +1255,7 @@ bool launch_chunk_small(const ChunkArgs& a, Form form, int64_t pieces, void* str
     if (form == kListed) kernel = rope ? mla_chunk_small_kernel<true, kListed> : mla_chunk_small_kernel<false, kListed>;
     const int smem = kSmemTotal + (form == kListed ? kSmemLists : has_masks(form) ? kSmemTokens : 0);
     if (!max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
-    return launch(kernel, pieces, kThreads, smem, stream, a);
+    return launch(kernel, pieces, kThreads, smem, stream, form == kListed ? a.nk : 1, a);
 }
 
 bool launch_chunk_merge(const ChunkArgs& a, Form form, void* stream) {
@@ -1177,9 +1264,9 @@ bool launch_chunk_merge(const ChunkArgs& a, Form form, void* stream) {
     const int64_t ctas = (rows + kMergeWarps - 1) / kMergeWarps;
     if (rows <= held)
         return launch(form == kBlocks ? mla_chunk_merge_kernel<4, kBlocks> : mla_chunk_merge_kernel<4, kDense>, rows,
-                      32 * kMergeWarps, 0, stream, a);
+                      32 * kMergeWarps, 0, stream, 1, a);
     return launch(form == kBlocks ? mla_chunk_merge_kernel<1, kBlocks> : mla_chunk_merge_kernel<1, kDense>,
-                  ctas < held ? ctas : held, 32 * kMergeWarps, 0, stream, a);
+                  ctas < held ? ctas : held, 32 * kMergeWarps, 0, stream, 1, a);
 }
 
 }  // namespace mla_host

@@ -19,6 +19,7 @@ constexpr int kLargeBlock = 128;       // positions per block there
 enum Form { kDense, kTree, kBlocks, kListed };
 constexpr bool has_masks(int form) { return form == kTree || form == kBlocks; }
 constexpr int kListMax = 512;          // entries of a list that a CTA reads itself
+constexpr int kListPieces = 8;         // pieces of such a token's tile, at most: a cluster
 
 // kBlocks: a block that tokens of a group list.
 struct __align__(16) BlockEntry {
@@ -66,7 +67,6 @@ struct ChunkArgs {
     // kListed
     const int32_t* lists;              // [T, width]
     int width;
-    int2* heads;                       // groups, to be written
 };
 
 // A sequence's new tokens and context, as far as they are valid.
@@ -244,17 +244,20 @@ __device__ __forceinline__ int64_t form_slot(const ChunkArgs& a, const Piece& p,
 }
 
 template <typename K, typename... A>
-bool launch(K kernel, int64_t grid, int threads, size_t smem, void* stream, A... args) {
+bool launch(K kernel, int64_t grid, int threads, size_t smem, void* stream, int cluster, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
 }
 

@@ -1051,7 +1051,7 @@ bool launch_chunk_large(const mla_chunk::ChunkArgs& a, mla_chunk::Form form, int
     if (form == kBlocks) kernel = rope ? mla_chunk_large_kernel<true, kBlocks> : mla_chunk_large_kernel<false, kBlocks>;
     const int smem = form == kDense ? kSmemTotal<kDense> : kSmemTotal<kBlocks>;
     if (!max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
-    return launch(kernel, pieces, kThreads, smem, stream, a);
+    return launch(kernel, pieces, kThreads, smem, stream, 1, a);
 }
 
 }  // namespace mla_host
