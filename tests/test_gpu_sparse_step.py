@@ -262,3 +262,39 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
     assert M.mla_get_error() == 0
     for p, q in zip(got, want[0]):
         assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+@pytest.mark.parametrize("start", [[0, 9, 5, 20], [4, 2, 0, -3], [0, 30, 10, 25], [-5, 6, 12, 20], [3, 3, 99, 20], [20, 20, 20, 20]], ids=str)
+@pytest.mark.parametrize("many", [False, True])
+def test_starts_out_of_order_are_flagged_and_nothing_else_is_touched(start, many):
+    b = B.batch([(5, 60), (7, 90), (8, 33)], 16, 576, 16, 656, seed=1, extra=20000 if many else 2)
+    t = {k: v.to(D) if isinstance(v, torch.Tensor) else v for k, v in b.items()}
+    T, width = 20, 20000 if many else 6
+    w = (ints(start), t["kv_len"], t["table"], 16)
+    flagged = start != [20, 20, 20, 20]
+
+    def guarded(shape, dtype):
+        flat = torch.zeros(64 + math.prod(shape) + 64, dtype=dtype, device=D)
+        return flat, flat[64:-64].view(shape)
+
+    keep = []
+    for make in (lambda: M.mla_block_keys(t["cache"], *w, one((b["pages"], 576), torch.bfloat16), T),
+                 lambda: M.mla_block_scores(t["q"], torch.zeros((b["pages"], 576), dtype=torch.bfloat16, device=D), *w, 0.04,
+                                            scores=one((T, b["table"].shape[1]), torch.float32)),
+                 lambda: M.mla_block_select(torch.zeros((T, b["table"].shape[1]), device=D), *w[:2], 16, 6, blocks=one((T, 6), torch.int32)),
+                 lambda: M.mla_block_attention(t["q"], t["cache"], torch.zeros((T, width), dtype=torch.int32, device=D), *w, 0.04,
+                                               out=one((T, 16, 512), torch.bfloat16), lse=one((T, 16), torch.float32)),
+                 lambda: M.mla_tree_mask(torch.full((T,), -1, dtype=torch.int32, device=D), *w[:2], mask=one((T, 1), torch.int32),
+                                         positions=one((T,), torch.int32)),
+                 lambda: M.mla_tree_attention(t["q"], t["cache"], *w, 0.04, torch.zeros((T, 1), dtype=torch.int32, device=D),
+                                              out=one((T, 16, 512), torch.bfloat16), lse=one((T, 16), torch.float32)),
+                 lambda: M.mla_tree_commit(t["cache"].clone(), *w, torch.zeros((3, 2), dtype=torch.int32, device=D), ints([0, 0, 0]))):
+        def one(shape, dtype):
+            flat, view = guarded(shape, dtype)
+            keep.append(flat)
+            return view
+        make()
+        torch.cuda.synchronize()
+        assert (M.mla_get_error() & M.MLA_ERR_CHUNK_RANGE != 0) == flagged
+    for flat in keep:
+        assert (flat[:64] == 0).all() and (flat[-64:] == 0).all()
