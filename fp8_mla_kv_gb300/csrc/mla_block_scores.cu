@@ -147,6 +147,19 @@ __device__ __forceinline__ float2 peer_float2(uint32_t saddr, int rank) {
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
     return v;
 }
+__device__ __forceinline__ void put_shared(uint32_t at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" :: "r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ float get_shared(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 get_shared4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
 // One thread of the warp; ptxas knows that it is one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -467,10 +480,13 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         const float f = lives ? 1.0f / (all_l == 0.0f ? 1.0f : all_l) : 0.0f;
         // Row r of column c at 16-byte unit r / 4 ^ c % 8 of the column: neither a column's rows nor eight columns' units
         // meet a bank twice.
-        float* const mine = turn + warp * kStep * 32;
-        auto place = [&](int c, int r) -> float* { return mine + 32 * c + ((((r >> 2) ^ (c & 7)) << 2) | (r & 3)); };
+        const uint32_t mine = smem_u32(turn) + warp * kStep * 128;     // (a multiple of 1,024: bits 4 .. 6 are the unit's)
         // What the lane sums and stores: column lane % kStep, and of the warp's tokens every other one, or half of the rows of one.
         const int col = lane & (kStep - 1), part = lane / kStep;
+        const uint32_t put = mine + 4 * lane, get = mine + 128 * col + ((col & 7) << 4);
+        const int my_token = a.H <= 16 ? quarter * per_warp + part : quarter / heads_warps;     // (16 heads, or 32 and more)
+        const int my_end = my_token < n_tokens ? min(seen_s[my_token], c0 + cols) - (c0 + col) : 0;
+        float* const my_scores = a.scores + (static_cast<int64_t>(q.start) + first + my_token) * a.b.max_pages + c0 + col;
         for (int r = 0; r < rounds && ok; ++r) {
             if (rounds > 1) {
                 keyed = keyed_columns(r);
@@ -487,43 +503,41 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     tmem_ld16(lanes + kStep * j, v);
                     const float g = ex2_approx(off_s[j * kRows + row] - off) * f;      // (0 where nothing was seen so far)
 #pragma unroll
-                    for (int c = 0; c < kStep; ++c) *place(c, lane) = lives ? __uint_as_float(v[c]) * g : 0.0f;
+                    for (int c = 0; c < kStep; ++c)
+                        put_shared((put ^ ((c & 7) << 4)) + 128 * c, lives ? __uint_as_float(v[c]) * g : 0.0f);
                 } else {
                     float x[kStep];
                     load(r, j, x);
 #pragma unroll
-                    for (int c = 0; c < kStep; ++c) *place(c, lane) = lives ? ex2_approx(x[c] - off) * f : 0.0f;
+                    for (int c = 0; c < kStep; ++c)
+                        put_shared((put ^ ((c & 7) << 4)) + 128 * c, lives ? ex2_approx(x[c] - off) * f : 0.0f);
                 }
                 __syncwarp();
-                const int c = c0 + r * kCols + kStep * j + col, end = c0 + cols;
+                const int at = r * kCols + kStep * j;          // column at + col of this CTA's
                 const bool has = ((keyed_step(j) >> col) & 1u) != 0u;
-                auto store = [&](int tok, float sum) {
-                    if (c < min(seen_s[tok], end))
-                        a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
-                };
-                auto sum16 = [&](int r) {
-                    const float4 v0 = *reinterpret_cast<const float4*>(place(col, r)), v1 = *reinterpret_cast<const float4*>(place(col, r + 4));
-                    const float4 v2 = *reinterpret_cast<const float4*>(place(col, r + 8)), v3 = *reinterpret_cast<const float4*>(place(col, r + 12));
+                auto sum16 = [&](int r) {                      // rows r .. r + 15
+                    const uint32_t from = get ^ (r << 2);
+                    const float4 v0 = get_shared4(from), v1 = get_shared4(from ^ 16), v2 = get_shared4(from ^ 32), v3 = get_shared4(from ^ 48);
                     return (((v0.x + v0.y) + (v0.z + v0.w)) + ((v1.x + v1.y) + (v1.z + v1.w))) +
                            (((v2.x + v2.y) + (v2.z + v2.w)) + ((v3.x + v3.y) + (v3.z + v3.w)));
                 };
                 if (a.H == 16) {
-                    const int tok = 2 * quarter + part;
                     const float sum = sum16(16 * part);
-                    if (tok < n_tokens) store(tok, sum);
+                    if (at < my_end) my_scores[at] = has ? sum : -INFINITY;
                 } else if (a.H < 32) {
                     for (int k = part; k < per_warp; k += 2) {
                         const int tok = quarter * per_warp + k;
                         if (tok >= n_tokens) break;
                         float sum = 0.0f;
-                        for (int h = 0; h < a.H; ++h) sum += *place(col, k * a.H + h);
-                        store(tok, sum);
+                        for (int h = k * a.H; h < (k + 1) * a.H; ++h) sum += get_shared((get ^ ((h >> 2) << 4)) + 4 * (h & 3));
+                        const int c = c0 + at + col;
+                        if (c < min(seen_s[tok], c0 + cols))
+                            a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
                     }
                 } else {
                     // a warp's part of one token's heads; lanes past the last head hold 0
                     float sum = sum16(16 * part);
                     sum += __shfl_xor_sync(0xffffffffu, sum, kStep);
-                    const int tok = quarter / heads_warps;
                     if (heads_warps > 1) {
                         if (part == 0) join[kStep * warp + col] = sum;
                         bar_sync_or(2 + half, 128, false);
@@ -531,7 +545,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                             for (int w = 1; w < heads_warps; ++w) sum += join[kStep * (warp + w) + col];
                         bar_sync_or(2 + half, 128, false);
                     }
-                    if (quarter % heads_warps == 0 && part == 0 && tok < n_tokens) store(tok, sum);
+                    if (quarter % heads_warps == 0 && part == 0 && at < my_end) my_scores[at] = has ? sum : -INFINITY;
                 }
                 __syncwarp();
             }
