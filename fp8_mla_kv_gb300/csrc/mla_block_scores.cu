@@ -15,10 +15,10 @@
 // says, by 16 bytes a thread and time (cp.async): TMA's gather of four rows took 41,000 cycles for what boxes take 15,000.
 // Both in 128-byte-swizzled tiles of 128 rows through a ring each, for each 64 dims one of q and up to two of keys.
 //
-// 4,096 tokens of 16 heads with up to 255 blocks: 39.8 us; 32 tokens of 128 heads with up to 1,024: 18.3 us. In both a CTA
-// takes about 31,000 cycles, one after the other: 5,000 until the first operands are asked for, 16,000 of products
+// 4,096 tokens of 16 heads with up to 255 blocks: 38.1 us; 32 tokens of 128 heads with up to 1,024: 18.3 us. In both a CTA
+// takes 26,000 to 31,000 cycles, one after the other: 5,000 until the first operands are asked for, 10,000 to 16,000 of products
 // (the first: shared memory, 96 KB a step of 64 dims and CTA with two CTAs an SM; the second: memory, as each step asks
-// for 128 bytes of every row), 10,000 of softmax, exchange and sums, and the first case has 512 tiles for 304 places.
+// for 128 bytes of every row), 9,000 to 11,000 of softmax, exchange and sums, and the first case has 512 tiles for 304 places.
 // Keys by TMA gather 135 us, copies that fence each tile 97, four softmax warps 80; q and keys prefetched into L2 by
 // rows: no faster.
 #include <algorithm>
@@ -41,20 +41,20 @@ constexpr int kRows = 128;                                 // M
 constexpr int kCols = 256;                                 // columns a round: tensor memory of a CTA
 constexpr int kTileKeys = 128;                             // keys per ring tile
 constexpr int kTileBytes = 128 * 128;
-constexpr int kSlots = 3, kQSlots = 3;                      // two CTAs an SM
+constexpr int kSlots = 6;                                  // of both rings: two CTAs an SM
+constexpr int kMostKeySlots = 4, kMostQSlots = 3;
 constexpr int kMaxCluster = 8;
 
 constexpr int kOffRing = 0;
-constexpr int kOffQ = kSlots * kTileBytes;
 constexpr int kStep = 16;                                  // columns that a softmax warp takes at a time
-constexpr int kOffTurn = kOffQ + (kQSlots - 1) * kTileBytes;       // per softmax warp kStep columns x 32 rows: where q's last slot is
+constexpr int kOffTurn = kOffRing + (kSlots - 1) * kTileBytes;     // per softmax warp kStep columns x 32 rows: where the last slot is
 static_assert(kSoftWarps * kStep * 32 * 4 <= kTileBytes, "the turned scores have the place of a tile");
-constexpr int kOffJoin = kOffQ + kQSlots * kTileBytes;     // per softmax warp and column: parts of a token's sum
+constexpr int kOffJoin = kOffRing + kSlots * kTileBytes;   // per softmax warp and column: parts of a token's sum
 constexpr int kOffMax = kOffJoin + kSoftWarps * kStep * 4; // per half of the softmax warps and row: maximum and sum, read by the cluster
 constexpr int kOffSeen = kOffMax + 2 * kRows * 8;          // per token: blocks that it sees
 constexpr int kOffOff = kOffSeen + kRows * 4;              // per kStep columns and row: the maximum that its exponentials go by
 constexpr int kOffBars = kOffOff + (kCols / kStep) * kRows * 4;
-constexpr int kNumBars = 2 * kSlots + 2 * kQSlots + 3;
+constexpr int kNumBars = 2 * kMostKeySlots + 2 * kMostQSlots + 3;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
 constexpr int kSmem = kOffMisc + 16;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -191,11 +191,11 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     float2* const max_s = reinterpret_cast<float2*>(smem + kOffMax);             // [2][kRows]
     int* const seen_s = reinterpret_cast<int*>(smem + kOffSeen);
     float* const off_s = reinterpret_cast<float*>(smem + kOffOff);              // [kCols / kStep][kRows]
-    uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kOffBars);        // [kSlots] a tile copied
-    uint64_t* const empty = full + kSlots;                                      // [kSlots] its products are done
-    uint64_t* const qfull = empty + kSlots;                                     // [kQSlots] the same for q
-    uint64_t* const qempty = qfull + kQSlots;
-    uint64_t* const dfull = qempty + kQSlots;                                   // a round's products are done
+    uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kOffBars);        // [kMostKeySlots] a tile copied
+    uint64_t* const empty = full + kMostKeySlots;                               // [kMostKeySlots] its products are done
+    uint64_t* const qfull = empty + kMostKeySlots;                              // [kMostQSlots] the same for q
+    uint64_t* const qempty = qfull + kMostQSlots;
+    uint64_t* const dfull = qempty + kMostQSlots;                               // a round's products are done
     uint64_t* const dfree = dfull + 1;                                          // and have been read
     uint64_t* const fin = dfree + 1;                                            // all products are done
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -223,15 +223,17 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     const int peers = (blocks + per - 1) / per;            // CTAs of the cluster with columns
     const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
     const int n_dims = a.d_qk / 64;
-    // With one round the copies are over when the scores are turned; with more, q does without its last slot.
-    const int q_slots = rounds == 1 ? kQSlots : kQSlots - 1;
+    // The rings hold two steps of 64 dims with two tiles of keys each, or three with one. With one round the copies are over when the
+    // scores are turned; with more, the last slot is kept free for that.
+    const int key_slots = cols > kTileKeys && rounds == 1 ? 4 : 3, q_slots = rounds == 1 ? kSlots - key_slots : 2;
+    const int q_off = kOffRing + key_slots * kTileBytes;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kMostKeySlots; ++i) {
             mbar_init(&full[i], 32 * kLoadWarps);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < kQSlots; ++i) {
+        for (int i = 0; i < kMostQSlots; ++i) {
             mbar_init(&qfull[i], 1);
             mbar_init(&qempty[i], 1);
         }
@@ -306,7 +308,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                                     copy16(ring + at.slot * kTileBytes + 2048 * i, src[t][i] + 64 * k, ((there >> (8 * t + i)) & 1u) != 0u);
                             copies_arrive(&full[at.slot]);
                         }
-                        at.next(kSlots);
+                        at.next(key_slots);
                     }
                 }
             }
@@ -331,7 +333,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     if (lane == 0) mbar_arrive_expect_tx(&qfull[at.slot], kTileBytes);
                     __syncwarp();
                     if (lane < 4)
-                        copy_box(smem + kOffQ + at.slot * kTileBytes + lane * (kTileBytes / 4), &q_map, 64 * k, q_row, &qfull[at.slot]);
+                        copy_box(smem + q_off + at.slot * kTileBytes + lane * (kTileBytes / 4), &q_map, 64 * k, q_row, &qfull[at.slot]);
                     at.next(q_slots);
                 }
             if (pass == 0 && a.cluster > 1) cluster_sync();
@@ -343,7 +345,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     } else if (warp == kMmaWarp) {
         // ---- products, one elected thread ----
         Turn at, q_at;                                     // (the elected thread is the same each time)
-        const uint32_t d_ring = smem_u32(smem) + kOffRing, d_q = smem_u32(smem) + kOffQ;
+        const uint32_t d_ring = smem_u32(smem) + kOffRing, d_q = smem_u32(smem) + q_off;
         for (int pass = 0; pass < passes; ++pass) {
             if (elect_one()) {
                 for (int r = 0; r < rounds && ok; ++r) {
@@ -366,7 +368,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                                 umma(tmem + kTileKeys * t, dq + static_cast<uint64_t>(2 * s), dk + static_cast<uint64_t>(2 * s),
                                      t == 0 ? id0 : id1, k > 0 || s > 0);
                             umma_commit(&empty[at.slot]);
-                            at.next(kSlots);
+                            at.next(key_slots);
                         }
                         if (ok) umma_commit(&qempty[q_at.slot]);
                         q_at.next(q_slots);
