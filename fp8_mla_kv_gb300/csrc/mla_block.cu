@@ -116,17 +116,93 @@ block_keys_kernel(const Batch b, const uint8_t* __restrict__ cache, int64_t num_
 
 // ---- selection ----
 //
-// A score becomes a 32-bit key that orders like it (0: not to be chosen). The last one wanted is found two bits at a time from
-// the top, by counting how many keys have each next digit; the keys above it are taken, and of those equal to it the first ones. A CTA takes a token, with its keys in registers;
-// where there are more than fit, each pass reads the scores again (from L2).
-// What it costs is the chain of passes (16 at most; it ends when a digit's keys are exactly those wanted, and bits in
-// which no two scores differ take none): 64 tokens of up to 2,048 blocks 7.3 us in a graph, 4,096 tokens of up to 256
-// blocks 12.3 us (1,500 instructions a token; a digit at a time with a count for each value 34 us, without leaving out
-// what does not differ 14.1, four tokens a CTA 15.6).
+// A score becomes a 32-bit key that orders like it (0: not to be chosen). The last one wanted is found a digit at a time from
+// the top, by counting the keys; those above it are taken, and of those equal to it the first ones. The passes over the keys, which are in
+// registers, end when a digit's keys are exactly those wanted, and bits in which no two scores differ take none: exponents are near
+// each other, and rounded scores end in zeros.
+// Up to 512 blocks a warp takes a token, a bit a pass: 4,096 tokens of up to 256 blocks 10.2 us in a graph, of which a warp
+// is there for half: 6,000 cycles until its keys are ready, 5,000 of passes, 600 until its list is written (two bits a pass
+// 12.3 us, a digit at a time with a count for each value 34; halving the range of the keys 14.9, as scores that are equal take it
+// to the last bit; two to eight tokens a CTA 11.9). With more blocks a CTA does, two bits a pass, as a pass has a barrier:
+// 64 tokens of up to 2,048 blocks 7.3 us, a chain of passes. Beyond 8,192 each pass reads the scores again (from L2).
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (!(x > -INFINITY)) return 0u;                       // -inf or NaN: not chosen
     const uint32_t u = x == 0.0f ? 0u : __float_as_uint(x);       // (-0 is 0)
     return (u >> 31) != 0u ? ~u : u | 0x80000000u;
+}
+
+// A token of up to 32 x kPer blocks. A pass counts the keys that are not below the threshold with the next bit set.
+template <int kPer>
+__global__ void __launch_bounds__(32)
+block_select_warp_kernel(const Batch b, const float* __restrict__ scores, int columns, int sink, int local, int width,
+                         int32_t* __restrict__ blocks) {
+    const int lane = threadIdx.x;
+    const int t = blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (t == 0) check_lengths(b);
+    const int s = sequence_at(b, t, lane);
+    if (s < 0) return;
+    const Sequence q = sequence_of(b, s);
+    const int pos = position_of(b, q, t - q.start);
+    int32_t* const out = blocks + static_cast<int64_t>(t) * width;
+    const int n = pos < 0 ? 0 : pos / b.page_size + 1;     // blocks up to the token's own
+    const float* const row = scores + static_cast<int64_t>(t) * columns;
+    uint32_t key[kPer], ones = 0u, zeros = 0u;             // set in any score's key, clear in any
+    int there = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = 32 * k + lane;
+        const bool always = i < n && (i < sink || i > n - 1 - local);
+        key[k] = i < n && !always ? order_key(__ldg(row + i)) : 0u;
+        ones |= key[k];
+        zeros |= key[k] != 0u ? ~key[k] : 0u;
+        key[k] = always ? ~0u : key[k];                    // above all scores' keys
+        there += key[k] != 0u ? 1 : 0;
+    }
+    there = __reduce_add_sync(0xffffffffu, there);
+    uint32_t found = 1u;                                   // keys from here on are taken,
+    int equal = 0;                                         // or, if above 0, those above and so many of those equal to it
+    if (there > width) {
+        ones = __reduce_or_sync(0xffffffffu, ones);
+        uint32_t differ = ones & __reduce_or_sync(0xffffffffu, zeros);     // bits in which two differ: the others need no pass
+        found = ones & ~differ;                            // (from here on there are more than wanted)
+        equal = width - sink - local;                      // (there are more blocks than wanted: the two are apart)
+        if (equal == 0) found = ~0u;
+#pragma unroll 1
+        while (differ != 0u && equal != 0) {
+            const uint32_t bit = 0x80000000u >> __clz(differ), mid = found | bit;
+            differ ^= bit;
+            int c = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) c += key[k] >= mid ? 1 : 0;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (c >= width) found = mid;                   // (else the bit is clear)
+            if (c <= width) equal = width - c;
+        }
+    }
+    // In ascending order; of equal ones the first.
+    const uint32_t lower = (1u << lane) - 1u;
+    int placed = 0;
+    if (equal == 0) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const unsigned taken = __ballot_sync(0xffffffffu, key[k] >= found);
+            if (key[k] >= found) out[placed + __popc(taken & lower)] = 32 * k + lane;
+            placed += __popc(taken);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const unsigned same = __ballot_sync(0xffffffffu, key[k] == found);
+            const bool take = key[k] > found || (key[k] == found && __popc(same & lower) < equal);
+            const unsigned taken = __ballot_sync(0xffffffffu, take);
+            if (take) out[placed + __popc(taken & lower)] = 32 * k + lane;
+            placed += __popc(taken);
+            equal = max(0, equal - __popc(same));
+        }
+    }
+    for (int i = placed + lane; i < width; i += 32) out[i] = -1;
 }
 
 // kWarps warps with kPer keys a thread hold a token's keys; kWide: more are read again for each pass.
@@ -180,15 +256,13 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
     }
     ones = __reduce_or_sync(0xffffffffu, ones);
     zeros = __reduce_or_sync(0xffffffffu, zeros);
-    if (kWarps > 1) {
-        if (lane == 0) {
-            counts[1][warp][0] = ones;
-            counts[1][warp][1] = zeros;
-        }
-        __syncthreads();
-        ones = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][0] : 0u);
-        zeros = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][1] : 0u);
+    if (lane == 0) {
+        counts[1][warp][0] = ones;
+        counts[1][warp][1] = zeros;
     }
+    __syncthreads();
+    ones = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][0] : 0u);
+    zeros = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][1] : 0u);
     const uint32_t differ = ones & zeros;
     int turn = 0;
 #pragma unroll 1
@@ -214,17 +288,15 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
             c2 += (packed >> 10) & 1023u;
             c3 += packed >> 20;
         }
-        if (kWarps > 1) {
-            if (lane == 0) {
-                counts[turn][warp][0] = c1;
-                counts[turn][warp][1] = c2;
-                counts[turn][warp][2] = c3;
-            }
-            __syncthreads();
-            c1 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][0] : 0);
-            c2 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][1] : 0);
-            c3 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][2] : 0);
+        if (lane == 0) {
+            counts[turn][warp][0] = c1;
+            counts[turn][warp][1] = c2;
+            counts[turn][warp][2] = c3;
         }
+        __syncthreads();
+        c1 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][0] : 0);
+        c2 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][1] : 0);
+        c3 = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[turn][lane][2] : 0);
         uint32_t digit = 3u;
         int here = c3;
         if (left > here) { left -= here; here = c2; digit = 2u; }
@@ -241,27 +313,21 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
         if (kWide) load(c * kChunk);
-        if (kWarps > 1) {
-            __syncthreads();                               // (the chunk before has been placed)
+        __syncthreads();                                   // (the chunk before has been placed)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const unsigned a = __ballot_sync(0xffffffffu, above(key[k], c * kChunk + k * kThreads + threadIdx.x)), e = __ballot_sync(0xffffffffu, equal(key[k]));
-                if (lane == 0) place[k][warp] = __popc(a) | __popc(e) << 16;
-            }
-            __syncthreads();
+        for (int k = 0; k < kPer; ++k) {
+            const unsigned a = __ballot_sync(0xffffffffu, above(key[k], c * kChunk + k * kThreads + threadIdx.x)), e = __ballot_sync(0xffffffffu, equal(key[k]));
+            if (lane == 0) place[k][warp] = __popc(a) | __popc(e) << 16;
         }
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             if (c * kChunk + k * kThreads >= n) break;
             const int i = c * kChunk + k * kThreads + threadIdx.x;
             const bool a = above(key[k], i), e = equal(key[k]);
             const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
-            int total = __popc(am) | __popc(em) << 16, before = 0;
-            if (kWarps > 1) {
-                const int mine = lane < kWarps ? place[k][lane] : 0;
-                total = __reduce_add_sync(0xffffffffu, mine);
-                before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
-            }
+            const int mine = lane < kWarps ? place[k][lane] : 0;
+            const int total = __reduce_add_sync(0xffffffffu, mine), before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
             const int e_rank = n_equal + (before >> 16) + __popc(em & lower);
             if (a || (e && e_rank < left))
                 out[n_above + (before & 0xffff) + __popc(am & lower) + min(e_rank, left)] = i;
@@ -311,8 +377,8 @@ extern "C" int mla_block_select(const float* scores, int T, int columns, const i
     if (b.err == nullptr) return MLA_ECUDA;
     void (*kernel)(const Batch, const float*, int, int, int, int, int32_t*) = block_select_kernel<32, 8, true>;
     int warps = 32;
-    if (columns <= 256) { kernel = block_select_kernel<1, 8, false>; warps = 1; }
-    else if (columns <= 512) { kernel = block_select_kernel<1, 16, false>; warps = 1; }
+    if (columns <= 256) { kernel = block_select_warp_kernel<8>; warps = 1; }
+    else if (columns <= 512) { kernel = block_select_warp_kernel<16>; warps = 1; }
     else if (columns <= 1024) { kernel = block_select_kernel<4, 8, false>; warps = 4; }
     else if (columns <= 4096) { kernel = block_select_kernel<16, 8, false>; warps = 16; }
     else if (columns <= 8192) { kernel = block_select_kernel<32, 8, false>; warps = 32; }

@@ -230,6 +230,24 @@ def test_select_from_many(blocks):
         check_select(b, some_scores(b, blocks, ties), width, 0, 1)
 
 
+@pytest.mark.parametrize("width,sink,local", [(1, 0, 1), (2, 0, 1), (7, 3, 4), (31, 1, 2), (64, 0, 1), (200, 7, 9)])
+@pytest.mark.parametrize("blocks", [31, 32, 33, 256, 511, 512, 513])
+def test_select_close_scores(blocks, width, sink, local):
+    """Scores that differ in their last bits, in their sign, or not at all; most of them absent."""
+    b = B.batch([(6, blocks), (1, 5), (4, blocks)], 1, 512, 1, 528, seed=blocks + width, extra=0)
+    g = torch.Generator().manual_seed(blocks)
+    sc = torch.randint(0, 3, (b["T"], b["table"].shape[1]), generator=g).float()
+    last = (torch.tensor([1.0]).view(torch.int32) + sc.int()).view(torch.float32)       # 1 and the two values after it
+    sc[0] = last[0]
+    sc[1] = -last[1]
+    sc[2] = 1.0
+    sc[3] = (sc[3] - 1.0) * 3.4028234663852886e38
+    sc[4, torch.rand(sc.shape[1], generator=g) < 0.8] = -math.inf
+    sc[8, torch.rand(sc.shape[1], generator=g) < 0.95] = -math.inf
+    sc[9] = last[9] * 2.0 ** torch.randint(-60, 60, sc.shape[1:], generator=g)
+    check_select(b, sc, width, sink, local)
+
+
 def test_select_special_values():
     b = B.batch([(6, 600)], 1, 512, 4, 528, seed=10)
     sc = some_scores(b, 3)
