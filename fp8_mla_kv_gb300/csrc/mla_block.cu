@@ -120,10 +120,10 @@ block_keys_kernel(const Batch b, const uint8_t* __restrict__ cache, int64_t num_
 // the top, by counting the keys; those above it are taken, and of those equal to it the first ones. The passes over the keys, which are in
 // registers, end when a digit's keys are exactly those wanted, and bits in which no two scores differ take none: exponents are near
 // each other, and rounded scores end in zeros.
-// Up to 512 blocks a warp takes a token, a bit a pass: 4,096 tokens of up to 256 blocks 10.2 us in a graph, of which a warp
-// is there for half: 6,000 cycles until its keys are ready, 5,000 of passes, 600 until its list is written (two bits a pass
-// 12.3 us, a digit at a time with a count for each value 34; halving the range of the keys 14.9, as scores that are equal take it
-// to the last bit; two to eight tokens a CTA 11.9). With more blocks a CTA does, two bits a pass, as a pass has a barrier:
+// Up to 512 blocks a warp takes a token, a bit a pass, with no more registers of keys than the token has blocks for: 4,096 tokens
+// of up to 256 blocks of a table of 258 take 7.2 us in a graph, bound by instructions. (Keys for the whole table 10.2 us, so two to
+// eight tokens a CTA 11.9, two bits a pass 12.3, halving the range of the keys, which equal scores take to the last bit, 14.9, a
+// count for each value of a digit 34.) With more blocks a CTA does, two bits a pass, as a pass has a barrier:
 // 64 tokens of up to 2,048 blocks 7.3 us, a chain of passes. Beyond 8,192 each pass reads the scores again (from L2).
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (!(x > -INFINITY)) return 0u;                       // -inf or NaN: not chosen
@@ -131,23 +131,10 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u >> 31) != 0u ? ~u : u | 0x80000000u;
 }
 
-// A token of up to 32 x kPer blocks. A pass counts the keys that are not below the threshold with the next bit set.
+// The list of a token with n blocks, at most 32 x kPer. A pass counts the keys that are not below the threshold with the next bit set.
 template <int kPer>
-__global__ void __launch_bounds__(32)
-block_select_warp_kernel(const Batch b, const float* __restrict__ scores, int columns, int sink, int local, int width,
-                         int32_t* __restrict__ blocks) {
-    const int lane = threadIdx.x;
-    const int t = blockIdx.x;
-    pdl_wait();
-    pdl_launch_dependents();
-    if (t == 0) check_lengths(b);
-    const int s = sequence_at(b, t, lane);
-    if (s < 0) return;
-    const Sequence q = sequence_of(b, s);
-    const int pos = position_of(b, q, t - q.start);
-    int32_t* const out = blocks + static_cast<int64_t>(t) * width;
-    const int n = pos < 0 ? 0 : pos / b.page_size + 1;     // blocks up to the token's own
-    const float* const row = scores + static_cast<int64_t>(t) * columns;
+__device__ __forceinline__ void select_in_warp(const float* __restrict__ row, int n, int sink, int local, int width, int lane,
+                                               int32_t* __restrict__ out) {
     uint32_t key[kPer], ones = 0u, zeros = 0u;             // set in any score's key, clear in any
     int there = 0;
 #pragma unroll
@@ -203,6 +190,28 @@ block_select_warp_kernel(const Batch b, const float* __restrict__ scores, int co
         }
     }
     for (int i = placed + lane; i < width; i += 32) out[i] = -1;
+}
+
+constexpr int kWarpBlocks = 512;
+
+__global__ void __launch_bounds__(32)
+block_select_warp_kernel(const Batch b, const float* __restrict__ scores, int columns, int sink, int local, int width,
+                         int32_t* __restrict__ blocks) {
+    const int lane = threadIdx.x;
+    const int t = blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (t == 0) check_lengths(b);
+    const int s = sequence_at(b, t, lane);
+    if (s < 0) return;
+    const Sequence q = sequence_of(b, s);
+    const int pos = position_of(b, q, t - q.start);
+    int32_t* const out = blocks + static_cast<int64_t>(t) * width;
+    const int n = pos < 0 ? 0 : pos / b.page_size + 1;     // blocks up to the token's own
+    const float* const row = scores + static_cast<int64_t>(t) * columns;
+    if (n <= 128) select_in_warp<4>(row, n, sink, local, width, lane, out);
+    else if (n <= 256) select_in_warp<8>(row, n, sink, local, width, lane, out);
+    else select_in_warp<kWarpBlocks / 32>(row, n, sink, local, width, lane, out);
 }
 
 // kWarps warps with kPer keys a thread hold a token's keys; kWide: more are read again for each pass.
@@ -377,8 +386,7 @@ extern "C" int mla_block_select(const float* scores, int T, int columns, const i
     if (b.err == nullptr) return MLA_ECUDA;
     void (*kernel)(const Batch, const float*, int, int, int, int, int32_t*) = block_select_kernel<32, 8, true>;
     int warps = 32;
-    if (columns <= 256) { kernel = block_select_warp_kernel<8>; warps = 1; }
-    else if (columns <= 512) { kernel = block_select_warp_kernel<16>; warps = 1; }
+    if (columns <= kWarpBlocks) { kernel = block_select_warp_kernel; warps = 1; }
     else if (columns <= 1024) { kernel = block_select_kernel<4, 8, false>; warps = 4; }
     else if (columns <= 4096) { kernel = block_select_kernel<16, 8, false>; warps = 16; }
     else if (columns <= 8192) { kernel = block_select_kernel<32, 8, false>; warps = 32; }
