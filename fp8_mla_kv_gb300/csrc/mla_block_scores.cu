@@ -49,8 +49,8 @@ constexpr int kOffRing = 0;
 constexpr int kStep = 16;                                  // columns that a softmax warp takes at a time
 constexpr int kOffTurn = kOffRing + (kSlots - 1) * kTileBytes;     // per softmax warp kStep columns x 32 rows: where the last slot is
 static_assert(kSoftWarps * kStep * 32 * 4 <= kTileBytes, "the turned scores have the place of a tile");
-constexpr int kOffJoin = kOffRing + kSlots * kTileBytes;   // per softmax warp and column: parts of a token's sum
-constexpr int kOffMax = kOffJoin + kSoftWarps * kStep * 4; // per half of the softmax warps and row: maximum and sum, read by the cluster
+constexpr int kOffJoin = kOffRing + kSlots * kTileBytes;   // per lane quarter and column: parts of a token's sum
+constexpr int kOffMax = kOffJoin + 4 * kCols * 4;          // per half of the softmax warps and row: maximum and sum, read by the cluster
 constexpr int kOffSeen = kOffMax + 2 * kRows * 8;          // per token: blocks that it sees
 constexpr int kOffOff = kOffSeen + kRows * 4;              // per kStep columns and row: the maximum that its exponentials go by
 constexpr int kOffBars = kOffOff + (kCols / kStep) * kRows * 4;
@@ -183,6 +183,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
 }
 
+// kSixteen: two tokens a warp, as whose rows the sums run without a look at the heads; kFew: fewer than 32 heads; kMany: 32 and more.
+enum Heads { kSixteen, kFew, kMany };
+
+template <int kHeads>
 __global__ void __launch_bounds__(kThreads, 2)
 block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -255,18 +259,19 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     bool ok = *abort_flag == 0;
 
     // Row r of the tile: lane r % 32 of warp r / 32. Tokens of at most 32 heads stand side by side in a warp.
-    const int heads_warps = a.H <= 32 ? 1 : a.H <= 64 ? 2 : 4;         // warps of a token
-    const int per_warp = a.H <= 32 ? 32 / a.H : 1;                     // tokens of a warp
+    const int H = kHeads == kSixteen ? 16 : a.H;
+    const int heads_warps = kHeads != kMany || H <= 32 ? 1 : H <= 64 ? 2 : 4;      // warps of a token
+    const int per_warp = kHeads != kMany ? 32 / H : 1;                 // tokens of a warp
     auto row_of = [&](int r, int& token, int& head) {                  // false: an empty lane
         const int w = r >> 5, l = r & 31;
         if (heads_warps == 1) {
-            token = w * per_warp + l / a.H;
-            head = l % a.H;
-            return l < per_warp * a.H && token < n_tokens;
+            token = w * per_warp + l / H;
+            head = l % H;
+            return l < per_warp * H && token < n_tokens;
         }
         token = w / heads_warps;
         head = (w % heads_warps) * 32 + l;
-        return head < a.H && token < n_tokens;
+        return head < H && token < n_tokens;
     };
 
     if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
@@ -319,9 +324,9 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         // ---- q: lane l < 4 the box of lane quarter l ----
         int q_row = 0;
         if (lane < 4)
-            q_row = heads_warps == 1 ? (q.start + first + lane * per_warp) * a.H
-                                     : (q.start + first + lane / heads_warps) * a.H + 32 * (lane % heads_warps);
-        q_row = min(q_row, a.b.T * a.H - 1);               // (a box of none of the tile's tokens)
+            q_row = heads_warps == 1 ? (q.start + first + lane * per_warp) * H
+                                     : (q.start + first + lane / heads_warps) * H + 32 * (lane % heads_warps);
+        q_row = min(q_row, a.b.T * H - 1);               // (a box of none of the tile's tokens)
         Turn at;
         at.parity = 1u;
         int issued = 0;
@@ -486,7 +491,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         // What the lane sums and stores: column lane % kStep, and of the warp's tokens every other one, or half of the rows of one.
         const int col = lane & (kStep - 1), part = lane / kStep;
         const uint32_t put = mine + 4 * lane, get = mine + 128 * col + ((col & 7) << 4);
-        const int my_token = a.H <= 16 ? quarter * per_warp + part : quarter / heads_warps;     // (16 heads, or 32 and more)
+        const int my_token = kHeads != kMany ? quarter * per_warp + part : quarter / heads_warps;     // (16 heads, or 32 and more)
         const int my_end = my_token < n_tokens ? min(seen_s[my_token], c0 + cols) - (c0 + col) : 0;
         float* const my_scores = a.scores + (static_cast<int64_t>(q.start) + first + my_token) * a.b.max_pages + c0 + col;
         for (int r = 0; r < rounds && ok; ++r) {
@@ -523,15 +528,15 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     return (((v0.x + v0.y) + (v0.z + v0.w)) + ((v1.x + v1.y) + (v1.z + v1.w))) +
                            (((v2.x + v2.y) + (v2.z + v2.w)) + ((v3.x + v3.y) + (v3.z + v3.w)));
                 };
-                if (a.H == 16) {
+                if (kHeads == kSixteen) {
                     const float sum = sum16(16 * part);
                     if (at < my_end) my_scores[at] = has ? sum : -INFINITY;
-                } else if (a.H < 32) {
+                } else if (kHeads == kFew) {
                     for (int k = part; k < per_warp; k += 2) {
                         const int tok = quarter * per_warp + k;
                         if (tok >= n_tokens) break;
                         float sum = 0.0f;
-                        for (int h = k * a.H; h < (k + 1) * a.H; ++h) sum += get_shared((get ^ ((h >> 2) << 4)) + 4 * (h & 3));
+                        for (int h = k * H; h < (k + 1) * H; ++h) sum += get_shared((get ^ ((h >> 2) << 4)) + 4 * (h & 3));
                         const int c = c0 + at + col;
                         if (c < min(seen_s[tok], c0 + cols))
                             a.scores[(static_cast<int64_t>(q.start) + first + tok) * a.b.max_pages + c] = has ? sum : -INFINITY;
@@ -541,15 +546,23 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
                     float sum = sum16(16 * part);
                     sum += __shfl_xor_sync(0xffffffffu, sum, kStep);
                     if (heads_warps > 1) {
-                        if (part == 0) join[kStep * warp + col] = sum;
-                        bar_sync_or(2 + half, 128, false);
-                        if (quarter % heads_warps == 0)
-                            for (int w = 1; w < heads_warps; ++w) sum += join[kStep * (warp + w) + col];
-                        bar_sync_or(2 + half, 128, false);
+                        if (part == 0) join[kCols * quarter + kStep * j + col] = sum;
+                    } else if (part == 0 && at < my_end) {
+                        my_scores[at] = has ? sum : -INFINITY;
                     }
-                    if (quarter % heads_warps == 0 && part == 0 && at < my_end) my_scores[at] = has ? sum : -INFINITY;
                 }
                 __syncwarp();
+            }
+            if (kHeads == kMany && heads_warps > 1) {      // thread = column
+                bar_sync_or(1, 32 * kSoftWarps, false);
+                const int at = r * kCols + 32 * warp + lane;
+                const bool has = ((__shfl_sync(0xffffffffu, keyed, warp) >> lane) & 1u) != 0u;
+                for (int k = 0; k < 4 / heads_warps && k < n_tokens; ++k) {
+                    float sum = 0.0f;
+                    for (int w = k * heads_warps; w < (k + 1) * heads_warps; ++w) sum += join[kCols * w + 32 * warp + lane];
+                    if (c0 + at < min(seen_s[k], c0 + cols))
+                        a.scores[(static_cast<int64_t>(q.start) + first + k) * a.b.max_pages + c0 + at] = has ? sum : -INFINITY;
+                }
             }
             if (rounds > 1) {
                 tc_before();
@@ -614,9 +627,11 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
     if (q_bf16 == nullptr || scores == nullptr || (keys_bf16 == nullptr && num_keys > 0) || off(q_bf16, 16) ||
         off(keys_bf16, 16) || off(scores, 4))
         return MLA_EINVAL;
+    void (*const kernel)(const CUtensorMap, const ScoreArgs) =
+        H == 16 ? block_scores_kernel<kSixteen> : H < 32 ? block_scores_kernel<kFew> : block_scores_kernel<kMany>;
     b.err = mla_host::device_error_word();
     const int sms = mla_host::sm_count();
-    if (b.err == nullptr || sms <= 0 || !mla_host::max_dynamic_smem(reinterpret_cast<const void*>(block_scores_kernel), kSmem))
+    if (b.err == nullptr || sms <= 0 || !mla_host::max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmem))
         return MLA_ECUDA;
     ScoreArgs a = {b, static_cast<const __nv_bfloat16*>(keys_bf16), scores, H, d_qk, num_keys, 1, kCols, 1, sm_scale * kLog2e};
     a.tile_tokens = H <= 32 ? 4 * (32 / H) : H <= 64 ? 2 : 1;
@@ -645,6 +660,6 @@ extern "C" int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, cons
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, block_scores_kernel, q_map, a) == cudaSuccess && cudaGetLastError() == cudaSuccess ? MLA_OK
+    return cudaLaunchKernelEx(&cfg, kernel, q_map, a) == cudaSuccess && cudaGetLastError() == cudaSuccess ? MLA_OK
                                                                                                               : MLA_ECUDA;
 }
