@@ -67,6 +67,7 @@ struct ChunkArgs {
     // kListed
     const int32_t* lists;              // [T, width]
     int width;
+    bool paired;                       // kTree: the plan counts what two waves take by pairs
 };
 
 // A sequence's new tokens and context, as far as they are valid.
