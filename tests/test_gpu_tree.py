@@ -111,6 +111,19 @@ def test_attention_heads(H, many):
 
 
 @pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("n_seq", [1, 9, 31, 32, 33])
+def test_attention_split_tiles_of_unlike_lengths(n_seq, many):
+    """Contexts that are cut into pieces, of one to two waves and more; a sequence without tokens, one without positions."""
+    g = torch.Generator().manual_seed(n_seq)
+    seqs = [(int(torch.randint(1, 13, (1,), generator=g)), int(torch.randint(14, 2600, (1,), generator=g))) for _ in range(n_seq)]
+    if n_seq > 8:
+        seqs[3], seqs[7] = (0, 50), (2, 0)
+    T = sum(n for n, _ in seqs)
+    b = B.batch(seqs, 16, 512, 16, 528, seed=n_seq, extra=wide(T, 16, 16, many))
+    check(b, B.ancestors(b, some_parents(b, 4, n_seq)), 1)
+
+
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("page", [1, 31, 128])
 def test_attention_pages_that_end_inside_a_tile(page, many):
     b = B.batch([(35, 333), (32, 70), (12, 64)], 16, 512, page, 528, seed=page, extra=wide(79, 16, page, many))
