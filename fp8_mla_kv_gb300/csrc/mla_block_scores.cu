@@ -208,30 +208,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x == 0) check_lengths(a.b);
-    const int rank = a.cluster > 1 ? static_cast<int>(blockIdx.x) % a.cluster : 0;
-    const int2 u = find_unit<kThreads>(a.b.n_seq, static_cast<int>(blockIdx.x) / a.cluster, [&](int s) {
-        return (sequence_of(a.b, s).n + a.tile_tokens - 1) / a.tile_tokens;
-    });
-    if (u.x < 0) return;                                   // (all CTAs of a cluster have the same tile)
-    const Sequence q = sequence_of(a.b, u.x);
-    const int first = u.y * a.tile_tokens, n_tokens = min(a.tile_tokens, q.n - first);
-    const int last = position_of(a.b, q, first + n_tokens - 1);
-    const int blocks = last < 0 ? 0 : last / a.b.page_size;            // the tile's columns
-    if (blocks == 0) return;
-    // This CTA's: [c0, c0 + cols)
-    const int share = ((blocks + a.cluster - 1) / a.cluster + 15) & ~15;
-    const int per = max(a.least, share), c0 = static_cast<int>(min(static_cast<int64_t>(blocks), static_cast<int64_t>(rank) * per));
-    const int cols = min(per, blocks - c0);
-    if (cols == 0) return;                                 // (its peers know: they neither wait for it nor read its maxima)
-    const int peers = (blocks + per - 1) / per;            // CTAs of the cluster with columns
-    const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
-    const int n_dims = a.d_qk / 64;
-    // The rings hold two steps of 64 dims with two tiles of keys each, or three with one. With one round the copies are over when the
-    // scores are turned; with more, the last slot is kept free for that.
-    const int key_slots = cols > kTileKeys && rounds == 1 ? 4 : 3, q_slots = rounds == 1 ? kSlots - key_slots : 2;
-    const int q_off = kOffRing + key_slots * kTileBytes;
-
+    // (while the first loads are on their way; find_unit's barriers are these writes' too)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMostKeySlots; ++i) {
             mbar_init(&full[i], 32 * kLoadWarps);
@@ -253,9 +230,36 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_before();
-    __syncthreads();
+    if (blockIdx.x == 0) check_lengths(a.b);
+    const int rank = a.cluster > 1 ? static_cast<int>(blockIdx.x) % a.cluster : 0;
+    const int2 u = find_unit<kThreads>(a.b.n_seq, static_cast<int>(blockIdx.x) / a.cluster, [&](int s) {
+        return (sequence_of(a.b, s).n + a.tile_tokens - 1) / a.tile_tokens;
+    });
     tc_after();
     const uint32_t tmem = *tmem_slot;
+    auto give_back = [&]() {
+        if (warp == kMmaWarp)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kCols) : "memory");
+    };
+    if (u.x < 0) return give_back();                       // (all CTAs of a cluster have the same tile)
+    const Sequence q = sequence_of(a.b, u.x);
+    const int first = u.y * a.tile_tokens, n_tokens = min(a.tile_tokens, q.n - first);
+    const int last = position_of(a.b, q, first + n_tokens - 1);
+    const int blocks = last < 0 ? 0 : last / a.b.page_size;            // the tile's columns
+    if (blocks == 0) return give_back();
+    // This CTA's: [c0, c0 + cols)
+    const int share = ((blocks + a.cluster - 1) / a.cluster + 15) & ~15;
+    const int per = max(a.least, share), c0 = static_cast<int>(min(static_cast<int64_t>(blocks), static_cast<int64_t>(rank) * per));
+    const int cols = min(per, blocks - c0);
+    if (cols == 0) return give_back();                     // (its peers know: they neither wait for it nor read its maxima)
+    const int peers = (blocks + per - 1) / per;            // CTAs of the cluster with columns
+    const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
+    const int n_dims = a.d_qk / 64;
+    // The rings hold two steps of 64 dims with two tiles of keys each, or three with one. With one round the copies are over when the
+    // scores are turned; with more, the last slot is kept free for that.
+    const int key_slots = cols > kTileKeys && rounds == 1 ? 4 : 3, q_slots = rounds == 1 ? kSlots - key_slots : 2;
+    const int q_off = kOffRing + key_slots * kTileBytes;
+
     bool ok = *abort_flag == 0;
 
     // Row r of the tile: lane r % 32 of warp r / 32. Tokens of at most 32 heads stand side by side in a warp.
@@ -574,10 +578,8 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     tc_before();
     __syncthreads();
     if (*abort_flag != 0 && threadIdx.x == 0) atomicOr(a.b.err, MLA_ERR_PIPELINE_TIMEOUT);
-    if (warp == kMmaWarp) {
-        tc_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kCols) : "memory");
-    }
+    tc_after();
+    give_back();
     if (a.cluster > 1) cluster_sync();                     // (the others have read this CTA's maxima)
 }
 
