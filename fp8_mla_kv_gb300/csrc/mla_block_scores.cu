@@ -476,16 +476,26 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
         }
         // Maxima and sums of both halves, of all CTAs
         max_s[half * kRows + row] = make_float2(m, l);
-        if (a.cluster > 1) cluster_sync();
-        else bar_sync_or(1, 32 * kSoftWarps, false);
         float all_m = -INFINITY, all_l = 0.0f;
-        for (int k = 0; k < 2 * peers; ++k) {
-            const float2* at = &max_s[(k & 1) * kRows + row];
-            const float2 v = a.cluster > 1 ? peer_float2(smem_u32(at), k >> 1) : *at;
+        auto add = [&](float2 v) {
             const float now = fmaxf(all_m, v.x), to = now == -INFINITY ? 0.0f : now;
             all_l = all_l * ex2_approx(all_m - to) + v.y * ex2_approx(v.x - to);       // (0 x 0 where there is nothing)
             all_m = now;
+        };
+        float2* const all_s = reinterpret_cast<float2*>(turn);
+        if (a.cluster > 1) {
+            cluster_sync();
+            const uint32_t at = smem_u32(&max_s[half * kRows + row]);
+            for (int k = 0; k < peers; ++k) add(peer_float2(at, k));
+            all_s[half * kRows + row] = make_float2(all_m, all_l);             // (a half's, of all CTAs)
+            all_m = -INFINITY;
+            all_l = 0.0f;
         }
+        bar_sync_or(1, 32 * kSoftWarps, false);
+        const float2* const both = a.cluster > 1 ? all_s : max_s;
+        add(both[row]);
+        add(both[kRows + row]);
+        if (a.cluster > 1) bar_sync_or(1, 32 * kSoftWarps, false);             // (the scores are turned there)
         // p = exp2(x - off) x f; with one round exp2(x - a maximum so far) is in tensor memory
         const float off = all_m == -INFINITY ? 0.0f : all_m;
         const float f = lives ? 1.0f / (all_l == 0.0f ? 1.0f : all_l) : 0.0f;
