@@ -15,7 +15,7 @@
 // says, by 16 bytes a thread and time (cp.async): TMA's gather of four rows took 41,000 cycles for what boxes take 15,000.
 // Both in 128-byte-swizzled tiles of 128 rows through a ring each, for each 64 dims one of q and up to two of keys.
 //
-// 4,096 tokens of 16 heads with up to 255 blocks: 37.1 us; 32 tokens of 128 heads with up to 1,024: 16.3 us. In both a CTA
+// 4,096 tokens of 16 heads with up to 255 blocks: 37.1 us; 32 tokens of 128 heads with up to 1,024: 15.4 us. In both a CTA
 // takes 24,000 to 30,000 cycles, one after the other: 5,000 until the first operands are asked for, 10,000 to 16,000 of products
 // (the first: what an SM gets from L2, 96 KB a step of 64 dims for its two CTAs in 1,700 cycles; the second: memory, as each step asks
 // for 128 bytes of every row; one product of 256 columns a step instead of two of 128: 38.3 us), 9,000 to 11,000 of softmax, exchange and sums, and the first case has 512 tiles for 304 places.
@@ -57,7 +57,7 @@ constexpr int kOffBars = kOffOff + (kCols / kStep) * kRows * 4;
 constexpr int kNumBars = 2 * kMostKeySlots + 2 * kMostQSlots + 3;
 constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
 constexpr int kSmem = kOffMisc + 16;
-static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(2 * (kSmem + 2048) <= 228 * 1024, "two CTAs an SM, each with 1 KB of find_unit's and 1 KB of the system's");
 
 struct ScoreArgs {
     Batch b;
