@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(32 * kWarps)
 block_select_kernel(const Batch b, const float* __restrict__ scores, int columns, int sink, int local, int width,
                     int32_t* __restrict__ blocks) {
     constexpr int kThreads = 32 * kWarps, kChunk = kThreads * kPer;
-    __shared__ uint32_t counts[2][kWarps][3];
+    __shared__ uint32_t counts[2][kWarps][3];              // of a pass and the one before, which a slow warp may still read
+    __shared__ uint32_t bits[kWarps][2];                   // (apart from them: a warp reads it while others count)
     __shared__ int place[kPer][kWarps];                    // keys above the threshold, and (upper half) equal to it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x;
@@ -266,12 +267,12 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
     ones = __reduce_or_sync(0xffffffffu, ones);
     zeros = __reduce_or_sync(0xffffffffu, zeros);
     if (lane == 0) {
-        counts[1][warp][0] = ones;
-        counts[1][warp][1] = zeros;
+        bits[warp][0] = ones;
+        bits[warp][1] = zeros;
     }
     __syncthreads();
-    ones = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][0] : 0u);
-    zeros = __reduce_or_sync(0xffffffffu, lane < kWarps ? counts[1][lane][1] : 0u);
+    ones = __reduce_or_sync(0xffffffffu, lane < kWarps ? bits[lane][0] : 0u);
+    zeros = __reduce_or_sync(0xffffffffu, lane < kWarps ? bits[lane][1] : 0u);
     const uint32_t differ = ones & zeros;
     int turn = 0;
 #pragma unroll 1
