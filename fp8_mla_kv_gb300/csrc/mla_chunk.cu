@@ -57,7 +57,10 @@ constexpr int kSmemQmax = 3 * kWarps * kHeads * 4;   // |q| maxima, block score 
 constexpr int kSmemMisc = 2 * kStages * 8 + kStages * 4 + 16 + 16;   // barriers, present masks, poisoned rows, issued
 constexpr int kSmemTokens = kStages * kNB * 4;       // where a position has a mask of tokens
 constexpr int kSmemLists = kListMax * 8;             // where the CTA reads its token's list: slot and position of each block
-static_assert(kListMax * 4 + 16 <= kSmemStages, "the list's place");
+// The list as it comes lies where the partials do, which no bulk copy writes: a barrier alone would not order its ordinary
+// reads and writes before the copies that fill the stages.
+constexpr int kOffList = kSmemStages;
+static_assert(kOffList >= kSmemStages && kOffList + kListMax * 4 + 16 <= kSmemStages + kSmemRed, "the list's place");
 constexpr int kSmemTotal = kSmemStages + kSmemRed + kSmemP + kSmemQmax + kSmemMisc;
 constexpr float kLn2 = 0.6931471805599453f;
 // The exp2 offset puts the largest score at kTop (log2 units) and moves only when one is
@@ -605,7 +608,7 @@ mla_chunk_small_kernel(const ChunkArgs args) {
     Piece pc;
     if (kForm == kListed) {
         const int tile = blockIdx.x / args.nk, token = tile / args.group_tiles;
-        const int count = read_list(args, token, entries_s, reinterpret_cast<int*>(stages), own_pos);
+        const int count = read_list(args, token, entries_s, reinterpret_cast<int*>(smem + kOffList), own_pos);
         if (count < 0) return;                           // (all CTAs of the cluster)
         pc = block_piece(args, blockIdx.x, count);
     } else {
