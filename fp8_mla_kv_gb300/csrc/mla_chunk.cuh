@@ -213,7 +213,9 @@ __device__ __forceinline__ int64_t chunk_slot(const ChunkArgs& a, const int32_t*
     return slot;
 }
 
-// The same for any form, with the tokens of the tile that attend the position (`rows` query rows in the tile).
+// The same for any form, with the tokens of the tile that attend the position (`rows` query rows in the tile). One that none
+// attends (past all of them in their own block, a drafted token that no mask names) is absent: what its row holds, which may
+// be past the context, must not move the scale that the tile's values are held by.
 template <int kForm>
 __device__ __forceinline__ int64_t form_slot(const ChunkArgs& a, const Piece& p, const int32_t* bt, int pos, int rows,
                                              uint32_t& tokens) {
@@ -223,7 +225,7 @@ __device__ __forceinline__ int64_t form_slot(const ChunkArgs& a, const Piece& p,
         const int64_t slot = static_cast<int64_t>(v.x) + off;
         const int ahead = v.y + off;                 // token k of the group attends it from k = ahead on
         tokens = ahead <= 0 ? v.z : ahead > 31 ? 0u : static_cast<uint32_t>(v.z) & (0xffffffffu << ahead);
-        if (slot == 0) return -1;
+        if (slot == 0 || tokens == 0u) return -1;
         if (slot >= a.num_slots) {
             atomicOr(a.err, MLA_ERR_DECODE_INDEX_RANGE);
             return -1;
@@ -240,6 +242,7 @@ __device__ __forceinline__ int64_t form_slot(const ChunkArgs& a, const Piece& p,
 #pragma unroll 1
             for (int i = 0; i < n; ++i) tokens |= ((__ldg(m + static_cast<int64_t>(i) * a.mask_words) >> (j & 31)) & 1u) << i;
         }
+        if (tokens == 0u) return -1;
     }
     return chunk_slot(a, bt, pos);
 }
