@@ -1076,7 +1076,8 @@ mla_chunk_small_kernel(const ChunkArgs args) {
         float* const part = reinterpret_cast<float*>(stages);
         float* const part_lse = part + kHeads * kPartRow;
         if (lost) {
-            if (threadIdx.x < kHeads) part_lse[threadIdx.x] = INFINITY;      // no lse: the tile gets no outputs
+            // No lse: the tile gets no outputs. By the thread that has waited for the copies, which may land here.
+            for (int r = 0; threadIdx.x == 0 && r < kHeads; ++r) part_lse[r] = INFINITY;
         } else {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
