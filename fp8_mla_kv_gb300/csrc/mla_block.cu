@@ -246,7 +246,7 @@ block_select_kernel(const Batch b, const float* __restrict__ scores, int columns
         }
     };
     load(0);
-    const int chunks = kWide ? (n + kChunk - 1) / kChunk : 1;
+    const int chunks = kWide ? parts_of(n, kChunk) : 1;
     // The threshold's digits; `left`: how many keys that agree with it so far are still wanted. Where there are no more
     // keys than wanted, all are taken: the threshold is 0, and a key of 0 never is.
     uint32_t found = 0u;

@@ -233,7 +233,7 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     if (blockIdx.x == 0) check_lengths(a.b);
     const int rank = a.cluster > 1 ? static_cast<int>(blockIdx.x) % a.cluster : 0;
     const int2 u = find_unit<kThreads>(a.b.n_seq, static_cast<int>(blockIdx.x) / a.cluster, [&](int s) {
-        return (sequence_of(a.b, s).n + a.tile_tokens - 1) / a.tile_tokens;
+        return parts_of(sequence_of(a.b, s).n, a.tile_tokens);
     });
     tc_after();
     const uint32_t tmem = *tmem_slot;
@@ -248,11 +248,11 @@ block_scores_kernel(const __grid_constant__ CUtensorMap q_map, const ScoreArgs a
     const int blocks = last < 0 ? 0 : last / a.b.page_size;            // the tile's columns
     if (blocks == 0) return give_back();
     // This CTA's: [c0, c0 + cols)
-    const int share = ((blocks + a.cluster - 1) / a.cluster + 15) & ~15;
+    const int share = (parts_of(blocks, a.cluster) + 15) & ~15;
     const int per = max(a.least, share), c0 = static_cast<int>(min(static_cast<int64_t>(blocks), static_cast<int64_t>(rank) * per));
     const int cols = min(per, blocks - c0);
     if (cols == 0) return give_back();                     // (its peers know: they neither wait for it nor read its maxima)
-    const int peers = (blocks + per - 1) / per;            // CTAs of the cluster with columns
+    const int peers = parts_of(blocks, per);               // CTAs of the cluster with columns
     const int rounds = (cols + kCols - 1) / kCols, passes = rounds > 1 ? 2 : 1;
     const int n_dims = a.d_qk / 64;
     // The rings hold two steps of 64 dims with two tiles of keys each, or three with one. With one round the copies are over when the

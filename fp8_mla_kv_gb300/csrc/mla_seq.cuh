@@ -29,6 +29,9 @@ __device__ __forceinline__ Sequence sequence_of(const Batch& b, int s) {
     return q;
 }
 
+// How many parts of `per` make n, for any n: sums like n + per - 1 may pass 2^31.
+__host__ __device__ __forceinline__ int parts_of(int n, int per) { return n / per + (n % per != 0 ? 1 : 0); }
+
 // Positions that the table has room for (below 2^31: checked on the host).
 __device__ __forceinline__ int capacity(const Batch& b) { return b.max_pages * b.page_size; }
 

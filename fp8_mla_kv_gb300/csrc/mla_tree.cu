@@ -25,7 +25,7 @@ tree_mask_kernel(const Batch b, const int32_t* __restrict__ parent, uint32_t* __
     pdl_launch_dependents();
     if (blockIdx.x == 0) check_lengths(b);
     const int2 u = find_unit<kMaskThreads>(b.n_seq, blockIdx.x, [&](int s) {
-        return (sequence_of(b, s).n + kMaskThreads - 1) / kMaskThreads;
+        return parts_of(sequence_of(b, s).n, kMaskThreads);
     });
     if (u.x < 0) return;
     const Sequence q = sequence_of(b, u.x);

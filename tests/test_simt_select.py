@@ -65,3 +65,10 @@ def test_no_order_of_warps_changes_a_list_that_is_read_again(lib, order):
     b = B.batch([(1, blocks)], 1, 512, 1, 528, seed=3, extra=0)
     scores = torch.randn((1, blocks), generator=torch.Generator().manual_seed(4))
     assert select(lib, b, scores, 64, 1, 2, order) == lists(b, scores, 64, 1, 2)
+
+
+@pytest.mark.parametrize("per", [1, 8, 128, 8192, 268435520, 2 ** 31 - 4097])
+@pytest.mark.parametrize("n", [0, 1, 127, 128, 129, 8193, 2 ** 31 - 8192, 2 ** 31 - 4097])
+def test_parts_of_the_longest_tables(lib, n, per):
+    """Chunks of a token's blocks, CTAs of a tile's: tables may have up to 2^31 - 4097 blocks (of one position)."""
+    assert lib.simt_parts(n, per) == -(-n // per)
