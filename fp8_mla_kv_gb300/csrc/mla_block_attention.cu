@@ -8,10 +8,10 @@
 // block once that would be read four times token by token. Tokens of different sequences may share a group: their
 // blocks stand side by side then.
 //
-// 4,096 tokens of 16 heads with 32 blocks of 64 of up to 256 each: 787 us, 366 TFLOP/s of the listed pairs (a group of four has
-// 49 blocks, of which each token lists two thirds; of the pairs that are multiplied it is 564). What bounds it is what
+// 4,096 tokens of 16 heads with 32 blocks of 64 of up to 256 each: 800 us, 360 TFLOP/s of the listed pairs (a group of four has
+// 49 blocks, of which each token lists two thirds; of the pairs that are multiplied it is 555). What bounds it is what
 // bounds the kernel for many rows, and 20,000 + 8,000 of a tile's 229,000 cycles are its start and end. 64 single tokens:
-// 33.8 us, 2.4 TB/s, bound as the kernel for few rows (256 pieces of 16 blocks of 32 positions for 304 places).
+// 34.2 us, 2.3 TB/s, bound as the kernel for few rows (256 pieces of 16 blocks of 32 positions for 304 places).
 //
 // Where a tile is one token's of few rows, its CTAs, a cluster, read the list themselves (read_list) and join their parts
 // through their shared memory (join_parts). Otherwise a first launch makes the groups' lists (block_lists_kernel; with

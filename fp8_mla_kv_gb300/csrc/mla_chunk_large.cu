@@ -41,8 +41,8 @@
 // 53 %, the tensor pipe 31 %; and a block is a chain of about a dozen hand-offs between the roles,
 // 120 cycles each, which keeps these from overlapping further. 24 sequences of two tokens of 128 heads
 // and up to 16,384 positions: 240 us, of which starting and ending a piece take about 12 us each of three. With masks (trees,
-// blocks) 8 trees of 60 tokens of 128 heads over up to 16,384 positions take 1,465 us, 625 TFLOP/s; 16 trees of up to 31 tokens
-// of 16 heads, NoPE, 106 us and with plan and merge 112.
+// blocks) 8 trees of 60 tokens of 128 heads over up to 16,384 positions take 1,487 us, 615 TFLOP/s; 16 trees of up to 31 tokens
+// of 16 heads, NoPE, 102 us (both with plan and merge).
 #include <cfloat>
 #include <climits>
 #include <cmath>

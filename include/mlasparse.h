@@ -417,8 +417,9 @@ int mla_chunk_attention(const void* q_bf16, int T, int H, int d_qk, mla_kv_cache
  * MLA_ERR_CHUNK_RANGE, and which tokens count as being in a sequence is then unspecified. Tokens outside
  * every sequence keep what their outputs hold. Lengths are read on the device, so a captured call serves any. As calls in turn:
  *   mla_rope_kv_write, mla_block_keys, mla_block_scores, mla_block_select, mla_block_attention.
- * All are launched with programmatic stream serialization. max_pages * page_size is below 2^31 - 4096
- * (otherwise MLA_EUNSUPPORTED); q_start, kv_len and block_table as in mla_chunk_attention.
+ * All are launched with programmatic stream serialization; with an empty table mla_block_keys, mla_block_scores and
+ * mla_block_select write and flag nothing. max_pages * page_size is below 2^31 - 4096 (otherwise MLA_EUNSUPPORTED);
+ * q_start, kv_len and block_table as in mla_chunk_attention.
  *
  * mla_block_keys - the mean key of each page that the new tokens completed:
  *   keys[p] = (sum over the rows of page p of [latent (code x scale), rope]) / rows, fp32 sums, rounded to BF16 once.
@@ -455,7 +456,8 @@ int mla_block_scores(const void* q_bf16, int T, int H, int d_qk, const void* key
  * (its own among them), and of those between the ones with the highest scores, `width` in all. Of equal scores the
  * lower block is taken; a block between whose score is -inf or NaN is not. Row t of `blocks` receives them in
  * ascending order, then -1. A token at a negative position gets -1 throughout.
- *   scores   fp32 [T, columns], device: a column for each block of the table
+ *   scores   fp32 [T, columns], device: a column for each block of the table (without columns, as for an empty table,
+ *            nothing is launched and `blocks` keeps what it holds)
  *   sink >= 0, local >= 1, sink + local <= width (otherwise MLA_EINVAL)
  *   blocks   int32 [T, width], device
  * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED or MLA_ECUDA.
